@@ -447,6 +447,127 @@ KDA_API kda_status kda_prefill_noalloc(const void *q, const void *k, const void 
                                        int32_t H, int32_t dk, int32_t dv, void *o, float *S_final,
                                        int32_t *device_status, kda_stream_t stream);
 
+/*
+ * The gated delta rule: the recurrence with the scalar gate of "Understanding
+ * Kimi Delta Attention" (pyshine), section "The KDA Recurrence: Scalar Gate vs
+ * Channel-wise Gate", one decay per token and head instead of one per channel:
+ *
+ *   S_t = a_t (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T,  a_t = exp(log_decay_t)
+ *   o_t = S_t^T q_t
+ *
+ * The kda_gdn_ entry points follow the conventions at the top of this file
+ * (dense tensors, q and k normalised by the caller, beta as given, dk = dv =
+ * 128) and add heads in groups: Hk heads of q and k, Hv of v, Hv a multiple of
+ * Hk; value head h uses q/k head h / (Hv / Hk).  log_decay has no lower limit
+ * (-inf, a decay of 0, included): decays enter as exp of differences that are
+ * at most the largest decay.  States, decays and the sums over tokens are
+ * fp32-accurate: S_final agrees with the token-by-token recurrence to about
+ * 1e-5 relative, not only to the rounding of bf16 operands.
+ */
+
+/*
+ * Workspace of kda_gdn_prefill (device bytes, 256-byte aligned start).
+ * Returns 0 for invalid arguments.
+ */
+KDA_API size_t kda_gdn_prefill_workspace_bytes(kda_dtype qkv_dtype, int32_t num_seqs, int64_t total_tokens,
+                                               int32_t Hk, int32_t Hv, int32_t dk, int32_t dv);
+
+/*
+ * kda_gdn_prefill -- the gated delta rule over packed variable-length sequences.
+ *
+ *   q, k       [total_tokens, Hk, dk]  qkv_dtype
+ *   v          [total_tokens, Hv, dv]  qkv_dtype
+ *   log_decay  [total_tokens, Hv]      fp32
+ *   beta       [total_tokens, Hv]      fp32
+ *   S0         [num_seqs, Hv, dk, dv]  fp32, or NULL for zero start states
+ *   cu_seqlens [num_seqs + 1]          int32, device; 0 = c_0 <= ... <= c_N = total_tokens
+ *   o          [total_tokens, Hv, dv]  qkv_dtype (out)
+ *   S_final    [num_seqs, Hv, dk, dv]  fp32 (out), or NULL
+ *   workspace  >= kda_gdn_prefill_workspace_bytes(...), else KDA_ERR_WORKSPACE
+ *
+ * Sequences, start and final states, aliasing (S_final may be S0 exactly, no
+ * other overlap) and errors are those of kda_prefill.  A malformed cu_seqlens
+ * sets KDA_DEV_BAD_CU_SEQLENS; sequences with invalid bounds are not written,
+ * and others may not be.  Results are bitwise repeatable.
+ */
+KDA_API kda_status kda_gdn_prefill(const void *q, const void *k, const void *v, kda_dtype qkv_dtype,
+                                   const float *log_decay, const float *beta, const float *S0,
+                                   const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens, int32_t Hk,
+                                   int32_t Hv, int32_t dk, int32_t dv, void *o, float *S_final, void *workspace,
+                                   size_t workspace_bytes, int32_t *device_status, kda_stream_t stream);
+
+/*
+ * kda_gdn_decode_step -- one token of the gated delta rule for N sequences;
+ * each head's state is read once and written once, in place.
+ *
+ *   q, k       [N, Hk, dk]  qkv_dtype        v [N, Hv, dv] qkv_dtype
+ *   log_decay  [N, Hv] fp32                  beta [N, Hv] fp32
+ *   S          [num_slots, Hv, dk, dv] fp32, updated in place
+ *   state_indices, device_status             as kda_decode_step
+ *   o          [N, Hv, dv]  qkv_dtype (out)
+ */
+KDA_API kda_status kda_gdn_decode_step(const void *q, const void *k, const void *v, kda_dtype qkv_dtype,
+                                       const float *log_decay, const float *beta, float *S, int32_t num_slots,
+                                       const int32_t *state_indices, int32_t N, int32_t Hk, int32_t Hv, int32_t dk,
+                                       int32_t dv, void *o, int32_t *device_status, kda_stream_t stream);
+
+/*
+ * kda_rms_norm -- the norm in front of a layer's projections ("Inside one KDA
+ * block" of "Understanding Kimi Delta Attention" (pyshine) begins with it),
+ * with the residual stream's addition and an optional output in 8 bits:
+ *
+ *   h = round(x + residual)  (h = x when residual is NULL)
+ *   y = h / sqrt(mean_c h_c^2 + eps) * weight
+ *
+ *   x, residual, residual_out  [rows, dim] dtype; residual_out (out, or NULL)
+ *              receives h; it may be x or residual exactly
+ *   weight     [dim] fp32 (NULL = all ones)
+ *   y          [rows, dim] (out): KDA_NORM_OUT_SAME in dtype (may be x
+ *              exactly); KDA_NORM_OUT_E4M3 or KDA_NORM_OUT_INT8 one byte each
+ *   group      8-bit outputs: 0 = one scale for a row, 128 = one for every 128
+ *              columns (dim a multiple of 128)
+ *   scales     [rows, group ? dim / group : 1] fp32 (out), 8-bit outputs only:
+ *              max(max |y| / qmax, 2^-126), qmax = 448 (e4m3) or 127 (int8).
+ *              The code is y / scale rounded to nearest even; it stands for
+ *              code * scale.  Values that are not finite make the scale they
+ *              share NaN.
+ *
+ * x, residual, residual_out, y 16-byte aligned, weight and scales 4-byte; dim
+ * from 1 to KDA_NORM_MAX_DIM.  Outputs overlap nothing but as said above
+ * (KDA_ERR_INVALID_ARG).  Asynchronous on `stream`, no workspace; results are
+ * bitwise repeatable.
+ */
+#define KDA_NORM_MAX_DIM (1 << 20)
+typedef enum {
+    KDA_NORM_OUT_SAME = 0,
+    KDA_NORM_OUT_E4M3 = 1,
+    KDA_NORM_OUT_INT8 = 2
+} kda_norm_out;
+KDA_API kda_status kda_rms_norm(const void *x, const void *residual, kda_dtype dtype, const float *weight, float eps,
+                                int64_t rows, int32_t dim, kda_norm_out out_type, int32_t group, void *y,
+                                float *scales, void *residual_out, kda_stream_t stream);
+
+/*
+ * kda_rms_norm_backward -- gradient of kda_rms_norm's y (KDA_NORM_OUT_SAME)
+ * and h for L = <y, grad_y> + <h, grad_h>, with r = (mean_c h_c^2 + eps)^(-1/2):
+ *     grad_x_c = r w_c dy_c - (r^3 h_c / dim) sum_j h_j w_j dy_j + grad_h_c
+ * (the gradient of x and of residual alike) and grad_weight_c = sum over rows
+ * of dy_c h_c r.
+ *
+ *   grad_y, h, grad_h  [rows, dim] dtype; h as the forward stored it; grad_h
+ *                      may be NULL (zeros)
+ *   grad_x             [rows, dim] dtype (out; may be grad_y or grad_h exactly)
+ *   grad_weight        [dim] fp32 (out), or NULL (not computed); rows are added
+ *                      in a fixed order (bitwise repeatable)
+ *   workspace          >= kda_rms_norm_backward_workspace_bytes(rows, dim) when
+ *                      grad_weight is given, 256-byte aligned, else it may be NULL
+ */
+KDA_API size_t kda_rms_norm_backward_workspace_bytes(int64_t rows, int32_t dim);
+KDA_API kda_status kda_rms_norm_backward(const void *grad_y, const void *h, const void *grad_h, kda_dtype dtype,
+                                         const float *weight, float eps, int64_t rows, int32_t dim, void *grad_x,
+                                         float *grad_weight, void *workspace, size_t workspace_bytes,
+                                         kda_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

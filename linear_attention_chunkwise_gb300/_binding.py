@@ -31,6 +31,9 @@ KDA_DEV_BOUNDS = 0x10  # only from a library built with KDA_DEBUG_BOUNDS
 KDA_FUSE_L2NORM_QK = 0x1
 KDA_FUSE_BETA_SIGMOID = 0x2
 KDA_FUSE_OUT_GATE = 0x4
+KDA_NORM_OUT_SAME = 0
+KDA_NORM_OUT_E4M3 = 1
+KDA_NORM_OUT_INT8 = 2
 
 
 class _KdaFusion(ctypes.Structure):
@@ -64,7 +67,9 @@ EXPORTED_SYMBOLS = ("kda_abi_version", "kda_status_string", "kda_prefill_workspa
                     "kda_prefill_noalloc", "kda_prefill_snapshots", "kda_prefill_ex", "kda_decode_step_ex",
                     "kda_decode_multi_ex", "kda_prefill_backward_workspace_bytes", "kda_prefill_backward",
                     "kda_prefill_backward_ex_workspace_bytes", "kda_prefill_backward_ex",
-                    "kda_prefill_backward_gated_workspace_bytes", "kda_prefill_backward_gated")
+                    "kda_prefill_backward_gated_workspace_bytes", "kda_prefill_backward_gated",
+                    "kda_gdn_prefill_workspace_bytes", "kda_gdn_prefill", "kda_gdn_decode_step", "kda_rms_norm",
+                    "kda_rms_norm_backward_workspace_bytes", "kda_rms_norm_backward")
 
 _lock = threading.Lock()
 _lib = None
@@ -132,6 +137,15 @@ def load_library(path: str | None = None):
         lib.kda_decode_step.restype = ctypes.c_int
         lib.kda_decode_multi.argtypes = [P, P, P, ctypes.c_int, P, P, P, i32, P, i32, i32, i32, i32, i32, P, P, P, P]
         lib.kda_decode_multi.restype = ctypes.c_int
+        E, F = ctypes.c_int, ctypes.c_float
+        for name, res, args in (
+                ("kda_gdn_prefill_workspace_bytes", sz, [E, i32, i64, i32, i32, i32, i32]),
+                ("kda_gdn_prefill", E, [P, P, P, E, P, P, P, P, i32, i64, i32, i32, i32, i32, P, P, P, sz, P, P]),
+                ("kda_gdn_decode_step", E, [P, P, P, E, P, P, P, i32, P, i32, i32, i32, i32, i32, P, P, P]),
+                ("kda_rms_norm", E, [P, P, E, P, F, i64, i32, E, i32, P, P, P, P]),
+                ("kda_rms_norm_backward_workspace_bytes", sz, [i64, i32]),
+                ("kda_rms_norm_backward", E, [P, P, P, E, P, F, i64, i32, P, P, P, sz, P])):
+            getattr(lib, name).restype, getattr(lib, name).argtypes = res, args
         if path is None:
             _lib = lib
         return lib

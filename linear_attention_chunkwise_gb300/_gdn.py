@@ -1,0 +1,252 @@
+"""Entry points of the gated delta rule and of the RMS norm (include/kda.h).  Argument marshalling only.
+
+As in ``_binding``: tensors are checked, outputs allocated when the caller passes none, and raw pointers
+handed to libkda.so, on the current stream of the tensors' own device or on ``stream``.
+"""
+from __future__ import annotations
+
+import contextlib
+
+import torch
+
+from . import _binding as _b
+
+_NORM_OUT = {None: (_b.KDA_NORM_OUT_SAME, None), "e4m3": (_b.KDA_NORM_OUT_E4M3, torch.float8_e4m3fn),
+             "int8": (_b.KDA_NORM_OUT_INT8, torch.int8)}
+_same_device = contextlib.nullcontext()
+
+
+def _check(t, name, dtype, shape, dev):
+    """t: a contiguous CUDA tensor of this type, shape and device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _first(t, name, dims):
+    """(device, dtype code) that the call goes by; t has `dims` dimensions."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
+    return t.device, _b._dtype_code(t.dtype)
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _on(dev):
+    """The call's device made current: launches go to it whatever device the caller has current."""
+    return _same_device if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _stream(stream, dev, *mine):
+    """The stream's handle; tensors that this call allocated are kept alive on a stream of the caller's."""
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, expected {dev}")
+    for t in mine:
+        if t is not None:
+            t.record_stream(stream)
+    return stream.cuda_stream
+
+
+def _done(name, st):
+    if st != _b.KDA_OK:
+        raise _b.KdaError(name, st, _b.kda_status_string(st))
+
+
+def _heads(q, v, name):
+    """Hk, Hv, dk, dv of q [.., Hk, dk] and v [.., Hv, dv]."""
+    if not isinstance(v, torch.Tensor) or v.dim() != q.dim():
+        raise ValueError(f"v must be {name}")
+    return q.shape[-2], v.shape[-2], q.shape[-1], v.shape[-1]
+
+
+def kda_gdn_prefill_workspace_bytes(qkv_dtype, num_seqs: int, total_tokens: int, Hk: int, Hv: int, dk: int = 128,
+                                    dv: int = 128) -> int:
+    code = qkv_dtype if isinstance(qkv_dtype, int) else _b._dtype_code(qkv_dtype)
+    return int(_b.load_library().kda_gdn_prefill_workspace_bytes(code, int(num_seqs), int(total_tokens), int(Hk),
+                                                                 int(Hv), int(dk), int(dv)))
+
+
+def kda_gdn_prefill(q, k, v, log_decay, beta, cu_seqlens, S0=None, *, o=None, S_final=None, return_final=True,
+                    workspace=None, device_status=None, stream=None):
+    """Prefill of the gated delta rule over packed sequences (see include/kda.h).
+
+    q, k: [T, Hk, 128]; v: [T, Hv, 128] (bf16 or fp32), Hv a multiple of Hk; log_decay, beta: [T, Hv] fp32;
+    cu_seqlens: int32 [N+1] on the device; S0: fp32 [N, Hv, 128, 128] or None.  Returns (o, S_final) --
+    S_final is None when return_final is False and none was given.
+    """
+    lib = _b.load_library()
+    dev, code = _first(q, "q", 3)
+    T = q.shape[0]
+    Hk, Hv, dk, dv = _heads(q, v, "[T, Hv, 128]")
+    _check(q, "q", q.dtype, (T, Hk, dk), dev)
+    _check(k, "k", q.dtype, (T, Hk, dk), dev)
+    _check(v, "v", q.dtype, (T, Hv, dv), dev)
+    _check(log_decay, "log_decay", torch.float32, (T, Hv), dev)
+    _check(beta, "beta", torch.float32, (T, Hv), dev)
+    N = cu_seqlens.numel() - 1
+    if N < 0:
+        raise ValueError("cu_seqlens must have at least one entry")
+    _check(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev)
+    if S0 is not None:
+        _check(S0, "S0", torch.float32, (N, Hv, dk, dv), dev)
+    mine = []
+    if o is None:
+        mine.append(o := torch.empty((T, Hv, dv), dtype=q.dtype, device=dev))
+    else:
+        _check(o, "o", q.dtype, (T, Hv, dv), dev)
+    if S_final is not None:
+        _check(S_final, "S_final", torch.float32, (N, Hv, dk, dv), dev)
+    elif return_final:
+        mine.append(S_final := torch.empty((N, Hv, dk, dv), dtype=torch.float32, device=dev))
+    if workspace is None:
+        need = lib.kda_gdn_prefill_workspace_bytes(code, N, T, Hk, Hv, dk, dv)
+        mine.append(workspace := torch.empty(max(need, 256), dtype=torch.uint8, device=dev))
+    else:
+        _b._check(workspace, "workspace", torch.uint8, dev)
+    _b._check(device_status, "device_status", torch.int32, dev)
+    with _on(dev):
+        _done("kda_gdn_prefill", lib.kda_gdn_prefill(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), code, log_decay.data_ptr(), beta.data_ptr(), _p(S0),
+            cu_seqlens.data_ptr(), N, T, Hk, Hv, dk, dv, o.data_ptr(), _p(S_final), workspace.data_ptr(),
+            workspace.numel(), _p(device_status), _stream(stream, dev, *mine)))
+    return o, S_final
+
+
+def kda_gdn_decode_step(q, k, v, log_decay, beta, S, state_indices=None, *, o=None, device_status=None,
+                        stream=None):
+    """One token of the gated delta rule; S [slots, Hv, 128, 128] fp32 is updated in place.
+
+    q, k: [N, Hk, 128]; v: [N, Hv, 128] (bf16 or fp32); log_decay, beta: [N, Hv] fp32; state_indices:
+    int32 [N] or None (slot n for sequence n).  Returns o [N, Hv, 128].
+    """
+    lib = _b.load_library()
+    dev, code = _first(q, "q", 3)
+    N = q.shape[0]
+    Hk, Hv, dk, dv = _heads(q, v, "[N, Hv, 128]")
+    _check(q, "q", q.dtype, (N, Hk, dk), dev)
+    _check(k, "k", q.dtype, (N, Hk, dk), dev)
+    _check(v, "v", q.dtype, (N, Hv, dv), dev)
+    _check(log_decay, "log_decay", torch.float32, (N, Hv), dev)
+    _check(beta, "beta", torch.float32, (N, Hv), dev)
+    slots = S.shape[0]
+    _check(S, "S", torch.float32, (slots, Hv, dk, dv), dev)
+    if state_indices is not None:
+        _check(state_indices, "state_indices", torch.int32, (N,), dev)
+    mine = []
+    if o is None:
+        mine.append(o := torch.empty((N, Hv, dv), dtype=q.dtype, device=dev))
+    else:
+        _check(o, "o", q.dtype, (N, Hv, dv), dev)
+    _b._check(device_status, "device_status", torch.int32, dev)
+    with _on(dev):
+        _done("kda_gdn_decode_step", lib.kda_gdn_decode_step(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), code, log_decay.data_ptr(), beta.data_ptr(), S.data_ptr(),
+            slots, _p(state_indices), N, Hk, Hv, dk, dv, o.data_ptr(), _p(device_status),
+            _stream(stream, dev, *mine)))
+    return o
+
+
+def kda_rms_norm(x, weight=None, residual=None, *, eps=1e-6, quant=None, group=0, y=None, scales=None,
+                 residual_out=None, stream=None):
+    """h = x + residual, y = h / sqrt(mean h^2 + eps) * weight over the last dimension (see include/kda.h).
+
+    x, residual: [rows, dim] (bf16 or fp32); weight: fp32 [dim] or None (ones).  quant: None (y in the
+    type of x), "e4m3" or "int8", with one fp32 scale for each row (group=0) or for every 128 columns
+    (group=128).  Returns (y, scales, residual_out): scales [rows, scales in a row] is None without quant,
+    residual_out (h in the type of x) None without a residual.
+    """
+    lib = _b.load_library()
+    dev, code = _first(x, "x", 2)
+    rows, dim = x.shape
+    _check(x, "x", x.dtype, (rows, dim), dev)
+    if weight is not None:
+        _check(weight, "weight", torch.float32, (dim,), dev)
+    if quant not in _NORM_OUT:
+        raise ValueError(f"quant must be None, 'e4m3' or 'int8', got {quant!r}")
+    out_type, out_dtype = _NORM_OUT[quant]
+    if group not in ((0, 128) if quant else (0,)) or (group and dim % group):
+        raise ValueError(f"group must be 0, or 128 with an 8-bit output and dim a multiple of it, got {group}")
+    mine = []
+    if residual is not None:
+        _check(residual, "residual", x.dtype, (rows, dim), dev)
+        if residual_out is None:
+            mine.append(residual_out := torch.empty_like(x))
+    if residual_out is not None:
+        _check(residual_out, "residual_out", x.dtype, (rows, dim), dev)
+    if y is None:
+        mine.append(y := torch.empty((rows, dim), dtype=out_dtype or x.dtype, device=dev))
+    else:
+        _check(y, "y", out_dtype or x.dtype, (rows, dim), dev)
+    if quant:
+        shape = (rows, dim // group if group else 1)
+        if scales is None:
+            mine.append(scales := torch.empty(shape, dtype=torch.float32, device=dev))
+        else:
+            _check(scales, "scales", torch.float32, shape, dev)
+    elif scales is not None:
+        raise ValueError("scales are written with an 8-bit output only")
+    with _on(dev):
+        _done("kda_rms_norm", lib.kda_rms_norm(
+            x.data_ptr(), _p(residual), code, _p(weight), eps, rows, dim, out_type, group, y.data_ptr(), _p(scales),
+            _p(residual_out), _stream(stream, dev, *mine)))
+    return y, scales, residual_out
+
+
+def kda_rms_norm_backward_workspace_bytes(rows: int, dim: int) -> int:
+    return int(_b.load_library().kda_rms_norm_backward_workspace_bytes(int(rows), int(dim)))
+
+
+def kda_rms_norm_backward(grad_y, h, weight=None, *, grad_h=None, eps=1e-6, need_grad_weight=True, grad_x=None,
+                          grad_weight=None, workspace=None, stream=None):
+    """Gradient of kda_rms_norm for L = <y, grad_y> + <h, grad_h> (see include/kda.h).
+
+    grad_y, h, grad_h: [rows, dim] of one type (bf16 or fp32), h the normed row (residual_out, or x);
+    weight: fp32 [dim] or None (ones).  Returns (grad_x, grad_weight): grad_x, in that type, is the
+    gradient of x and of residual alike; grad_weight fp32 [dim], or None when not asked for.
+    """
+    lib = _b.load_library()
+    dev, code = _first(h, "h", 2)
+    rows, dim = h.shape
+    _check(h, "h", h.dtype, (rows, dim), dev)
+    _check(grad_y, "grad_y", h.dtype, (rows, dim), dev)
+    if grad_h is not None:
+        _check(grad_h, "grad_h", h.dtype, (rows, dim), dev)
+    if weight is not None:
+        _check(weight, "weight", torch.float32, (dim,), dev)
+    mine = []
+    if grad_x is None:
+        mine.append(grad_x := torch.empty_like(h))
+    else:
+        _check(grad_x, "grad_x", h.dtype, (rows, dim), dev)
+    if grad_weight is not None:
+        _check(grad_weight, "grad_weight", torch.float32, (dim,), dev)
+    elif need_grad_weight:
+        mine.append(grad_weight := torch.empty((dim,), dtype=torch.float32, device=dev))
+    if workspace is not None:
+        _b._check(workspace, "workspace", torch.uint8, dev)
+    elif grad_weight is not None:
+        need = lib.kda_rms_norm_backward_workspace_bytes(rows, dim)
+        mine.append(workspace := torch.empty(max(need, 256), dtype=torch.uint8, device=dev))
+    with _on(dev):
+        _done("kda_rms_norm_backward", lib.kda_rms_norm_backward(
+            grad_y.data_ptr(), h.data_ptr(), _p(grad_h), code, _p(weight), eps, rows, dim, grad_x.data_ptr(),
+            _p(grad_weight), _p(workspace), 0 if workspace is None else workspace.numel(),
+            _stream(stream, dev, *mine)))
+    return grad_x, grad_weight

@@ -8,27 +8,22 @@
 #include <cstdint>
 #include <mutex>
 
+#include "kda_args.h"
 #include "kda_internal.h"
 
 namespace {
 
+using kda::aligned;
+using kda::esize_of;
+using kda::kAlign;
 using kda::kHeadDim;
+using kda::overlap;
+using kda::Range;
+using kda::range_of;
+using kda::round_up;
+using kda::sizes_ok;
 
-constexpr size_t kAlign = 256;
 constexpr int kMaxDevices = 64;
-
-size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-struct Range {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-Range range_of(const void* p, size_t bytes) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return Range{a, a + bytes};
-}
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.hi > a.lo && b.hi > b.lo; }
 
 // Device must be sm_103 (the kernels are built for sm_103a only).
 kda_status check_device() {
@@ -63,6 +58,14 @@ int sm_count() {
     }
     return count[dev];
 }
+
+}  // namespace
+
+namespace kda {
+int device_sm_count() { return sm_count(); }
+}  // namespace kda
+
+namespace {
 
 // Piecewise schedule of the two-pass prefill.  When the scan takes at most half
 // of the GPU's SMs (few sequences), the scan runs in pieces of 48 or more
@@ -113,8 +116,6 @@ bool make_map(CUtensorMap* m, CUtensorMapDataType dt, size_t esize, const void* 
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-size_t esize_of(kda_dtype t) { return t == KDA_DTYPE_F32 ? 4 : 2; }
-
 // Workspace layouts.  Two-pass path: [schedule][chunk table][bf16 q,k,v if
 // fp32 inputs][per-(chunk, head) operand images].  Single-pass path:
 // [schedule][bf16 q,k,v if fp32 inputs].
@@ -144,12 +145,6 @@ WsLayout fused_layout(kda_dtype t, int32_t N, int64_t T, int32_t H) {
     return w;
 }
 bool ws_args_ok(kda_dtype t, int32_t N, int64_t T, int32_t H, int32_t dk, int32_t dv);
-
-bool sizes_ok(int64_t a, int64_t b, int64_t c, int64_t d) {  // product fits comfortably in int64
-    const double prod = static_cast<double>(a) * static_cast<double>(b) * static_cast<double>(c) *
-                        static_cast<double>(d);
-    return prod < 4.0e18;
-}
 
 bool ws_args_ok(kda_dtype t, int32_t N, int64_t T, int32_t H, int32_t dk, int32_t dv) {
     if (N < 0 || T < 0 || H <= 0 || dk != kHeadDim || dv != kHeadDim) return false;

@@ -1,0 +1,35 @@
+// kda_args.h -- argument checks shared by the C-ABI front ends.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include "kda_internal.h"
+
+namespace kda {
+
+constexpr size_t kAlign = 256;  // workspaces and the regions inside them
+
+inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+struct Range {
+    uintptr_t lo, hi;  // [lo, hi)
+};
+inline Range range_of(const void* p, size_t bytes) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    return Range{a, a + bytes};
+}
+inline bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.hi > a.lo && b.hi > b.lo; }
+
+// Whether the product fits comfortably in int64.
+inline bool sizes_ok(int64_t a, int64_t b, int64_t c, int64_t d) {
+    const double prod = static_cast<double>(a) * static_cast<double>(b) * static_cast<double>(c) *
+                        static_cast<double>(d);
+    return prod < 4.0e18;
+}
+
+inline size_t esize_of(kda_dtype t) { return t == KDA_DTYPE_F32 ? 4 : 2; }
+
+}  // namespace kda

@@ -1,0 +1,265 @@
+// kda_gdn_recurrent.cu -- the gated delta rule token by token, in fp32: the decode
+// step, and the prefill of short sequences and of fp32 inputs.
+//
+// The gated delta rule is the recurrence of "Understanding Kimi Delta Attention"
+// (pyshine), "The KDA Recurrence: Scalar Gate vs Channel-wise Gate", with its
+// scalar gate: one decay a_t = exp(log_decay_t) per (token, value head),
+//   S_t = a_t (I - b_t k_t k_t^T) S_{t-1} + b_t k_t v_t^T,   o_t = S_t^T q_t,
+// evaluated in one pass over the state:
+//   y = a S^T k,  p = a S^T q,  u = b (v - y),  S <- a S + k u^T,  o = p + (k . q) u.
+// Value head h reads q/k head h / (Hv / Hk).
+#include <cuda_bf16.h>
+
+#include "kda_internal.h"
+#include "kda_ptx.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int D = kHeadDim;
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void st_f32(float* p, float x) { *p = x; }
+__device__ __forceinline__ void st_f32(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
+    const uint2 r = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16),
+                       __uint_as_float(r.y & 0xffff0000u));
+}
+
+// ================================================================ decode ==
+// One CTA per (sequence, value head); the 64 KB state passes once through the registers of 256
+// threads: thread (warp w, lane l) holds rows 16w..16w+15 of columns 4l..4l+3, so that a warp reads
+// and writes whole 512-byte rows.  Bound by HBM.
+constexpr int kDecThreads = 256;
+constexpr int kDecRows = D / (kDecThreads / 32);  // rows of a warp
+
+template <typename IoT>
+__global__ void __launch_bounds__(kDecThreads, 2)
+    kda_gdn_decode_kernel(const IoT* __restrict__ q, const IoT* __restrict__ k, const IoT* __restrict__ v,
+                          const float* __restrict__ log_decay, const float* __restrict__ beta, float* S,
+                          int32_t num_slots, const int32_t* __restrict__ state_indices, int32_t Hk, int32_t Hv,
+                          IoT* __restrict__ o, int32_t* device_status) {
+    const int n = blockIdx.x / Hv, h = blockIdx.x - n * Hv;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int32_t slot = state_indices ? state_indices[n] : n;
+    if (slot < 0 || slot >= num_slots) {
+        if (tid == 0 && device_status) atomicOr(device_status, KDA_DEV_BAD_SLOT);
+        return;
+    }
+    __shared__ __align__(16) float k_s[D], q_s[D], u_s[D];
+    __shared__ __align__(16) float red_y[kDecThreads / 32][D], red_p[kDecThreads / 32][D];
+    __shared__ float kq_s;
+
+    float* const Sg = S + (static_cast<size_t>(slot) * Hv + h) * D * D + static_cast<size_t>(warp) * kDecRows * D;
+    float4 s[kDecRows];  // the whole state in flight before anything is waited for
+#pragma unroll
+    for (int i = 0; i < kDecRows; ++i) s[i] = __ldcs(reinterpret_cast<const float4*>(Sg + i * D) + lane);
+
+    const size_t tok = static_cast<size_t>(n) * Hv + h;
+    const size_t qk = (static_cast<size_t>(n) * Hk + h / (Hv / Hk)) * D;
+    float vv = 0.f, b = 0.f;
+    if (tid < D) {
+        k_s[tid] = to_f32(k[qk + tid]);
+        q_s[tid] = to_f32(q[qk + tid]);
+        vv = to_f32(v[tok * D + tid]);
+        b = beta[tok];
+    }
+    const float a = expf(log_decay[tok]);
+    __syncthreads();
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f), p = y;
+#pragma unroll
+    for (int i = 0; i < kDecRows; ++i) {
+        const float kr = k_s[warp * kDecRows + i], qr = q_s[warp * kDecRows + i];
+        s[i].x *= a; s[i].y *= a; s[i].z *= a; s[i].w *= a;
+        y.x = fmaf(kr, s[i].x, y.x); y.y = fmaf(kr, s[i].y, y.y);
+        y.z = fmaf(kr, s[i].z, y.z); y.w = fmaf(kr, s[i].w, y.w);
+        p.x = fmaf(qr, s[i].x, p.x); p.y = fmaf(qr, s[i].y, p.y);
+        p.z = fmaf(qr, s[i].z, p.z); p.w = fmaf(qr, s[i].w, p.w);
+    }
+    reinterpret_cast<float4*>(red_y[warp])[lane] = y;
+    reinterpret_cast<float4*>(red_p[warp])[lane] = p;
+    if (warp == 0) {
+        const float4 kk = reinterpret_cast<const float4*>(k_s)[lane], qq = reinterpret_cast<const float4*>(q_s)[lane];
+        float d = fmaf(kk.x, qq.x, fmaf(kk.y, qq.y, fmaf(kk.z, qq.z, kk.w * qq.w)));
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+        if (lane == 0) kq_s = d;
+    }
+    __syncthreads();
+    if (tid < D) {
+        float yy = 0.f, pp = 0.f;
+#pragma unroll
+        for (int w = 0; w < kDecThreads / 32; ++w) {
+            yy += red_y[w][tid];
+            pp += red_p[w][tid];
+        }
+        const float u = b * (vv - yy);
+        u_s[tid] = u;
+        st_f32(o + tok * D + tid, fmaf(kq_s, u, pp));
+    }
+    __syncthreads();
+    const float4 uu = reinterpret_cast<const float4*>(u_s)[lane];
+#pragma unroll
+    for (int i = 0; i < kDecRows; ++i) {
+        const float kr = k_s[warp * kDecRows + i];
+        float4 t = s[i];
+        t.x = fmaf(kr, uu.x, t.x); t.y = fmaf(kr, uu.y, t.y);
+        t.z = fmaf(kr, uu.z, t.z); t.w = fmaf(kr, uu.w, t.w);
+        __stcs(reinterpret_cast<float4*>(Sg + i * D) + lane, t);
+    }
+}
+
+// =============================================================== prefill ==
+// The state's columns never mix, so a CTA takes 16 of them for one (sequence, value head): 8 lanes
+// hold a column, 16 rows each (rows 4 (8 i + part) .. + 3, i = 0..3, so that the 8 lanes of a column
+// read 128 consecutive bytes of a k or q row, and the warp's other columns the same ones).  A token
+// is a chain of about 80 multiply-adds, three shuffles and the update, with no barrier; the rows of
+// kTB tokens are staged at a time, the next ones in flight meanwhile.
+constexpr int kTB = 16;          // tokens staged at a time
+constexpr int kRecThreads = 128;
+constexpr int kRecCols = 16;     // state columns of a CTA
+
+template <typename IoT>
+__global__ void __launch_bounds__(kRecThreads) kda_gdn_recurrent_kernel(const GdnArgs a) {
+    __shared__ __align__(16) float k_s[2][kTB][D], q_s[2][kTB][D], v_s[2][kTB][kRecCols];
+    __shared__ float a_s[2][kTB], b_s[2][kTB];
+    const int tid = threadIdx.x, part = tid & 7, col = tid >> 3;
+    constexpr int NSL = D / kRecCols;
+    const int slice = blockIdx.x % NSL;
+    const int h = (blockIdx.x / NSL) % a.Hv;
+    const int n = blockIdx.x / (NSL * a.Hv);
+    const int hk = h / (a.Hv / a.Hk);
+    const int j0 = slice * kRecCols;
+    const int64_t t_begin = a.cu_seqlens[n], t_end = a.cu_seqlens[n + 1];
+    const bool ends_ok = a.cu_seqlens[0] == 0 && a.cu_seqlens[a.num_seqs] == a.total_tokens;
+    const bool ok = t_begin >= 0 && t_end >= t_begin && t_end <= a.total_tokens;
+    if ((!ok || !ends_ok) && tid == 0 && a.device_status) atomicOr(a.device_status, KDA_DEV_BAD_CU_SEQLENS);
+    if (!ok) return;
+    const IoT* const q = static_cast<const IoT*>(a.q);
+    const IoT* const k = static_cast<const IoT*>(a.k);
+    const IoT* const v = static_cast<const IoT*>(a.v);
+
+    float S[16];
+    const size_t st = ((static_cast<size_t>(n) * a.Hv + h) * D) * D + j0 + col;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        S[i] = a.S0 ? a.S0[st + static_cast<size_t>(4 * (8 * (i >> 2) + part) + (i & 3)) * D] : 0.f;
+
+    // this thread's share of a batch of rows: four quads of k and of q, two values of v, one gate
+    float4 kr[4], qr[4];
+    float vr[2], ar = 0.f, br = 0.f;
+    auto fetch = [&](int64_t t0) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int r = (tid + e * kRecThreads) >> 5, c = 4 * (tid & 31);
+            kr[e] = qr[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (t0 + r < t_end) {
+                const size_t off = (static_cast<size_t>(t0 + r) * a.Hk + hk) * D + c;
+                kr[e] = ld4(k + off);
+                qr[e] = ld4(q + off);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = (tid + e * kRecThreads) >> 4, c = tid & 15;
+            vr[e] = t0 + r < t_end ? to_f32(v[(static_cast<size_t>(t0 + r) * a.Hv + h) * D + j0 + c]) : 0.f;
+        }
+        if (tid < kTB && t0 + tid < t_end) {
+            ar = a.log_decay[(t0 + tid) * a.Hv + h];
+            br = a.beta[(t0 + tid) * a.Hv + h];
+        }
+    };
+    auto stage = [&](int buf) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int r = (tid + e * kRecThreads) >> 5, c = 4 * (tid & 31);
+            *reinterpret_cast<float4*>(&k_s[buf][r][c]) = kr[e];
+            *reinterpret_cast<float4*>(&q_s[buf][r][c]) = qr[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) v_s[buf][(tid + e * kRecThreads) >> 4][tid & 15] = vr[e];
+        if (tid < kTB) {
+            a_s[buf][tid] = expf(ar);
+            b_s[buf][tid] = br;
+        }
+    };
+    if (t_begin < t_end) fetch(t_begin);
+    int buf = 0;
+    for (int64_t t0 = t_begin; t0 < t_end; t0 += kTB, buf ^= 1) {
+        stage(buf);
+        __syncthreads();  // the other buffer's readers are past it too
+        if (t0 + kTB < t_end) fetch(t0 + kTB);
+        const int nt = static_cast<int>(t_end - t0 < kTB ? t_end - t0 : kTB);
+        for (int t = 0; t < nt; ++t) {
+            float4 kk[4];
+            float y[4] = {0.f, 0.f, 0.f, 0.f}, p[4] = {0.f, 0.f, 0.f, 0.f}, kq[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                kk[i] = *reinterpret_cast<const float4*>(&k_s[buf][t][4 * (8 * i + part)]);
+                const float4 qq = *reinterpret_cast<const float4*>(&q_s[buf][t][4 * (8 * i + part)]);
+                y[i] = fmaf(kk[i].x, S[4 * i], fmaf(kk[i].y, S[4 * i + 1], fmaf(kk[i].z, S[4 * i + 2], kk[i].w * S[4 * i + 3])));
+                p[i] = fmaf(qq.x, S[4 * i], fmaf(qq.y, S[4 * i + 1], fmaf(qq.z, S[4 * i + 2], qq.w * S[4 * i + 3])));
+                kq[i] = fmaf(kk[i].x, qq.x, fmaf(kk[i].y, qq.y, fmaf(kk[i].z, qq.z, kk[i].w * qq.w)));
+            }
+            float ys = (y[0] + y[1]) + (y[2] + y[3]), ps = (p[0] + p[1]) + (p[2] + p[3]);
+            float kqs = (kq[0] + kq[1]) + (kq[2] + kq[3]);
+#pragma unroll
+            for (int off = 4; off > 0; off >>= 1) {
+                ys += __shfl_xor_sync(0xffffffffu, ys, off);
+                ps += __shfl_xor_sync(0xffffffffu, ps, off);
+                kqs += __shfl_xor_sync(0xffffffffu, kqs, off);
+            }
+            const float al = a_s[buf][t];
+            const float u = b_s[buf][t] * (v_s[buf][t][col] - al * ys);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                S[4 * i] = fmaf(kk[i].x, u, al * S[4 * i]);
+                S[4 * i + 1] = fmaf(kk[i].y, u, al * S[4 * i + 1]);
+                S[4 * i + 2] = fmaf(kk[i].z, u, al * S[4 * i + 2]);
+                S[4 * i + 3] = fmaf(kk[i].w, u, al * S[4 * i + 3]);
+            }
+            if (part == 0)
+                st_f32(static_cast<IoT*>(a.o) + (static_cast<size_t>(t0 + t) * a.Hv + h) * D + j0 + col,
+                       fmaf(kqs, u, al * ps));
+        }
+    }
+    if (a.S_final) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            a.S_final[st + static_cast<size_t>(4 * (8 * (i >> 2) + part) + (i & 3)) * D] = S[i];
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_gdn_decode(bool f32_io, const void* q, const void* k, const void* v, const float* log_decay,
+                              const float* beta, float* S, int32_t num_slots, const int32_t* state_indices, int32_t N,
+                              int32_t Hk, int32_t Hv, void* o, int32_t* device_status, cudaStream_t stream) {
+    const int64_t units = static_cast<int64_t>(N) * Hv;
+    if (units == 0) return cudaSuccess;
+    const unsigned blocks = static_cast<unsigned>(units);
+    if (f32_io)
+        kda_gdn_decode_kernel<float><<<blocks, kDecThreads, 0, stream>>>(
+            static_cast<const float*>(q), static_cast<const float*>(k), static_cast<const float*>(v), log_decay, beta, S,
+            num_slots, state_indices, Hk, Hv, static_cast<float*>(o), device_status);
+    else
+        kda_gdn_decode_kernel<__nv_bfloat16><<<blocks, kDecThreads, 0, stream>>>(
+            static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
+            static_cast<const __nv_bfloat16*>(v), log_decay, beta, S, num_slots, state_indices, Hk, Hv,
+            static_cast<__nv_bfloat16*>(o), device_status);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_gdn_recurrent(bool f32_io, const GdnArgs& a, cudaStream_t stream) {
+    const int64_t units = static_cast<int64_t>(a.num_seqs) * a.Hv * (D / kRecCols);
+    if (units == 0) return cudaSuccess;
+    const unsigned blocks = static_cast<unsigned>(units);
+    if (f32_io) kda_gdn_recurrent_kernel<float><<<blocks, kRecThreads, 0, stream>>>(a);
+    else kda_gdn_recurrent_kernel<__nv_bfloat16><<<blocks, kRecThreads, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace kda

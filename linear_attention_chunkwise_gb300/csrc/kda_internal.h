@@ -33,6 +33,8 @@ constexpr int kHeadDim = 128;  // dk = dv
 // KDA_OK when the current device is sm_103 (the only architecture the kernels are built for),
 // KDA_ERR_UNSUPPORTED for another one, KDA_ERR_CUDA when the runtime cannot say.
 kda_status device_check();
+// SMs of the current device (0 when the runtime cannot say).
+int device_sm_count();
 
 // ---- decode ----
 struct DecodeFusion {  // KDA_FUSE_* bits and their parameters (see kda_fusion)
@@ -171,5 +173,58 @@ cudaError_t launch_bwd_outgate(bool f32_io, const void* o, const void* g, const 
                                void* dout, float* dg, float* dw, float* dw_part, int64_t rows, cudaStream_t stream);
 // prep, scan, value and key kernels; chunk_slots bounds the batch's chunk count.
 cudaError_t launch_backward(const BackwardArgs& a, bool f32_io, int64_t chunk_slots, cudaStream_t stream);
+
+
+// ---- gated delta rule, one decay per (token, value head) ----
+struct GdnArgs {
+    const void* q = nullptr;  // [T, Hk, 128]
+    const void* k = nullptr;
+    const void* v = nullptr;  // [T, Hv, 128]
+    const float* log_decay = nullptr;  // [T, Hv]
+    const float* beta = nullptr;
+    const float* S0 = nullptr;         // NULL: zeros
+    const int32_t* cu_seqlens = nullptr;
+    void* o = nullptr;
+    float* S_final = nullptr;          // NULL: not stored
+    int32_t* device_status = nullptr;
+    int64_t total_tokens = 0;
+    int32_t num_seqs = 0;
+    int32_t Hk = 0, Hv = 0;
+};
+// Token by token in fp32 (kda_gdn_recurrent.cu).
+cudaError_t launch_gdn_recurrent(bool f32_io, const GdnArgs& a, cudaStream_t stream);
+cudaError_t launch_gdn_decode(bool f32_io, const void* q, const void* k, const void* v, const float* log_decay,
+                              const float* beta, float* S, int32_t num_slots, const int32_t* state_indices, int32_t N,
+                              int32_t Hk, int32_t Hv, void* o, int32_t* device_status, cudaStream_t stream);
+
+// ---- RMS norm (kda_rms_norm.cu) ----
+struct NormArgs {
+    const void* x = nullptr;
+    const void* residual = nullptr;  // NULL: none
+    const float* weight = nullptr;   // NULL: ones
+    float eps = 0.f;
+    int64_t rows = 0;
+    int32_t dim = 0;
+    int32_t group = 0;               // columns per scale (0: the row)
+    void* y = nullptr;
+    float* scales = nullptr;
+    void* residual_out = nullptr;    // NULL: not stored
+};
+cudaError_t launch_rms_norm(bool f32_io, int32_t out_type, const NormArgs& a, cudaStream_t stream);
+struct NormBackwardArgs {
+    const void* grad_y = nullptr;
+    const void* h = nullptr;
+    const void* grad_h = nullptr;    // NULL: none
+    const float* weight = nullptr;   // NULL: ones
+    float eps = 0.f;
+    int64_t rows = 0;
+    int32_t dim = 0;
+    void* grad_x = nullptr;
+    float* grad_weight = nullptr;    // NULL: not computed
+    float* partial = nullptr;        // [rms_norm_backward_partials(rows)][dim]
+};
+// Row blocks whose sums of the weight's gradient are added at the end.
+int64_t rms_norm_backward_partials(int64_t rows);
+cudaError_t launch_rms_norm_backward(bool f32_io, const NormBackwardArgs& a, cudaStream_t stream);
 
 }  // namespace kda
