@@ -116,6 +116,17 @@ bool make_map(CUtensorMap* m, CUtensorMapDataType dt, size_t esize, const void* 
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+}  // namespace
+
+namespace kda {
+bool make_tensor_map(CUtensorMap* m, const void* base, uint64_t H, uint64_t T, uint32_t box_inner, uint32_t box_rows,
+                     CUtensorMapSwizzle sw) {
+    return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, kHeadDim, H, T, box_inner, box_rows, sw);
+}
+}  // namespace kda
+
+namespace {
+
 // Workspace layouts.  Two-pass path: [schedule][chunk table][bf16 q,k,v if
 // fp32 inputs][per-(chunk, head) operand images].  Single-pass path:
 // [schedule][bf16 q,k,v if fp32 inputs].

@@ -26,11 +26,17 @@ kda_status gdn_shape(kda_dtype t, int64_t rows, int32_t states, int32_t Hk, int3
     if (rows < 0 || states < 0 || Hk <= 0 || Hv <= 0 || rows > INT32_MAX - 64) return KDA_ERR_INVALID_ARG;
     if (dk != kHeadDim || dv != kHeadDim) return KDA_ERR_UNSUPPORTED;
     if (Hv % Hk != 0) return KDA_ERR_INVALID_ARG;
-    // a launch has one grid dimension: 8 blocks for every (sequence, value head)
+    // a launch has one grid dimension: 8 blocks for every (sequence, value head), one for every chunk's
     if (!sizes_ok(rows, Hv, kHeadDim, 4) || !sizes_ok(states, Hv, kStateBytes, 1) ||
-        static_cast<double>(states) * Hv * 8.0 > 2147483647.0)
+        static_cast<double>(states) * Hv * 8.0 > 2147483647.0 ||
+        (static_cast<double>(rows) / kda::kChunk + 1.0 + states) * Hv > 2147483647.0)
         return KDA_ERR_INVALID_ARG;
     return KDA_OK;
+}
+
+// fp32 inputs and short sequences go token by token.
+bool chunked(kda_dtype t, int32_t num_seqs, int64_t total_tokens) {
+    return t == KDA_DTYPE_BF16 && total_tokens > 16 * static_cast<int64_t>(num_seqs);
 }
 
 }  // namespace
@@ -40,7 +46,8 @@ extern "C" {
 size_t kda_gdn_prefill_workspace_bytes(kda_dtype qkv_dtype, int32_t num_seqs, int64_t total_tokens, int32_t Hk,
                                        int32_t Hv, int32_t dk, int32_t dv) {
     if (gdn_shape(qkv_dtype, total_tokens, num_seqs, Hk, Hv, dk, dv) != KDA_OK) return 0;
-    return kAlign;
+    if (!chunked(qkv_dtype, num_seqs, total_tokens)) return kAlign;
+    return kda::gdn_layout(num_seqs, total_tokens, Hv).total;
 }
 
 kda_status kda_gdn_prefill(const void* q, const void* k, const void* v, kda_dtype qkv_dtype, const float* log_decay,
@@ -95,9 +102,12 @@ kda_status kda_gdn_prefill(const void* q, const void* k, const void* v, kda_dtyp
     a.num_seqs = num_seqs;
     a.Hk = Hk;
     a.Hv = Hv;
-    const bool f32 = qkv_dtype == KDA_DTYPE_F32;
-    return kda::launch_gdn_recurrent(f32, a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK
-                                                                                                   : KDA_ERR_CUDA;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t err =
+        chunked(qkv_dtype, num_seqs, total_tokens)
+            ? kda::launch_gdn_chunked(a, kda::gdn_layout(num_seqs, total_tokens, Hv), static_cast<uint8_t*>(workspace), s)
+            : kda::launch_gdn_recurrent(qkv_dtype == KDA_DTYPE_F32, a, s);
+    return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 kda_status kda_gdn_decode_step(const void* q, const void* k, const void* v, kda_dtype qkv_dtype,

@@ -36,6 +36,11 @@ kda_status device_check();
 // SMs of the current device (0 when the runtime cannot say).
 int device_sm_count();
 
+// Tensor map over a bf16 [T][H][128] tensor with boxes of box_rows tokens of one head and box_inner
+// channels; false when the driver refuses it.
+bool make_tensor_map(CUtensorMap* m, const void* base, uint64_t H, uint64_t T, uint32_t box_inner, uint32_t box_rows,
+                     CUtensorMapSwizzle sw);
+
 // ---- decode ----
 struct DecodeFusion {  // KDA_FUSE_* bits and their parameters (see kda_fusion)
     uint32_t flags = 0;
@@ -193,6 +198,13 @@ struct GdnArgs {
 };
 // Token by token in fp32 (kda_gdn_recurrent.cu).
 cudaError_t launch_gdn_recurrent(bool f32_io, const GdnArgs& a, cudaStream_t stream);
+// Chunkwise, bf16 (kda_gdn_prefill.cu): workspace layout and the launches.
+struct GdnLayout {
+    size_t order = 0, table = 0, images = 0, total = 0;
+    int64_t chunks = 0;  // chunk entries: ceil(T / 64) + num_seqs
+};
+GdnLayout gdn_layout(int32_t num_seqs, int64_t total_tokens, int32_t Hv);
+cudaError_t launch_gdn_chunked(const GdnArgs& a, const GdnLayout& lay, uint8_t* workspace, cudaStream_t stream);
 cudaError_t launch_gdn_decode(bool f32_io, const void* q, const void* k, const void* v, const float* log_decay,
                               const float* beta, float* S, int32_t num_slots, const int32_t* state_indices, int32_t N,
                               int32_t Hk, int32_t Hv, void* o, int32_t* device_status, cudaStream_t stream);

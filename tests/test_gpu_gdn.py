@@ -19,6 +19,11 @@ from tests.gpu_util import host
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not cuda_ok(), reason="needs a CUDA GPU")]
 
 STATE = 5 * 2.0 ** -18
+# The chunkwise prefill (bf16) rounds four things to bf16 on the way to o: the state and U as the output
+# products take them, P, and o itself.  A rounding is spread over +- half a step (2^-8 of the value), so
+# in the 2-norm it is at most 2^-8 / sqrt(3) of what it rounds, and the four add up in squares at worst
+# with equal weight on all of o: 2 x 2^-8 / sqrt(3) = 4.6e-3; twice that where Q S and P U cancel in o.
+CHUNKED_O = 4 * 2.0 ** -8 / 3 ** 0.5
 
 
 def half_step(dtype):
@@ -44,6 +49,10 @@ def check_o(o, ref):
     assert np.all(np.abs(o64 - ref) <= half_step(o.dtype) * np.abs(ref) * (1 + STATE) + STATE * top)
 
 
+def check_chunked_o(o, ref):
+    assert np.linalg.norm(host(o).astype(np.float64) - ref) <= CHUNKED_O * np.linalg.norm(ref)
+
+
 def check_state(S, ref):
     d = np.abs(host(S).astype(np.float64) - ref)
     assert np.all(d <= STATE * np.abs(ref).max(axis=(-1, -2), initial=1e-30, keepdims=True))
@@ -51,7 +60,10 @@ def check_state(S, ref):
 
 def check(x, o, S):
     ro, rs = reference(x)
-    check_o(o, ro)
+    if o.dtype == torch.bfloat16:
+        check_chunked_o(o, ro)
+    else:
+        check_o(o, ro)
     check_state(S, rs)
 
 
@@ -123,7 +135,7 @@ def test_prefill_in_parts_and_decode_agree(cut):
     y = part(199, 200)
     o3 = kda.kda_gdn_decode_step(y["q"], y["k"], y["v"], y["log_decay"], y["beta"], S)
     ro, rs = reference(x)
-    check_o(torch.cat([o2, o3]), ro[cut:])
+    check_chunked_o(torch.cat([o2, o3]), ro[cut:])
     check_state(S, rs)
 
 
