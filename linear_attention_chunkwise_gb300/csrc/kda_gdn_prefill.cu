@@ -57,7 +57,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 // d += a b for one 16 x 8 tile (m16n8k16).  With g = lane / 4, t = lane % 4: a = A(g, 2t..), A(g + 8, 2t..),
 // A(g, 2t + 8..), A(g + 8, 2t + 8..); b = B(2t.., g), B(2t + 8.., g); d = D(g, 2t..), D(g + 8, 2t..).
 __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -85,34 +85,47 @@ __device__ __forceinline__ BTerms b_terms(const float (&c)[4]) {
 }
 
 // =============================================================== pass 1 ==
-constexpr int kPrepThreads = 256;
-constexpr int kLd = 68;  // floats in a row of the fp32 matrices: rows of 4 consecutive threads in other banks
+// One CTA of four warps for a (chunk, q/k head) and `hp` of its value heads, which share the Gram
+// matrices: warp r holds rows 16 r of K K^T and Q K^T in registers.  Per value head: the decays and
+// b make A and P of them; the 16 x 16 diagonal blocks of I + A are inverted by forward substitution
+// in fp32 (stable for any A; a column for each of 64 threads); then warp j forms block column j of the
+// inverse, T_ij = -D_i sum_{j <= k < i} A_ik T_kj, by mma.sync on two-term operands, its blocks staying in
+// its registers.  (The block products in fp32 on the CUDA cores and one value head a CTA, 256 threads:
+// 109 us for 8192 tokens x 32 heads, 16.1 K warp instructions a (chunk, head).)
+constexpr int kPrepThreads = 128;
 
 struct PrepSmem {
-    static constexpr uint32_t K = 0, Q = 16384;        // 2 x [64][128 B] each, 128B-swizzled
-    static constexpr uint32_t T = 0;                   // f32 [64][kLd], over K and Q once the Gram matrices are out
-    static constexpr uint32_t X = C * kLd * 4;         // f32 [32][kLd / 2 + ...]: product scratch, beside T
-    static constexpr uint32_t A = 32768;               // f32 [64][kLd]
-    static constexpr uint32_t G = A + C * kLd * 4;     // f32 [4][64]: g (two terms), beta, e^g
-    static constexpr uint32_t BAR = G + 4 * C * 4;
+    static constexpr uint32_t K = 0, Q = 16384;  // 2 x [64][128 B] each, 128B-swizzled
+    static constexpr uint32_t AH = 0;            // A's and the diagonal inverses' two terms: [64][128 B] bf16
+    static constexpr uint32_t AL = 8192;         // (over K and Q once the Gram matrices are out)
+    static constexpr uint32_t DG = 16384;        // f32 [4][16][17]: diagonal blocks of A
+    static constexpr uint32_t G = 32768;         // f32 [3][64]: g (two terms, base 2), beta
+    static constexpr uint32_t BAR = G + 3 * C * 4;
     static constexpr uint32_t TOTAL = BAR + 16;
     static constexpr uint32_t ALLOC = TOTAL + 1024;
 };
-static_assert(PrepSmem::X + 32 * 36 * 4 <= PrepSmem::A, "the inverse's scratch fits beside T");
 
 // log decays below this (a decay of 0 in fp32, as -inf) are taken as this, so that differences of the
 // cumulative sums stay numbers.
 constexpr float kDecayFloor = -1e4f;
 
-__global__ void __launch_bounds__(kPrepThreads)
+// 2^x by the special function unit (2 ulp); x is a difference of decays in base 2.
+__device__ __forceinline__ float exp2_sfu(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__global__ void __launch_bounds__(kPrepThreads, 4)
     kda_gdn_prep_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                        const GdnArgs p, const int32_t* __restrict__ co, uint8_t* images, int64_t chunk_slots) {
+                        const GdnArgs p, const int32_t* __restrict__ co, uint8_t* images, int64_t chunk_slots,
+                        int32_t hp) {
     using L = PrepSmem;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int N = p.num_seqs, Hv = p.Hv;
-    const int j = blockIdx.x / Hv, h = blockIdx.x - j * Hv;
+    const int N = p.num_seqs, Hv = p.Hv, groups = Hv / hp;
+    const int j = blockIdx.x / groups, h0 = (blockIdx.x - j * groups) * hp;
     if (co[N + 1] == 0 || j >= co[N]) return;  // malformed cu_seqlens, or no such chunk
     int seq;
     {  // the largest n with co[n] <= j
@@ -130,7 +143,6 @@ __global__ void __launch_bounds__(kPrepThreads)
     if (!KDA_BOUNDS(seq >= 0 && seq < N && j < chunk_slots && t0 >= 0 && Lc >= 1 && t0 + Lc <= p.total_tokens,
                     p.device_status))
         return;
-    uint8_t* const img = images + (static_cast<size_t>(j) * Hv + h) * kImgStride;
 
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::BAR);
     float* const g_hi = reinterpret_cast<float*>(sm + L::G);
@@ -140,14 +152,16 @@ __global__ void __launch_bounds__(kPrepThreads)
         mbar_init(bar, 1);
         fence_mbar_init();
         mbar_arrive_expect_tx(bar, 32768);
-        const int hk = h / (Hv / p.Hk);
+        const int hk = h0 / (Hv / p.Hk);
 #pragma unroll
         for (int kh = 0; kh < 2; ++kh) {
             tma_load_3d(sm + L::K + kh * 8192, &tm_k, bar, 64 * kh, hk, static_cast<int32_t>(t0));
             tma_load_3d(sm + L::Q + kh * 8192, &tm_q, bar, 64 * kh, hk, static_cast<int32_t>(t0));
         }
     }
-    if (warp == 1) {  // cumulative log decay, two tokens a lane, in fp64: kept as two fp32 terms
+    // Value head h's cumulative log decay (base 2, two tokens a lane, in fp64; kept as two fp32 terms), beta,
+    // and the image's decays.
+    auto decays = [&](int h) {
         double x[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -157,7 +171,7 @@ __global__ void __launch_bounds__(kPrepThreads)
                 ld = p.log_decay[(t0 + r) * Hv + h];
                 b = p.beta[(t0 + r) * Hv + h];
             }
-            x[e] = ld < kDecayFloor ? kDecayFloor : ld;
+            x[e] = static_cast<double>(ld < kDecayFloor ? kDecayFloor : ld) * 1.4426950408889634;
             beta_s[r] = b;
         }
         double s = x[0] + x[1];
@@ -167,7 +181,7 @@ __global__ void __launch_bounds__(kPrepThreads)
             if (lane >= off) s += y;
         }
         const double last = __shfl_sync(0xffffffffu, s, 31);
-        float* gv = reinterpret_cast<float*>(img + kImgG);
+        float* gv = reinterpret_cast<float*>(images + (static_cast<size_t>(j) * Hv + h) * kImgStride + kImgG);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int r = 2 * lane + e;
@@ -175,164 +189,211 @@ __global__ void __launch_bounds__(kPrepThreads)
             const float hi = static_cast<float>(g);
             g_hi[r] = hi;
             g_lo[r] = static_cast<float>(g - hi);
-            gv[r] = expf(hi) * (1.f + static_cast<float>(g - hi));
-            gv[C + r] = expf(static_cast<float>(last - g));
+            gv[r] = exp2f(static_cast<float>(g));
+            gv[C + r] = exp2f(static_cast<float>(last - g));
         }
-        if (lane == 0) gv[2 * C] = expf(static_cast<float>(last));
-    }
+        if (lane == 0) gv[2 * C] = exp2f(static_cast<float>(last));
+    };
+    if (warp == 1) decays(h0);
     bool ok = true;
     if (tid == 0) ok = mbar_wait_pipe(bar, 0);
     if (!ok && p.device_status) atomicOr(p.device_status, KDA_DEV_TIMEOUT);
     __syncthreads();
 
-    // Gram rows: warp w < 4 takes rows 16 w of K K^T, warp 4 + w rows 16 (3 - w) of Q K^T (so that the two
-    // warps of an SM quarter share its ten 16 x 16 blocks evenly), columns up to the diagonal block.
+    // Gram rows up to the diagonal block.  The row block of a warp turns with the CTA, so that no quarter of
+    // the SM has the long rows of every CTA.
     const int g = lane >> 2, t = lane & 3;
-    const bool is_q = warp >= 4;
-    const int mr = is_q ? 7 - warp : warp;
-    float acc[8][4];
+    const int mr = (warp + blockIdx.x) & 3;
+    float kk[8][4], qk[8][4];
 #pragma unroll
     for (int n = 0; n < 8; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+        for (int e = 0; e < 4; ++e) kk[n][e] = qk[n][e] = 0.f;
     {
-        const uint32_t a_base = smem_u32(sm + (is_q ? L::Q : L::K)), b_base = smem_u32(sm + L::K);
+        const uint32_t kb = smem_u32(sm + L::K), qb = smem_u32(sm + L::Q);
         const int ar = 16 * mr + (lane & 15), br = (lane & 7) + ((lane >> 4) << 3), bc = (lane >> 3) & 1;
 #pragma unroll
         for (int kt = 0; kt < 8; ++kt) {
-            uint32_t a[4];
-            ldsm4(a, a_base + (kt >> 2) * 8192 + sw128_chunk(ar, 2 * (kt & 3) + (lane >> 4)));
+            uint32_t ak[4], aq[4];
+            const uint32_t off = (kt >> 2) * 8192;
+            ldsm4(ak, kb + off + sw128_chunk(ar, 2 * (kt & 3) + (lane >> 4)));
+            ldsm4(aq, qb + off + sw128_chunk(ar, 2 * (kt & 3) + (lane >> 4)));
 #pragma unroll
             for (int np = 0; np < 4; ++np) {
-                if (np > mr) continue;
+                if (np > mr) break;
                 uint32_t b[4];
-                ldsm4(b, b_base + (kt >> 2) * 8192 + sw128_chunk(16 * np + br, 2 * (kt & 3) + bc));
-                mma16(acc[2 * np], a, b[0], b[1]);
-                mma16(acc[2 * np + 1], a, b[2], b[3]);
+                ldsm4(b, kb + off + sw128_chunk(16 * np + br, 2 * (kt & 3) + bc));
+                mma16(kk[2 * np], ak, b[0], b[1]);
+                mma16(kk[2 * np + 1], ak, b[2], b[3]);
+                mma16(qk[2 * np], aq, b[0], b[1]);
+                mma16(qk[2 * np + 1], aq, b[2], b[3]);
             }
         }
     }
-    __syncthreads();  // K and Q have been read: T may take their place
-    float* const As = reinterpret_cast<float*>(sm + L::A);
-    float* const Ts = reinterpret_cast<float*>(sm + L::T);
-    float* const Xs = reinterpret_cast<float*>(sm + L::X);
+    const uint32_t ah_base = smem_u32(sm + L::AH), al_base = smem_u32(sm + L::AL);
+    float* const dg = reinterpret_cast<float*>(sm + L::DG);
+    for (int hh = 0; hh < hp; ++hh) {
+        const int h = h0 + hh;
+        uint8_t* const img = images + (static_cast<size_t>(j) * Hv + h) * kImgStride;
+        __syncthreads();  // K and Q, or the previous head's A and decays, have been read
+        if (hh > 0) {
+            if (warp == 1) decays(h);
+            __syncthreads();
+        }
+        // A (two terms; its diagonal blocks in fp32) and P
 #pragma unroll
-    for (int n = 0; n < 8; ++n) {
-        if (n > 2 * mr + 1) continue;
+        for (int n = 0; n < 8; ++n) {
+            if (n > 2 * mr + 1) break;
 #pragma unroll
-        for (int e2 = 0; e2 < 2; ++e2) {  // rows g and g + 8 of the tile
-            const int i = 16 * mr + g + 8 * e2;
-            float v[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int jj = 8 * n + 2 * t + e;
-                const float d = (g_hi[i] - g_hi[jj]) + (g_lo[i] - g_lo[jj]);
-                const bool in = i < Lc && (is_q ? jj <= i : jj < i);
-                v[e] = in ? expf(d) * acc[n][2 * e2 + e] : 0.f;
-            }
-            if (is_q) {
-                *reinterpret_cast<uint32_t*>(img + kImgP + sw128_chunk(i, n) + 4 * t) = pack_bf16(v[0], v[1]);
-            } else {
-                const float b = beta_s[i];
-                *reinterpret_cast<float2*>(As + i * kLd + 8 * n + 2 * t) =
-                    make_float2(v[0] * b, v[1] * b);
+            for (int e2 = 0; e2 < 2; ++e2) {  // rows g and g + 8 of the tile
+                const int i = 16 * mr + g + 8 * e2;
+                const float2 ch = *reinterpret_cast<const float2*>(g_hi + 8 * n + 2 * t);
+                const float2 cl = *reinterpret_cast<const float2*>(g_lo + 8 * n + 2 * t);
+                const float gi = g_hi[i], gl = g_lo[i], b = beta_s[i];
+                const int jj = 8 * n + 2 * t;
+                const bool row = i < Lc;
+                const float d0 = exp2_sfu((gi - ch.x) + (gl - cl.x)), d1 = exp2_sfu((gi - ch.y) + (gl - cl.y));
+                const float p0 = row && jj <= i ? d0 * qk[n][2 * e2] : 0.f;
+                const float p1 = row && jj + 1 <= i ? d1 * qk[n][2 * e2 + 1] : 0.f;
+                *reinterpret_cast<uint32_t*>(img + kImgP + sw128_chunk(i, n) + 4 * t) = pack_bf16(p0, p1);
+                const float a0 = row && jj < i ? b * d0 * kk[n][2 * e2] : 0.f;
+                const float a1 = row && jj + 1 < i ? b * d1 * kk[n][2 * e2 + 1] : 0.f;
+                if ((n >> 1) == mr) {
+                    float* d = dg + mr * 272 + (g + 8 * e2) * 17 + 8 * (n & 1) + 2 * t;
+                    d[0] = a0;
+                    d[1] = a1;
+                } else {
+                    uint32_t hi, lo;
+                    split2(a0, a1, hi, lo);
+                    *reinterpret_cast<uint32_t*>(sm + L::AH + sw128_chunk(i, n) + 4 * t) = hi;
+                    *reinterpret_cast<uint32_t*>(sm + L::AL + sw128_chunk(i, n) + 4 * t) = lo;
+                }
             }
         }
-    }
-    __syncthreads();
-    // T = (I + A)^-1 by blocks.  Diagonal 16 x 16 blocks: a column for each of 64 threads, by forward
-    // substitution (stable for any A).
-    if (tid < 64) {
-        const int b0 = tid & ~15, c = tid & 15;
-        float x[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float s0 = i == c ? 1.f : 0.f, s1 = 0.f;
-#pragma unroll
-            for (int k = 0; k < i; ++k) {
-                const float av = As[(b0 + i) * kLd + b0 + k];
-                if (k & 1) s1 = fmaf(-av, x[k], s1);
-                else s0 = fmaf(-av, x[k], s0);
-            }
-            x[i] = s0 + s1;
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) Ts[(b0 + i) * kLd + b0 + c] = x[i];
-    }
-    __syncthreads();
-    // Blocks (1,0) and (3,2): X = A_lo T_diag, then T = -T_diag X; two outputs a thread.
-    {
-        const int pr = tid >> 7, e = tid & 127, r = e >> 3, c = 2 * (e & 7), b0 = 32 * pr;
-        float x0 = 0.f, x1 = 0.f;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const float av = As[(b0 + 16 + r) * kLd + b0 + k];
-            const float2 tv = *reinterpret_cast<const float2*>(Ts + (b0 + k) * kLd + b0 + c);
-            x0 = fmaf(av, tv.x, x0);
-            x1 = fmaf(av, tv.y, x1);
-        }
-        *reinterpret_cast<float2*>(Xs + (16 * pr + r) * 36 + c) = make_float2(x0, x1);
         __syncthreads();
-        x0 = x1 = 0.f;
+        if (tid < 64) {  // D_b = (I + A_bb)^-1, column c of block b
+            const int b = tid >> 4, c = tid & 15;
+            const float* A = dg + b * 272;
+            float x[16];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const float tv = Ts[(b0 + 16 + r) * kLd + b0 + 16 + k];
-            const float2 xv = *reinterpret_cast<const float2*>(Xs + (16 * pr + k) * 36 + c);
-            x0 = fmaf(-tv, xv.x, x0);
-            x1 = fmaf(-tv, xv.y, x1);
+            for (int i = 0; i < 16; ++i) {
+                float s0 = i == c ? 1.f : 0.f, s1 = 0.f;
+#pragma unroll
+                for (int k = 0; k < i; ++k) {
+                    if (k & 1) s1 = fmaf(-A[i * 17 + k], x[k], s1);
+                    else s0 = fmaf(-A[i * 17 + k], x[k], s0);
+                }
+                x[i] = s0 + s1;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t off = sw128_chunk(16 * b + i, 2 * b + (c >> 3)) + 2 * (c & 7);
+                const __nv_bfloat16 hi = __float2bfloat16_rn(x[i]);
+                *reinterpret_cast<__nv_bfloat16*>(sm + L::AH + off) = hi;
+                *reinterpret_cast<__nv_bfloat16*>(sm + L::AL + off) = __float2bfloat16_rn(x[i] - __bfloat162float(hi));
+            }
         }
-        *reinterpret_cast<float2*>(Ts + (b0 + 16 + r) * kLd + b0 + c) = make_float2(x0, x1);
-        *reinterpret_cast<float2*>(Ts + (b0 + r) * kLd + b0 + 16 + c) = make_float2(0.f, 0.f);
-    }
-    __syncthreads();
-    // The lower left 32 x 32 block: X = A_hl T_ll, T_hl = -T_hh X; four columns of a row a thread.
-    {
-        const int r = tid >> 3, c = 4 * (tid & 7);
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int k = 0; k < 32; ++k) {
-            const float av = As[(32 + r) * kLd + k];
-            const float4 tv = *reinterpret_cast<const float4*>(Ts + k * kLd + c);
-            x.x = fmaf(av, tv.x, x.x); x.y = fmaf(av, tv.y, x.y);
-            x.z = fmaf(av, tv.z, x.z); x.w = fmaf(av, tv.w, x.w);
-        }
-        __syncthreads();  // the first products' scratch has been read
-        *reinterpret_cast<float4*>(Xs + r * 36 + c) = x;
         __syncthreads();
-        x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int k = 0; k < 32; ++k) {
-            const float tv = Ts[(32 + r) * kLd + 32 + k];
-            const float4 xv = *reinterpret_cast<const float4*>(Xs + k * 36 + c);
-            x.x = fmaf(-tv, xv.x, x.x); x.y = fmaf(-tv, xv.y, x.y);
-            x.z = fmaf(-tv, xv.z, x.z); x.w = fmaf(-tv, xv.w, x.w);
-        }
-        *reinterpret_cast<float4*>(Ts + (32 + r) * kLd + c) = x;
-    }
-    __syncthreads();
-    // T Diag(b) in two bf16 terms, 8 columns of a row at a time
-    for (int e = tid; e < C * 8; e += kPrepThreads) {
-        const int r = e >> 3, ch = e & 7;
-        if ((ch >> 1) > (r >> 4)) continue;
-        float v[8];
+        // Block column w of the inverse by warp w.  T_ww = D_w from shared memory, the others from the products.
+        {
+            const int w = mr;
+            const int lr = lane & 15, lc = lane >> 4;
+            const int tr = (lane & 7) + (((lane >> 3) & 1) << 3), tc = lane >> 4;
+            BTerms T[4][2];  // blocks (k, w) as B operands, two 8-column halves
+            {
+                uint32_t bh[4], bl[4];
+                ldsm4t(bh, ah_base + sw128_chunk(16 * w + tr, 2 * w + tc));
+                ldsm4t(bl, al_base + sw128_chunk(16 * w + tr, 2 * w + tc));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = Ts[r * kLd + 8 * ch + i] * beta_s[8 * ch + i];
-        uint4 hi, lo;
-        split2(v[0], v[1], hi.x, lo.x);
-        split2(v[2], v[3], hi.y, lo.y);
-        split2(v[4], v[5], hi.z, lo.z);
-        split2(v[6], v[7], hi.w, lo.w);
-        *reinterpret_cast<uint4*>(img + kImgTh + sw128_chunk(r, ch)) = hi;
-        *reinterpret_cast<uint4*>(img + kImgTl + sw128_chunk(r, ch)) = lo;
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)  // every slot below the diagonal is overwritten before its use
+                        T[k][n] = BTerms{bh[2 * n], bh[2 * n + 1], bl[2 * n], bl[2 * n + 1]};
+            }
+            const float b0 = beta_s[16 * w + 2 * t], b1 = beta_s[16 * w + 2 * t + 1];
+            const float b2 = beta_s[16 * w + 8 + 2 * t], b3 = beta_s[16 * w + 9 + 2 * t];
+            auto store = [&](int i, const float (&x)[2][4]) {  // block (i, w), times b of its columns
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e2 = 0; e2 < 2; ++e2) {
+                        uint32_t hi, lo;
+                        split2(x[n][2 * e2] * (n ? b2 : b0), x[n][2 * e2 + 1] * (n ? b3 : b1), hi, lo);
+                        const uint32_t off = sw128_chunk(16 * i + g + 8 * e2, 2 * w + n) + 4 * t;
+                        *reinterpret_cast<uint32_t*>(img + kImgTh + off) = hi;
+                        *reinterpret_cast<uint32_t*>(img + kImgTl + off) = lo;
+                    }
+            };
+            {  // the diagonal block itself, as accumulators hold it
+                float x[2][4];
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e2 = 0; e2 < 2; ++e2) {
+                        const uint32_t off = sw128_chunk(16 * w + g + 8 * e2, 2 * w + n) + 4 * t;
+                        const float2 hi = unpack_bf16(*reinterpret_cast<const uint32_t*>(sm + L::AH + off));
+                        const float2 lo = unpack_bf16(*reinterpret_cast<const uint32_t*>(sm + L::AL + off));
+                        x[n][2 * e2] = hi.x + lo.x;
+                        x[n][2 * e2 + 1] = hi.y + lo.y;
+                    }
+                store(w, x);
+            }
+#pragma unroll
+            for (int i = 1; i < 4; ++i) {
+                if (i <= w) continue;
+                float x[2][4];
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
+                uint32_t ah[4], al[4];
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    if (k < w || k >= i) continue;
+                    ldsm4(ah, ah_base + sw128_chunk(16 * i + lr, 2 * k + lc));
+                    ldsm4(al, al_base + sw128_chunk(16 * i + lr, 2 * k + lc));
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) mma16(x[n], ah, T[k][n].h0, T[k][n].h1);
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) mma16(x[n], ah, T[k][n].l0, T[k][n].l1);
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) mma16(x[n], al, T[k][n].h0, T[k][n].h1);
+                }
+                BTerms X[2];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[n][e] = -x[n][e];
+                    X[n] = b_terms(x[n]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
+                }
+                ldsm4(ah, ah_base + sw128_chunk(16 * i + lr, 2 * i + lc));
+                ldsm4(al, al_base + sw128_chunk(16 * i + lr, 2 * i + lc));
+#pragma unroll
+                for (int n = 0; n < 2; ++n) mma16(x[n], ah, X[n].h0, X[n].h1);
+#pragma unroll
+                for (int n = 0; n < 2; ++n) mma16(x[n], ah, X[n].l0, X[n].l1);
+#pragma unroll
+                for (int n = 0; n < 2; ++n) mma16(x[n], al, X[n].h0, X[n].h1);
+#pragma unroll
+                for (int n = 0; n < 2; ++n) T[i][n] = b_terms(x[n]);
+                store(i, x);
+            }
+        }
     }
 }
 
 // =============================================================== pass 2 ==
-// NW warps of 8 NT state columns each; ST stages of tiles, filled by copies that thread 0 issues.
+// NW warps of 8 NT state columns each and one that issues the copies; ST stages of tiles.
 template <int NT, int NW, int ST>
 struct ScanCfg {
     static constexpr int kCols = 8 * NT * NW;
-    static constexpr int kThreads = 32 * NW;
+    // Four consumer warps leave each thread 255 registers beside the copying warp.  Eight do not (an SM
+    // quarter would hold three warps): they take a warpgroup of 128 for the copies, whose registers go to
+    // the consumers: launched with 168 a thread, 384 x 168 = 256 x 232 + 128 x 40.
+    static constexpr bool kSplit = NW == 8;
+    static constexpr int kThreads = kSplit ? 384 : 32 * (NW + 1);
     static constexpr uint32_t kVRow = kCols >= 64 ? 128 : kCols * 2;  // bytes of a v row in a block
     static constexpr int kVBlocks = kCols >= 64 ? kCols / 64 : 1;
     static constexpr uint32_t K = 0, Q = 16384, IMG = 32768, V = IMG + 25600;
@@ -379,243 +440,253 @@ __global__ void __launch_bounds__(ScanCfg<NT, NW, ST>::kThreads, 1)
     }
     __syncthreads();
 
-    // Chunk c's tiles into stage c mod ST.
-    auto issue = [&](int c) {
-        const int s = c % ST;
-        uint8_t* st = sm + s * L::STAGE;
-        const int32_t tok = static_cast<int32_t>(t_begin + static_cast<int64_t>(c) * C);
-        const int hk = h / (Hv / p.Hk);
-        mbar_arrive_expect_tx(&full[s], 32768 + kImgBytes + C * L::kVRow * L::kVBlocks);
+    // A warp of its own issues the copies (a thread is held for about 0.1 us by each): chunk c's tiles go into
+    // stage c mod ST once every reader is done with chunk c - ST.
+    if (warp >= NW) {
+        if constexpr (L::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == NW && lane == 0) {
+            const int hk = h / (Hv / p.Hk);
+            int c = 0;
+            for (; c < nch && !*abort_s; ++c) {
+                const int s = c % ST;
+                if (c >= ST && !mbar_wait_pipe(&empty[s], ((c / ST) - 1) & 1)) {
+                    *abort_s = 1;
+                    break;
+                }
+                uint8_t* st = sm + s * L::STAGE;
+                const int32_t tok = static_cast<int32_t>(t_begin + static_cast<int64_t>(c) * C);
+                mbar_arrive_expect_tx(&full[s], 32768 + kImgBytes + C * L::kVRow * L::kVBlocks);
 #pragma unroll
-        for (int kh = 0; kh < 2; ++kh) {
-            tma_load_3d(st + L::K + kh * 8192, &tm_k, &full[s], 64 * kh, hk, tok);
-            tma_load_3d(st + L::Q + kh * 8192, &tm_q, &full[s], 64 * kh, hk, tok);
-        }
-        bulk_g2s(st + L::IMG, images + (static_cast<size_t>(jb + c) * Hv + h) * kImgStride, kImgBytes, &full[s]);
+                for (int kh = 0; kh < 2; ++kh) tma_load_3d(st + L::K + kh * 8192, &tm_k, &full[s], 64 * kh, hk, tok);
 #pragma unroll
-        for (int b = 0; b < L::kVBlocks; ++b)
-            tma_load_3d(st + L::V + b * C * L::kVRow, &tm_v, &full[s], slice * L::kCols + 64 * b, h, tok);
-    };
-    int issued = min(ST, nch);  // chunks whose copies thread 0 has issued
-    if (tid == 0)
-        for (int c = 0; c < issued; ++c) issue(c);
-    const int g = lane >> 2, t = lane & 3;
-    const int wc = 8 * NT * warp;                  // the warp's first column in the CTA's
-    const int j0 = slice * L::kCols + wc + 2 * t;  // this thread's first state column
-    const size_t sbase = (static_cast<size_t>(seq) * Hv + h) * D * D;
-    float S[8][NT][4];  // rows 16 m + g (+ 8), columns j0 + 8 n (+ 1)
+                for (int b = 0; b < L::kVBlocks; ++b)
+                    tma_load_3d(st + L::V + b * C * L::kVRow, &tm_v, &full[s], slice * L::kCols + 64 * b, h, tok);
+                bulk_g2s(st + L::IMG, images + (static_cast<size_t>(jb + c) * Hv + h) * kImgStride, kImgBytes, &full[s]);
 #pragma unroll
-    for (int m = 0; m < 8; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const size_t off = sbase + static_cast<size_t>(16 * m + g + 8 * e) * D + j0 + 8 * n;
-                const float2 x = p.S0 ? *reinterpret_cast<const float2*>(p.S0 + off) : make_float2(0.f, 0.f);
-                S[m][n][2 * e] = x.x;
-                S[m][n][2 * e + 1] = x.y;
+                for (int kh = 0; kh < 2; ++kh) tma_load_3d(st + L::Q + kh * 8192, &tm_q, &full[s], 64 * kh, hk, tok);
             }
-    // ldmatrix addresses within a tile: rows of tokens (row-major operand) and their transposes
-    const int lr = lane & 15, lc = lane >> 4;
-    const int tr = (lane & 7) + ((lane >> 4) << 3), tc = (lane >> 3) & 1;
-    for (int c = 0; c < nch; ++c) {
-        const int s = c % ST;
-        uint8_t* st = sm + s * L::STAGE;
-        const bool landed = !*abort_s && mbar_wait_pipe(&full[s], (c / ST) & 1);
-        if (!__all_sync(0xffffffffu, landed)) {  // a bounded wait expired, here or elsewhere
-            *abort_s = 1;
-            break;
+            for (int d = max(0, c - ST); d < c; ++d)  // no copy is left in flight
+                (void)mbar_wait(&full[d % ST], (d / ST) & 1, kDrainLimit);
         }
-        const int64_t t0 = t_begin + static_cast<int64_t>(c) * C;
-        const int Lc = static_cast<int>(t_end - t0 < C ? t_end - t0 : C);
-        if (Lc < C) {  // k rows behind the sequence's end meet zeros of U: they must be numbers
-            for (int e = lane; e < (C - Lc) * 16; e += 32)
-                *reinterpret_cast<uint4*>(st + L::K + (e & 1) * 8192 + sw128_chunk(Lc + (e >> 4), (e >> 1) & 7)) =
-                    make_uint4(0u, 0u, 0u, 0u);
-            __syncwarp();
-        }
-        const uint32_t kb = smem_u32(st + L::K), qb = smem_u32(st + L::Q), ib = smem_u32(st + L::IMG);
-        const float* gs = reinterpret_cast<const float*>(st + L::IMG + kImgG);
-        float ks[4][NT][4], qs[4][NT][4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
+    } else {
+        if constexpr (L::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        const int g = lane >> 2, t = lane & 3;
+        const int wc = 8 * NT * warp;                  // the warp's first column in the CTA's
+        const int j0 = slice * L::kCols + wc + 2 * t;  // this thread's first state column
+        const size_t sbase = (static_cast<size_t>(seq) * Hv + h) * D * D;
+        float S[8][NT][4];  // rows 16 m + g (+ 8), columns j0 + 8 n (+ 1)
+    #pragma unroll
+        for (int m = 0; m < 8; ++m)
+    #pragma unroll
             for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) ks[m][n][e] = qs[m][n][e] = 0.f;
-        // K S (state in two terms) and Q S (the output takes one term: it is rounded to bf16 too)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            BTerms b[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) b[n] = b_terms(S[k][n]);
-            const uint32_t off = (k >> 2) * 8192;
-            uint32_t a[4][4];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) ldsm4(a[m], kb + off + sw128_chunk(16 * m + lr, 2 * (k & 3) + lc));
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma16(ks[m][n], a[m], b[n].h0, b[n].h1);
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma16(ks[m][n], a[m], b[n].l0, b[n].l1);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) ldsm4(a[m], qb + off + sw128_chunk(16 * m + lr, 2 * (k & 3) + lc));
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma16(qs[m][n], a[m], b[n].h0, b[n].h1);
-        }
-        // The previous chunk's stage is refilled once every warp is done with it.
-        if (warp == 0 && c > 0 && issued < nch) {
-            bool done = true;
-            if (lane == 0) {
-                done = mbar_wait_pipe(&empty[(c - 1) % ST], ((c - 1) / ST) & 1);
-                if (done) issue(issued);
-                else *abort_s = 1;
-            }
-            if (__all_sync(0xffffffffu, done)) ++issued;
-        }
-        // R = V - e^g K S, then U = T R with both in two terms
-        float u[4][NT][4];
-        float eg[4][2];
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) u[m][n][e] = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            BTerms b[NT];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) eg[k][e] = gs[16 * k + g + 8 * e];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float r[4];
-#pragma unroll
+    #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int row = 16 * k + g + 8 * e, col = wc + 8 * n;  // the 16-byte piece of 8 columns
-                    const uint32_t piece = static_cast<uint32_t>(col >> 3);
-                    uint32_t off;
-                    if constexpr (L::kVRow == 128)
-                        off = (piece >> 3) * (C * 128) + sw128_chunk(row, piece & 7);
-                    else  // 64-byte rows: the swizzle takes bits 1 and 2 of the row
-                        off = row * 64 + (((piece ^ (row >> 1)) & 3) << 4);
-                    const uint32_t vv = *reinterpret_cast<const uint32_t*>(st + L::V + off + 4 * t);
-                    r[2 * e] = fmaf(-eg[k][e], ks[k][n][2 * e], __uint_as_float(vv << 16));
-                    r[2 * e + 1] = fmaf(-eg[k][e], ks[k][n][2 * e + 1], __uint_as_float(vv & 0xffff0000u));
-                    if (row >= Lc) r[2 * e] = r[2 * e + 1] = 0.f;
+                    const size_t off = sbase + static_cast<size_t>(16 * m + g + 8 * e) * D + j0 + 8 * n;
+                    const float2 x = p.S0 ? *reinterpret_cast<const float2*>(p.S0 + off) : make_float2(0.f, 0.f);
+                    S[m][n][2 * e] = x.x;
+                    S[m][n][2 * e + 1] = x.y;
                 }
-                b[n] = b_terms(r);
+        // ldmatrix addresses within a tile: rows of tokens (row-major operand) and their transposes
+        const int lr = lane & 15, lc = lane >> 4;
+        const int tr = (lane & 7) + ((lane >> 4) << 3), tc = (lane >> 3) & 1;
+        for (int c = 0; c < nch; ++c) {
+            const int s = c % ST;
+            uint8_t* st = sm + s * L::STAGE;
+            const bool landed = !*abort_s && mbar_wait_pipe(&full[s], (c / ST) & 1);
+            if (!__all_sync(0xffffffffu, landed)) {  // a bounded wait expired, here or elsewhere
+                *abort_s = 1;
+                break;
             }
-            uint32_t ah[4][4];
-#pragma unroll
-            for (int m = k; m < 4; ++m) ldsm4(ah[m], ib + kImgTh + sw128_chunk(16 * m + lr, 2 * k + lc));
-#pragma unroll
-            for (int m = k; m < 4; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma16(u[m][n], ah[m], b[n].h0, b[n].h1);
-#pragma unroll
-            for (int m = k; m < 4; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma16(u[m][n], ah[m], b[n].l0, b[n].l1);
-#pragma unroll
-            for (int m = k; m < 4; ++m) ldsm4(ah[m], ib + kImgTl + sw128_chunk(16 * m + lr, 2 * k + lc));
-#pragma unroll
-            for (int m = k; m < 4; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma16(u[m][n], ah[m], b[n].h0, b[n].h1);
-        }
-        // S <- e^gC S + K^T (e^(gC - g) U), U in two terms
-        const float gc = gs[2 * C];
-#pragma unroll
-        for (int m = 0; m < 8; ++m)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) S[m][n][e] *= gc;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float e0 = gs[C + 16 * k + g], e1 = gs[C + 16 * k + g + 8];
-            BTerms b[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float x[4] = {u[k][n][0] * e0, u[k][n][1] * e0, u[k][n][2] * e1, u[k][n][3] * e1};
-                b[n] = b_terms(x);
+            const int64_t t0 = t_begin + static_cast<int64_t>(c) * C;
+            const int Lc = static_cast<int>(t_end - t0 < C ? t_end - t0 : C);
+            if (Lc < C) {  // k rows behind the sequence's end meet zeros of U: they must be numbers
+                for (int e = lane; e < (C - Lc) * 16; e += 32)
+                    *reinterpret_cast<uint4*>(st + L::K + (e & 1) * 8192 + sw128_chunk(Lc + (e >> 4), (e >> 1) & 7)) =
+                        make_uint4(0u, 0u, 0u, 0u);
+                __syncwarp();
             }
-#pragma unroll
-            for (int mh = 0; mh < 2; ++mh) {
+            const uint32_t kb = smem_u32(st + L::K), qb = smem_u32(st + L::Q), ib = smem_u32(st + L::IMG);
+            const float* gs = reinterpret_cast<const float*>(st + L::IMG + kImgG);
+            float ks[4][NT][4], qs[4][NT][4];
+    #pragma unroll
+            for (int m = 0; m < 4; ++m)
+    #pragma unroll
+                for (int n = 0; n < NT; ++n)
+    #pragma unroll
+                    for (int e = 0; e < 4; ++e) ks[m][n][e] = qs[m][n][e] = 0.f;
+            // K S, the state in two terms; the first one is kept for Q S (the output is rounded to bf16 too)
+            uint32_t sh[8][NT][2];
+    #pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                BTerms b[NT];
+    #pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    b[n] = b_terms(S[k][n]);
+                    sh[k][n][0] = b[n].h0;
+                    sh[k][n][1] = b[n].h1;
+                }
                 uint32_t a[4][4];
-#pragma unroll
-                for (int m = 0; m < 4; ++m) ldsm4t(a[m], kb + mh * 8192 + sw128_chunk(16 * k + tr, 2 * m + tc));
-#pragma unroll
+    #pragma unroll
                 for (int m = 0; m < 4; ++m)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) mma16(S[4 * mh + m][n], a[m], b[n].h0, b[n].h1);
-#pragma unroll
+                    ldsm4(a[m], kb + (k >> 2) * 8192 + sw128_chunk(16 * m + lr, 2 * (k & 3) + lc));
+    #pragma unroll
                 for (int m = 0; m < 4; ++m)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) mma16(S[4 * mh + m][n], a[m], b[n].l0, b[n].l1);
+    #pragma unroll
+                    for (int n = 0; n < NT; ++n) mma16(ks[m][n], a[m], b[n].h0, b[n].h1);
+    #pragma unroll
+                for (int m = 0; m < 4; ++m)
+    #pragma unroll
+                    for (int n = 0; n < NT; ++n) mma16(ks[m][n], a[m], b[n].l0, b[n].l1);
             }
-        }
-        // O = e^g Q S + P U
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) qs[m][n][e] *= eg[m][e >> 1];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            uint32_t b0[NT], b1[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                b0[n] = transpose8(pack_bf16(u[k][n][0], u[k][n][1]));
-                b1[n] = transpose8(pack_bf16(u[k][n][2], u[k][n][3]));
-            }
-#pragma unroll
-            for (int m = k; m < 4; ++m) {
-                uint32_t a[4];
-                ldsm4(a, ib + kImgP + sw128_chunk(16 * m + lr, 2 * k + lc));
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma16(qs[m][n], a, b0[n], b1[n]);
-            }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[s]);  // the warp has read all it takes of this stage
-        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + (t0 * Hv + h) * D + j0;
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int row = 16 * m + g + 8 * e;
-                if (row < Lc) {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        *reinterpret_cast<uint32_t*>(o + static_cast<int64_t>(row) * Hv * D + 8 * n) =
-                            pack_bf16(qs[m][n][2 * e], qs[m][n][2 * e + 1]);
+            // R = V - e^g K S; Q S runs beside it, a quarter for each 16 rows of R
+            float eg[4][2];
+            BTerms r[4][NT];
+    #pragma unroll
+            for (int k = 0; k < 4; ++k) {
+    #pragma unroll
+                for (int e = 0; e < 2; ++e) eg[k][e] = gs[16 * k + g + 8 * e];
+    #pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float x[4];
+    #pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int row = 16 * k + g + 8 * e;
+                        const uint32_t piece = static_cast<uint32_t>((wc + 8 * n) >> 3);  // 16 bytes: 8 columns
+                        uint32_t off;
+                        if constexpr (L::kVRow == 128) off = (piece >> 3) * (C * 128) + sw128_chunk(row, piece & 7);
+                        else off = row * 64 + (((piece ^ (row >> 1)) & 3) << 4);  // 64-byte rows
+                        const uint32_t vv = *reinterpret_cast<const uint32_t*>(st + L::V + off + 4 * t);
+                        x[2 * e] = fmaf(-eg[k][e], ks[k][n][2 * e], __uint_as_float(vv << 16));
+                        x[2 * e + 1] = fmaf(-eg[k][e], ks[k][n][2 * e + 1], __uint_as_float(vv & 0xffff0000u));
+                        if (row >= Lc) x[2 * e] = x[2 * e + 1] = 0.f;
+                    }
+                    r[k][n] = b_terms(x);
+                }
+    #pragma unroll
+                for (int kq = 2 * k; kq < 2 * k + 2; ++kq) {
+                    uint32_t a[4][4];
+    #pragma unroll
+                    for (int m = 0; m < 4; ++m)
+                        ldsm4(a[m], qb + (kq >> 2) * 8192 + sw128_chunk(16 * m + lr, 2 * (kq & 3) + lc));
+    #pragma unroll
+                    for (int m = 0; m < 4; ++m)
+    #pragma unroll
+                        for (int n = 0; n < NT; ++n) mma16(qs[m][n], a[m], sh[kq][n][0], sh[kq][n][1]);
                 }
             }
-    }
-    if (p.S_final && !*abort_s) {
-#pragma unroll
-        for (int m = 0; m < 8; ++m)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    *reinterpret_cast<float2*>(p.S_final + sbase + static_cast<size_t>(16 * m + g + 8 * e) * D + j0 +
-                                               8 * n) = make_float2(S[m][n][2 * e], S[m][n][2 * e + 1]);
+            // U = T R, both in two terms
+            float u[4][NT][4];
+    #pragma unroll
+            for (int m = 0; m < 4; ++m)
+    #pragma unroll
+                for (int n = 0; n < NT; ++n)
+    #pragma unroll
+                    for (int e = 0; e < 4; ++e) u[m][n][e] = 0.f;
+    #pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t ah[4][4], al[4][4];
+    #pragma unroll
+                for (int m = k; m < 4; ++m) {
+                    ldsm4(ah[m], ib + kImgTh + sw128_chunk(16 * m + lr, 2 * k + lc));
+                    ldsm4(al[m], ib + kImgTl + sw128_chunk(16 * m + lr, 2 * k + lc));
+                }
+    #pragma unroll
+                for (int m = k; m < 4; ++m)
+    #pragma unroll
+                    for (int n = 0; n < NT; ++n) mma16(u[m][n], ah[m], r[k][n].h0, r[k][n].h1);
+    #pragma unroll
+                for (int m = k; m < 4; ++m)
+    #pragma unroll
+                    for (int n = 0; n < NT; ++n) mma16(u[m][n], ah[m], r[k][n].l0, r[k][n].l1);
+    #pragma unroll
+                for (int m = k; m < 4; ++m)
+    #pragma unroll
+                    for (int n = 0; n < NT; ++n) mma16(u[m][n], al[m], r[k][n].h0, r[k][n].h1);
+            }
+            // S <- e^gC S + K^T (e^(gC - g) U), U in two terms
+            const float gc = gs[2 * C];
+    #pragma unroll
+            for (int m = 0; m < 8; ++m)
+    #pragma unroll
+                for (int n = 0; n < NT; ++n)
+    #pragma unroll
+                    for (int e = 0; e < 4; ++e) S[m][n][e] *= gc;
+    #pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float e0 = gs[C + 16 * k + g], e1 = gs[C + 16 * k + g + 8];
+                BTerms b[NT];
+    #pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float x[4] = {u[k][n][0] * e0, u[k][n][1] * e0, u[k][n][2] * e1, u[k][n][3] * e1};
+                    b[n] = b_terms(x);
+                }
+    #pragma unroll
+                for (int mh = 0; mh < 2; ++mh) {
+                    uint32_t a[4][4];
+    #pragma unroll
+                    for (int m = 0; m < 4; ++m) ldsm4t(a[m], kb + mh * 8192 + sw128_chunk(16 * k + tr, 2 * m + tc));
+    #pragma unroll
+                    for (int m = 0; m < 4; ++m)
+    #pragma unroll
+                        for (int n = 0; n < NT; ++n) mma16(S[4 * mh + m][n], a[m], b[n].h0, b[n].h1);
+    #pragma unroll
+                    for (int m = 0; m < 4; ++m)
+    #pragma unroll
+                        for (int n = 0; n < NT; ++n) mma16(S[4 * mh + m][n], a[m], b[n].l0, b[n].l1);
+                }
+            }
+            // O = e^g Q S + P U
+    #pragma unroll
+            for (int m = 0; m < 4; ++m)
+    #pragma unroll
+                for (int n = 0; n < NT; ++n)
+    #pragma unroll
+                    for (int e = 0; e < 4; ++e) qs[m][n][e] *= eg[m][e >> 1];
+    #pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t b0[NT], b1[NT];
+    #pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    b0[n] = transpose8(pack_bf16(u[k][n][0], u[k][n][1]));
+                    b1[n] = transpose8(pack_bf16(u[k][n][2], u[k][n][3]));
+                }
+    #pragma unroll
+                for (int m = k; m < 4; ++m) {
+                    uint32_t a[4];
+                    ldsm4(a, ib + kImgP + sw128_chunk(16 * m + lr, 2 * k + lc));
+    #pragma unroll
+                    for (int n = 0; n < NT; ++n) mma16(qs[m][n], a, b0[n], b1[n]);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[s]);  // the warp has read all it takes of this stage
+            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + (t0 * Hv + h) * D + j0;
+    #pragma unroll
+            for (int m = 0; m < 4; ++m)
+    #pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int row = 16 * m + g + 8 * e;
+                    if (row < Lc) {
+    #pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            *reinterpret_cast<uint32_t*>(o + static_cast<int64_t>(row) * Hv * D + 8 * n) =
+                                pack_bf16(qs[m][n][2 * e], qs[m][n][2 * e + 1]);
+                    }
+                }
+        }
+        if (p.S_final && !*abort_s) {
+    #pragma unroll
+            for (int m = 0; m < 8; ++m)
+    #pragma unroll
+                for (int n = 0; n < NT; ++n)
+    #pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        *reinterpret_cast<float2*>(p.S_final + sbase + static_cast<size_t>(16 * m + g + 8 * e) * D + j0 +
+                                                   8 * n) = make_float2(S[m][n][2 * e], S[m][n][2 * e + 1]);
+        }
     }
     __syncthreads();
-    if (tid == 0 && *abort_s) {
-        for (int c = max(0, issued - ST); c < issued; ++c)  // no copy is left in flight
-            (void)mbar_wait(&full[c % ST], (c / ST) & 1, kDrainLimit);
-        if (p.device_status) atomicOr(p.device_status, KDA_DEV_TIMEOUT);
-    }
+    if (tid == 0 && *abort_s && p.device_status) atomicOr(p.device_status, KDA_DEV_TIMEOUT);
 }
 
 template <typename K>
@@ -672,8 +743,11 @@ cudaError_t launch_gdn_chunked(const GdnArgs& a, const GdnLayout& lay, uint8_t* 
     static int configured[64];
     if (err == cudaSuccess) err = set_smem(kda_gdn_prep_kernel, PrepSmem::ALLOC, configured);
     if (err != cudaSuccess) return err;
-    const unsigned units = static_cast<unsigned>(lay.chunks * a.Hv);
-    kda_gdn_prep_kernel<<<units, kPrepThreads, PrepSmem::ALLOC, stream>>>(tm_q, tm_k, a, table, images, lay.chunks);
+    // the value heads of a group share a CTA's Gram matrices where that leaves a CTA for every SM
+    const int m = a.Hv / a.Hk;
+    const int hp = lay.chunks * a.Hk >= device_sm_count() ? m : 1;
+    kda_gdn_prep_kernel<<<static_cast<unsigned>(lay.chunks * (a.Hv / hp)), kPrepThreads, PrepSmem::ALLOC, stream>>>(
+        tm_q, tm_k, a, table, images, lay.chunks, hp);
     err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     const int32_t* ord = a.num_seqs > 1 ? order : nullptr;
