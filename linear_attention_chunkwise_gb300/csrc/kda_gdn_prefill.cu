@@ -389,11 +389,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
 template <int NT, int NW, int ST>
 struct ScanCfg {
     static constexpr int kCols = 8 * NT * NW;
-    // Four consumer warps leave each thread 255 registers beside the copying warp.  Eight do not (an SM
-    // quarter would hold three warps): they take a warpgroup of 128 for the copies, whose registers go to
-    // the consumers: launched with 168 a thread, 384 x 168 = 256 x 232 + 128 x 40.
-    static constexpr bool kSplit = NW == 8;
-    static constexpr int kThreads = kSplit ? 384 : 32 * (NW + 1);
+    static constexpr int kThreads = 32 * (NW + 1);
     static constexpr uint32_t kVRow = kCols >= 64 ? 128 : kCols * 2;  // bytes of a v row in a block
     static constexpr int kVBlocks = kCols >= 64 ? kCols / 64 : 1;
     static constexpr uint32_t K = 0, Q = 16384, IMG = 32768, V = IMG + 25600;
@@ -442,9 +438,8 @@ __global__ void __launch_bounds__(ScanCfg<NT, NW, ST>::kThreads, 1)
 
     // A warp of its own issues the copies (a thread is held for about 0.1 us by each): chunk c's tiles go into
     // stage c mod ST once every reader is done with chunk c - ST.
-    if (warp >= NW) {
-        if constexpr (L::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        if (warp == NW && lane == 0) {
+    if (warp == NW) {
+        if (lane == 0) {
             const int hk = h / (Hv / p.Hk);
             int c = 0;
             for (; c < nch && !*abort_s; ++c) {
@@ -469,7 +464,6 @@ __global__ void __launch_bounds__(ScanCfg<NT, NW, ST>::kThreads, 1)
                 (void)mbar_wait(&full[d % ST], (d / ST) & 1, kDrainLimit);
         }
     } else {
-        if constexpr (L::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         const int g = lane >> 2, t = lane & 3;
         const int wc = 8 * NT * warp;                  // the warp's first column in the CTA's
         const int j0 = slice * L::kCols + wc + 2 * t;  // this thread's first state column
@@ -753,7 +747,7 @@ cudaError_t launch_gdn_chunked(const GdnArgs& a, const GdnLayout& lay, uint8_t* 
     const int32_t* ord = a.num_seqs > 1 ? order : nullptr;
     if (static_cast<int64_t>(a.num_seqs) * a.Hv * 4 <= device_sm_count())
         return launch_scan<1, 4, 3>(tm_q, tm_k, a, table, ord, images, lay.chunks, stream);
-    return launch_scan<2, 8, 2>(tm_q, tm_k, a, table, ord, images, lay.chunks, stream);
+    return launch_scan<2, 4, 3>(tm_q, tm_k, a, table, ord, images, lay.chunks, stream);
 }
 
 }  // namespace kda
