@@ -484,6 +484,7 @@ KDA_API size_t kda_gdn_prefill_workspace_bytes(kda_dtype qkv_dtype, int32_t num_
  *   o          [total_tokens, Hv, dv]  qkv_dtype (out)
  *   S_final    [num_seqs, Hv, dk, dv]  fp32 (out), or NULL
  *   workspace  >= kda_gdn_prefill_workspace_bytes(...), else KDA_ERR_WORKSPACE
+ *              (bf16: about 0.4 KB per token and value head)
  *
  * Sequences, start and final states, aliasing (S_final may be S0 exactly, no
  * other overlap) and errors are those of kda_prefill.  A malformed cu_seqlens
@@ -495,6 +496,43 @@ KDA_API kda_status kda_gdn_prefill(const void *q, const void *k, const void *v, 
                                    const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens, int32_t Hk,
                                    int32_t Hv, int32_t dk, int32_t dv, void *o, float *S_final, void *workspace,
                                    size_t workspace_bytes, int32_t *device_status, kda_stream_t stream);
+
+/*
+ * kda_gdn_prefill_backward -- reverse-mode gradient of kda_gdn_prefill for
+ *     L = sum_{t,h,j} o[t,h,j] grad_o[t,h,j] + sum_{n,h,i,j} S_final grad_S_final.
+ *
+ *   q, k, v, log_decay, beta, S0, cu_seqlens, num_seqs, total_tokens, Hk, Hv,
+ *   dk, dv        the forward's inputs (S0 may be NULL = zeros)
+ *   grad_o        [total_tokens, Hv, dv] qkv_dtype, device (dL/do)
+ *   grad_S_final  [num_seqs, Hv, dk, dv] fp32 device, or NULL (zeros)
+ *   grad_q, grad_k  [total_tokens, Hk, dk] qkv_dtype out: the value heads of a
+ *                   group are added in fp32 and rounded once
+ *   grad_v        [total_tokens, Hv, dv] qkv_dtype out
+ *   grad_log_decay, grad_beta  [total_tokens, Hv] fp32 out
+ *   grad_S0       [num_seqs, Hv, dk, dv] fp32 out, or NULL (not computed)
+ *
+ * qkv_dtype is KDA_DTYPE_BF16 (else KDA_ERR_UNSUPPORTED).  The call reruns the
+ * chunkwise forward, keeping the state before every 64-token chunk, walks the
+ * state's adjoint back over the chunks, and forms everything else per chunk.
+ * The fp32 gradients are accurate as S_final is; results are bitwise
+ * repeatable.  The gradient of a log_decay at which the decay is 0 in fp32 is 0.
+ *
+ * Workspace: >= kda_gdn_prefill_backward_workspace_bytes(...) device bytes
+ * (about 3.6 KB per token and value head), 256-byte aligned.  q, k, v, grad_o,
+ * states and their gradients are 16-byte aligned, the others 4.  The outputs
+ * overlap nothing (KDA_ERR_INVALID_ARG).  A malformed cu_seqlens sets
+ * KDA_DEV_BAD_CU_SEQLENS and leaves the gradients unspecified.
+ */
+KDA_API size_t kda_gdn_prefill_backward_workspace_bytes(kda_dtype qkv_dtype, int32_t num_seqs, int64_t total_tokens,
+                                                        int32_t Hk, int32_t Hv, int32_t dk, int32_t dv);
+KDA_API kda_status kda_gdn_prefill_backward(const void *q, const void *k, const void *v, kda_dtype qkv_dtype,
+                                            const float *log_decay, const float *beta, const float *S0,
+                                            const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                                            int32_t Hk, int32_t Hv, int32_t dk, int32_t dv, const void *grad_o,
+                                            const float *grad_S_final, void *grad_q, void *grad_k, void *grad_v,
+                                            float *grad_log_decay, float *grad_beta, float *grad_S0,
+                                            void *workspace, size_t workspace_bytes, int32_t *device_status,
+                                            kda_stream_t stream);
 
 /*
  * kda_gdn_decode_step -- one token of the gated delta rule for N sequences;

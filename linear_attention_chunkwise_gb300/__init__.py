@@ -5,7 +5,8 @@ Python names mirror the C ABI in include/kda.h:
   kda_prefill_backward_gated, kda_decode_step, kda_decode_step_ex, kda_decode_multi, kda_decode_multi_ex,
   kda_prefill_workspace_bytes, kda_prefill_backward_workspace_bytes,
   kda_prefill_backward_ex_workspace_bytes, kda_prefill_backward_gated_workspace_bytes, kda_status_string;
-  the gated delta rule: kda_gdn_prefill, kda_gdn_decode_step, kda_gdn_prefill_workspace_bytes;
+  the gated delta rule: kda_gdn_prefill, kda_gdn_prefill_backward, kda_gdn_decode_step,
+  kda_gdn_prefill_workspace_bytes, kda_gdn_prefill_backward_workspace_bytes;
   the norm in front of a layer: kda_rms_norm, kda_rms_norm_backward, kda_rms_norm_backward_workspace_bytes.
 The library must be built first (``__graft_entry__.build()`` or
 ``python -m linear_attention_chunkwise_gb300._build``); there is no fallback.
@@ -54,6 +55,8 @@ from ._binding import (  # noqa: F401
 from ._gdn import (  # noqa: F401
     kda_gdn_decode_step,
     kda_gdn_prefill,
+    kda_gdn_prefill_backward,
+    kda_gdn_prefill_backward_workspace_bytes,
     kda_gdn_prefill_workspace_bytes,
     kda_rms_norm,
     kda_rms_norm_backward,

@@ -68,7 +68,8 @@ EXPORTED_SYMBOLS = ("kda_abi_version", "kda_status_string", "kda_prefill_workspa
                     "kda_decode_multi_ex", "kda_prefill_backward_workspace_bytes", "kda_prefill_backward",
                     "kda_prefill_backward_ex_workspace_bytes", "kda_prefill_backward_ex",
                     "kda_prefill_backward_gated_workspace_bytes", "kda_prefill_backward_gated",
-                    "kda_gdn_prefill_workspace_bytes", "kda_gdn_prefill", "kda_gdn_decode_step", "kda_rms_norm",
+                    "kda_gdn_prefill_workspace_bytes", "kda_gdn_prefill", "kda_gdn_prefill_backward_workspace_bytes",
+                    "kda_gdn_prefill_backward", "kda_gdn_decode_step", "kda_rms_norm",
                     "kda_rms_norm_backward_workspace_bytes", "kda_rms_norm_backward")
 
 _lock = threading.Lock()
@@ -141,6 +142,9 @@ def load_library(path: str | None = None):
         for name, res, args in (
                 ("kda_gdn_prefill_workspace_bytes", sz, [E, i32, i64, i32, i32, i32, i32]),
                 ("kda_gdn_prefill", E, [P, P, P, E, P, P, P, P, i32, i64, i32, i32, i32, i32, P, P, P, sz, P, P]),
+                ("kda_gdn_prefill_backward_workspace_bytes", sz, [E, i32, i64, i32, i32, i32, i32]),
+                ("kda_gdn_prefill_backward", E, [P, P, P, E, P, P, P, P, i32, i64, i32, i32, i32, i32, P, P, P, P, P, P,
+                                                 P, P, P, sz, P, P]),
                 ("kda_gdn_decode_step", E, [P, P, P, E, P, P, P, i32, P, i32, i32, i32, i32, i32, P, P, P]),
                 ("kda_rms_norm", E, [P, P, E, P, F, i64, i32, E, i32, P, P, P, P]),
                 ("kda_rms_norm_backward_workspace_bytes", sz, [i64, i32]),

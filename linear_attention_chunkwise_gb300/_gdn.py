@@ -129,6 +129,68 @@ def kda_gdn_prefill(q, k, v, log_decay, beta, cu_seqlens, S0=None, *, o=None, S_
     return o, S_final
 
 
+def kda_gdn_prefill_backward_workspace_bytes(qkv_dtype, num_seqs: int, total_tokens: int, Hk: int, Hv: int,
+                                             dk: int = 128, dv: int = 128) -> int:
+    code = qkv_dtype if isinstance(qkv_dtype, int) else _b._dtype_code(qkv_dtype)
+    return int(_b.load_library().kda_gdn_prefill_backward_workspace_bytes(code, int(num_seqs), int(total_tokens),
+                                                                          int(Hk), int(Hv), int(dk), int(dv)))
+
+
+def kda_gdn_prefill_backward(q, k, v, log_decay, beta, cu_seqlens, grad_o, S0=None, grad_S_final=None, *,
+                             need_grad_S0=True, grads=None, workspace=None, device_status=None, stream=None):
+    """Gradient of kda_gdn_prefill for L = <o, grad_o> + <S_final, grad_S_final> (see include/kda.h; bf16).
+
+    grad_o: [T, Hv, 128] in the dtype of q; grad_S_final: fp32 [N, Hv, 128, 128] or None (zeros).
+    Returns (grad_q, grad_k, grad_v, grad_log_decay, grad_beta, grad_S0): the first three in the dtype of q,
+    the others fp32; grad_S0 is None when need_grad_S0 is False.  `grads` may pass those six tensors in.
+    """
+    lib = _b.load_library()
+    dev, code = _first(q, "q", 3)
+    T = q.shape[0]
+    Hk, Hv, dk, dv = _heads(q, v, "[T, Hv, 128]")
+    f32 = torch.float32
+    _check(q, "q", q.dtype, (T, Hk, dk), dev)
+    _check(k, "k", q.dtype, (T, Hk, dk), dev)
+    _check(v, "v", q.dtype, (T, Hv, dv), dev)
+    _check(grad_o, "grad_o", q.dtype, (T, Hv, dv), dev)
+    _check(log_decay, "log_decay", f32, (T, Hv), dev)
+    _check(beta, "beta", f32, (T, Hv), dev)
+    N = cu_seqlens.numel() - 1
+    if N < 0:
+        raise ValueError("cu_seqlens must have at least one entry")
+    _check(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev)
+    state = (N, Hv, dk, dv)
+    for x, name in ((S0, "S0"), (grad_S_final, "grad_S_final")):
+        if x is not None:
+            _check(x, name, f32, state, dev)
+    specs = (("grad_q", q.dtype, (T, Hk, dk)), ("grad_k", q.dtype, (T, Hk, dk)), ("grad_v", q.dtype, (T, Hv, dv)),
+             ("grad_log_decay", f32, (T, Hv)), ("grad_beta", f32, (T, Hv)), ("grad_S0", f32, state))
+    mine = []
+    if grads is None:
+        grads = tuple(torch.empty(shape, dtype=dt, device=dev) if n != "grad_S0" or need_grad_S0 else None
+                      for n, dt, shape in specs)
+        mine.extend(grads)
+    elif len(grads) != 6:
+        raise ValueError("grads must hold 6 tensors")
+    else:
+        for x, (n, dt, shape) in zip(grads, specs):
+            if x is not None or n != "grad_S0":
+                _check(x, n, dt, shape, dev)
+    if workspace is None:
+        need = lib.kda_gdn_prefill_backward_workspace_bytes(code, N, T, Hk, Hv, dk, dv)
+        mine.append(workspace := torch.empty(max(need, 256), dtype=torch.uint8, device=dev))
+    else:
+        _b._check(workspace, "workspace", torch.uint8, dev)
+    _b._check(device_status, "device_status", torch.int32, dev)
+    with _on(dev):
+        _done("kda_gdn_prefill_backward", lib.kda_gdn_prefill_backward(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), code, log_decay.data_ptr(), beta.data_ptr(), _p(S0),
+            cu_seqlens.data_ptr(), N, T, Hk, Hv, dk, dv, grad_o.data_ptr(), _p(grad_S_final),
+            *(_p(x) for x in grads), workspace.data_ptr(), workspace.numel(), _p(device_status),
+            _stream(stream, dev, *mine)))
+    return tuple(grads)
+
+
 def kda_gdn_decode_step(q, k, v, log_decay, beta, S, state_indices=None, *, o=None, device_status=None,
                         stream=None):
     """One token of the gated delta rule; S [slots, Hv, 128, 128] fp32 is updated in place.

@@ -25,7 +25,7 @@ kda_status gdn_shape(kda_dtype t, int64_t rows, int32_t states, int32_t Hk, int3
     if (t != KDA_DTYPE_BF16 && t != KDA_DTYPE_F32) return KDA_ERR_UNSUPPORTED;
     if (rows < 0 || states < 0 || Hk <= 0 || Hv <= 0 || rows > INT32_MAX - 64) return KDA_ERR_INVALID_ARG;
     if (dk != kHeadDim || dv != kHeadDim) return KDA_ERR_UNSUPPORTED;
-    if (Hv % Hk != 0) return KDA_ERR_INVALID_ARG;
+    if (Hv % Hk != 0 || (states == 0 && rows > 0)) return KDA_ERR_INVALID_ARG;
     // a launch has one grid dimension: 8 blocks for every (sequence, value head), one for every chunk's
     if (!sizes_ok(rows, Hv, kHeadDim, 4) || !sizes_ok(states, Hv, kStateBytes, 1) ||
         static_cast<double>(states) * Hv * 8.0 > 2147483647.0 ||
@@ -47,7 +47,7 @@ size_t kda_gdn_prefill_workspace_bytes(kda_dtype qkv_dtype, int32_t num_seqs, in
                                        int32_t Hv, int32_t dk, int32_t dv) {
     if (gdn_shape(qkv_dtype, total_tokens, num_seqs, Hk, Hv, dk, dv) != KDA_OK) return 0;
     if (!chunked(qkv_dtype, num_seqs, total_tokens)) return kAlign;
-    return kda::gdn_layout(num_seqs, total_tokens, Hv).total;
+    return kda::gdn_workspace(num_seqs, total_tokens, Hv, false, nullptr, nullptr);
 }
 
 kda_status kda_gdn_prefill(const void* q, const void* k, const void* v, kda_dtype qkv_dtype, const float* log_decay,
@@ -103,10 +103,108 @@ kda_status kda_gdn_prefill(const void* q, const void* k, const void* v, kda_dtyp
     a.Hk = Hk;
     a.Hv = Hv;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t err =
-        chunked(qkv_dtype, num_seqs, total_tokens)
-            ? kda::launch_gdn_chunked(a, kda::gdn_layout(num_seqs, total_tokens, Hv), static_cast<uint8_t*>(workspace), s)
-            : kda::launch_gdn_recurrent(qkv_dtype == KDA_DTYPE_F32, a, s);
+    cudaError_t err = cudaSuccess;
+    if (chunked(qkv_dtype, num_seqs, total_tokens)) {
+        kda::GdnWorkspace w;
+        kda::gdn_workspace(num_seqs, total_tokens, Hv, false, static_cast<uint8_t*>(workspace), &w);
+        err = kda::launch_gdn_tables(a, w, s);
+        if (err == cudaSuccess) err = kda::launch_gdn_prep(a, w, s);
+        if (err == cudaSuccess) err = kda::launch_gdn_scan(a, w, s);
+    } else {
+        err = kda::launch_gdn_recurrent(qkv_dtype == KDA_DTYPE_F32, a, s);
+    }
+    return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+size_t kda_gdn_prefill_backward_workspace_bytes(kda_dtype qkv_dtype, int32_t num_seqs, int64_t total_tokens, int32_t Hk,
+                                                int32_t Hv, int32_t dk, int32_t dv) {
+    if (qkv_dtype != KDA_DTYPE_BF16 || gdn_shape(qkv_dtype, total_tokens, num_seqs, Hk, Hv, dk, dv) != KDA_OK) return 0;
+    return kda::gdn_workspace(num_seqs, total_tokens, Hv, true, nullptr, nullptr);
+}
+
+kda_status kda_gdn_prefill_backward(const void* q, const void* k, const void* v, kda_dtype qkv_dtype,
+                                    const float* log_decay, const float* beta, const float* S0,
+                                    const int32_t* cu_seqlens, int32_t num_seqs, int64_t total_tokens, int32_t Hk,
+                                    int32_t Hv, int32_t dk, int32_t dv, const void* grad_o,
+                                    const float* grad_S_final, void* grad_q, void* grad_k, void* grad_v,
+                                    float* grad_log_decay, float* grad_beta, float* grad_S0, void* workspace,
+                                    size_t workspace_bytes, int32_t* device_status, kda_stream_t stream) {
+    const kda_status shape = gdn_shape(qkv_dtype, total_tokens, num_seqs, Hk, Hv, dk, dv);
+    if (shape != KDA_OK) return shape;
+    if (qkv_dtype != KDA_DTYPE_BF16) return KDA_ERR_UNSUPPORTED;
+    if (!cu_seqlens || !workspace) return KDA_ERR_INVALID_ARG;
+    const bool have_tokens = total_tokens > 0;
+    if (have_tokens && (!q || !k || !v || !log_decay || !beta || !grad_o || !grad_q || !grad_k || !grad_v ||
+                        !grad_log_decay || !grad_beta))
+        return KDA_ERR_INVALID_ARG;
+    for (const void* x : {q, k, v, grad_o, static_cast<const void*>(grad_q), static_cast<const void*>(grad_k),
+                          static_cast<const void*>(grad_v), static_cast<const void*>(S0),
+                          static_cast<const void*>(grad_S_final), static_cast<const void*>(grad_S0)})
+        if (!aligned(x, 16)) return KDA_ERR_INVALID_ARG;
+    for (const void* x : {static_cast<const void*>(log_decay), static_cast<const void*>(beta),
+                          static_cast<const void*>(grad_log_decay), static_cast<const void*>(grad_beta),
+                          static_cast<const void*>(cu_seqlens), static_cast<const void*>(device_status)})
+        if (!aligned(x, 4)) return KDA_ERR_INVALID_ARG;
+    if (!aligned(workspace, kAlign)) return KDA_ERR_INVALID_ARG;
+    const size_t need = kda_gdn_prefill_backward_workspace_bytes(qkv_dtype, num_seqs, total_tokens, Hk, Hv, dk, dv);
+    if (workspace_bytes < need) return KDA_ERR_WORKSPACE;
+
+    // the outputs (and the workspace) overlap nothing
+    const size_t T = static_cast<size_t>(total_tokens), nqk = T * Hk * kHeadDim * 2, nv = T * Hv * kHeadDim * 2;
+    const size_t nst = static_cast<size_t>(num_seqs) * Hv * kStateBytes;
+    const Range outs[] = {range_of(grad_q, nqk),
+                          range_of(grad_k, nqk),
+                          range_of(grad_v, nv),
+                          range_of(grad_log_decay, T * Hv * 4),
+                          range_of(grad_beta, T * Hv * 4),
+                          range_of(grad_S0, grad_S0 ? nst : 0),
+                          range_of(workspace, need),
+                          range_of(device_status, device_status ? 4 : 0)};
+    const Range ins[] = {range_of(q, nqk), range_of(k, nqk), range_of(v, nv), range_of(grad_o, nv),
+                         range_of(log_decay, T * Hv * 4), range_of(beta, T * Hv * 4), range_of(S0, S0 ? nst : 0),
+                         range_of(grad_S_final, grad_S_final ? nst : 0),
+                         range_of(cu_seqlens, (static_cast<size_t>(num_seqs) + 1) * 4)};
+    constexpr int n_outs = sizeof(outs) / sizeof(outs[0]);
+    for (int i = 0; i < n_outs; ++i) {
+        for (int j = i + 1; j < n_outs; ++j)
+            if (overlap(outs[i], outs[j])) return KDA_ERR_INVALID_ARG;
+        for (const Range& in : ins)
+            if (overlap(outs[i], in)) return KDA_ERR_INVALID_ARG;
+    }
+    const kda_status dev = kda::device_check();
+    if (dev != KDA_OK) return dev;
+    if (num_seqs == 0) return KDA_OK;
+
+    kda::GdnArgs a;
+    // tensor maps want a valid base even when there are no tokens (never read then)
+    a.q = have_tokens ? q : workspace;
+    a.k = have_tokens ? k : workspace;
+    a.v = have_tokens ? v : workspace;
+    a.log_decay = log_decay;
+    a.beta = beta;
+    a.S0 = S0;
+    a.cu_seqlens = cu_seqlens;
+    a.device_status = device_status;
+    a.total_tokens = total_tokens;
+    a.num_seqs = num_seqs;
+    a.Hk = Hk;
+    a.Hv = Hv;
+    kda::GdnBackwardArgs b;
+    b.grad_o = have_tokens ? grad_o : workspace;
+    b.grad_S_final = grad_S_final;
+    b.grad_q = grad_q;
+    b.grad_k = grad_k;
+    b.grad_v = grad_v;
+    b.grad_log_decay = grad_log_decay;
+    b.grad_beta = grad_beta;
+    b.grad_S0 = grad_S0;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    kda::GdnWorkspace w;
+    kda::gdn_workspace(num_seqs, total_tokens, Hv, true, static_cast<uint8_t*>(workspace), &w);
+    cudaError_t err = kda::launch_gdn_tables(a, w, s);
+    if (err == cudaSuccess) err = kda::launch_gdn_prep(a, w, s);
+    if (err == cudaSuccess) err = kda::launch_gdn_scan(a, w, s);
+    if (err == cudaSuccess) err = kda::launch_gdn_backward(a, b, w, s);
     return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

@@ -1,0 +1,796 @@
+// kda_gdn_backward.cu -- gradient of the gated delta rule's chunkwise prefill (bf16 inputs).
+//
+// For L = <o, dO> + <S_final, dS_final>, with a chunk's quantities of kda_gdn_prefill.cu (g, G, A, T, P, U,
+// start state S) and X the adjoint of the state at its end, e_i = exp(gC - g_i), b = beta:
+//   dU = P^T dO + Diag(e) K X,   W = T^T dU,   dv = b W,
+//   adjoint of the start state = e^gC X + K^T (-Diag(e^g b) W) + Q^T (Diag(e^g) dO)
+//   dP = dO U^T, dA = -W U^T (below the diagonal), M = G dP, E = b G dA
+//   dq = Diag(e^g) dO S^T + M K
+//   dk = -Diag(e^g b) W S^T + Diag(e) U X^T + M^T Q + (E + E^T) K
+//   db_i = (W_i . U_i) / b_i      (U_i / b_i are the rows that b multiplies)
+// log_decay_t scales what passes from before token t to it or later: the pairs i >= t > j, the start state
+// as tokens from t on read it, what tokens before t leave in the end state, and the start state there:
+//   gradient of log_decay_t = sum_{i >= t > j} (dP P + dA A)_ij + sum_{i >= t} a_i + sum_{j < t} w_j + e^gC <X, S>,
+//   a_i = q_i . (e^g dO S^T)_i - k_i . (e^g b W S^T)_i,   w_j = k_j . (e U X^T)_j.
+// (As the sums, from t on, of one gradient for each g_i it would need a difference of large sums; here a
+// decay of 0 gives exactly 0.)
+//
+// Kernels: the prefill's prep and its walk over the chunks (leaving S and U), a walk back (leaving X and
+// W, writing dv and the start state's gradient), and one CTA per (chunk, q/k head) for the rest, which adds
+// up the value heads of a group in its registers.  Operands that are not raw bf16 inputs are two bf16 terms
+// wherever the result is kept in fp32 (states, decays, b); M and E, which only reach the bf16 dq and dk,
+// are one.
+#include "kda_gdn_common.cuh"
+
+namespace kda {
+namespace {
+
+using namespace gdn;
+
+// =========================================================== walk back ==
+template <int NT, int ST>
+struct BackCfg {
+    static constexpr int kWarps = 4;
+    static constexpr int kCols = 8 * NT * kWarps;
+    static constexpr int kThreads = 32 * (kWarps + 1);
+    static constexpr uint32_t kVRow = 2 * kCols;  // bytes of a dO row
+    static constexpr uint32_t K = 0, Q = 16384, IMG = 32768, V = IMG + 34816;
+    static constexpr uint32_t STAGE = V + C * kVRow;
+    static constexpr uint32_t BARS = ST * STAGE;  // full[ST], empty[ST]
+    static constexpr uint32_t ABORT = BARS + 16 * ST;
+    static constexpr uint32_t ALLOC = ABORT + 16 + 1024;
+    static_assert(kVRow == 64 || kVRow == 128, "swizzled rows");
+    static_assert(STAGE % 1024 == 0 && ALLOC <= 232448 && kImgStrideBwd <= 34816, "stages");
+};
+
+template <int NT, int ST>
+__global__ void __launch_bounds__(BackCfg<NT, ST>::kThreads, 1)
+    kda_gdn_walk_back_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                             const __grid_constant__ CUtensorMap tm_do, const GdnArgs p, const GdnBackwardArgs gr,
+                             const int32_t* __restrict__ co, const int32_t* __restrict__ order,
+                             const uint8_t* __restrict__ images, int64_t chunk_slots, uint8_t* records) {
+    using L = BackCfg<NT, ST>;
+    constexpr int NW = L::kWarps;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int N = p.num_seqs, Hv = p.Hv;
+    constexpr int NSL = D / L::kCols;
+    const int slice = blockIdx.x % NSL;
+    const int h = (blockIdx.x / NSL) % Hv;
+    const int pos = blockIdx.x / (NSL * Hv);
+    if (co[N + 1] == 0) return;
+    const int seq = order ? order[pos] : pos;
+    const int nch = co[seq + 1] - co[seq], jb = co[seq];
+    const int64_t t_begin = p.cu_seqlens[seq], t_end = p.cu_seqlens[seq + 1];
+    if (!KDA_BOUNDS(seq >= 0 && seq < N && h < Hv && t_begin >= 0 && t_end <= p.total_tokens && jb >= 0 &&
+                        static_cast<int64_t>(jb) + nch <= chunk_slots &&
+                        static_cast<int64_t>(nch) * C >= t_end - t_begin,
+                    p.device_status))
+        return;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::BARS);
+    uint64_t* empty = full + ST;
+    volatile int* abort_s = reinterpret_cast<volatile int*>(sm + L::ABORT);
+    if (tid == 0) {
+        *abort_s = 0;
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], NW);
+        }
+        fence_mbar_init();
+    }
+    __syncthreads();
+
+    if (warp == NW) {  // the copies: step i takes chunk nch - 1 - i, into stage i mod ST
+        if (lane == 0) {
+            const int hk = h / (Hv / p.Hk);
+            int i = 0;
+            for (; i < nch && !*abort_s; ++i) {
+                const int s = i % ST, c = nch - 1 - i;
+                if (i >= ST && !mbar_wait_pipe(&empty[s], ((i / ST) - 1) & 1)) {
+                    *abort_s = 1;
+                    break;
+                }
+                uint8_t* st = sm + s * L::STAGE;
+                const int32_t tok = static_cast<int32_t>(t_begin + static_cast<int64_t>(c) * C);
+                mbar_arrive_expect_tx(&full[s], 32768 + static_cast<uint32_t>(kImgStrideBwd) + C * L::kVRow);
+#pragma unroll
+                for (int kh = 0; kh < 2; ++kh) tma_load_3d(st + L::K + kh * 8192, &tm_k, &full[s], 64 * kh, hk, tok);
+                tma_load_3d(st + L::V, &tm_do, &full[s], slice * L::kCols, h, tok);
+                bulk_g2s(st + L::IMG, images + (static_cast<size_t>(jb + c) * Hv + h) * kImgStrideBwd,
+                         static_cast<uint32_t>(kImgStrideBwd), &full[s]);
+#pragma unroll
+                for (int kh = 0; kh < 2; ++kh) tma_load_3d(st + L::Q + kh * 8192, &tm_q, &full[s], 64 * kh, hk, tok);
+            }
+            for (int d = max(0, i - ST); d < i; ++d)  // no copy is left in flight
+                (void)mbar_wait(&full[d % ST], (d / ST) & 1, kDrainLimit);
+        }
+    } else {
+        const int g = lane >> 2, t = lane & 3;
+        const int wc = 8 * NT * warp;               // the warp's first column in the CTA's
+        const int col = slice * L::kCols + wc + 2 * t;  // this thread's first column
+        const size_t sbase = (static_cast<size_t>(seq) * Hv + h) * D * D;
+        float X[8][NT][4];  // rows 16 m + g (+ 8), columns col + 8 n (+ 1)
+#pragma unroll
+        for (int m = 0; m < 8; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const size_t off = sbase + static_cast<size_t>(16 * m + g + 8 * e) * D + col + 8 * n;
+                    const float2 x =
+                        gr.grad_S_final ? *reinterpret_cast<const float2*>(gr.grad_S_final + off) : make_float2(0.f, 0.f);
+                    X[m][n][2 * e] = x.x;
+                    X[m][n][2 * e + 1] = x.y;
+                }
+        // ldmatrix addresses: rows of tokens, and transposed [channels or columns][tokens] blocks
+        const int lr = lane & 15, lc = lane >> 4;
+        const int tr = (lane & 7) + ((lane >> 4) << 3), tc = (lane >> 3) & 1;
+        for (int i = 0; i < nch; ++i) {
+            const int s = i % ST, c = nch - 1 - i;
+            uint8_t* st = sm + s * L::STAGE;
+            const bool landed = !*abort_s && mbar_wait_pipe(&full[s], (i / ST) & 1);
+            if (!__all_sync(0xffffffffu, landed)) {  // a bounded wait expired, here or elsewhere
+                *abort_s = 1;
+                break;
+            }
+            const int64_t t0 = t_begin + static_cast<int64_t>(c) * C;
+            const int Lc = static_cast<int>(t_end - t0 < C ? t_end - t0 : C);
+            if (Lc < C) {  // rows behind the sequence's end: no tokens (every warp clears all it reads)
+                const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+                for (int e = lane; e < (C - Lc) * 16; e += 32) {
+                    const uint32_t off = (e & 1) * 8192 + sw128_chunk(Lc + (e >> 4), (e >> 1) & 7);
+                    *reinterpret_cast<uint4*>(st + L::K + off) = z;
+                    *reinterpret_cast<uint4*>(st + L::Q + off) = z;
+                }
+                for (uint32_t e = Lc * L::kVRow + 16 * lane; e < C * L::kVRow; e += 512)
+                    *reinterpret_cast<uint4*>(st + L::V + e) = z;
+                __syncwarp();
+            }
+            const uint32_t kb = smem_u32(st + L::K), qb = smem_u32(st + L::Q), ib = smem_u32(st + L::IMG);
+            const float* gs = reinterpret_cast<const float*>(st + L::IMG + kImgG);
+            uint8_t* const rec = records + (static_cast<size_t>(jb + c) * Hv + h) * kRecStride;
+            // K X
+            float u[4][NT][4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) u[m][n][e] = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                BTerms b[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    put_record(X[k][n], rec + kRecX, 16384, 32768, 16 * k + g, col + 8 * n);
+                    b[n] = b_terms(X[k][n]);
+                }
+                uint32_t a[4][4];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) ldsm4(a[m], kb + (k >> 2) * 8192 + sw128_chunk(16 * m + lr, 2 * (k & 3) + lc));
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma16(u[m][n], a[m], b[n].h0, b[n].h1);
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma16(u[m][n], a[m], b[n].l0, b[n].l1);
+            }
+            // dO as B operand: [k][n] registers of tokens 16 k + 2 t (+ 1) and 16 k + 8 + 2 t (+ 1)
+            uint32_t dob[4][NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int row = 32 * hf + lane, piece = (wc >> 3) + n;
+                    uint32_t off;
+                    if constexpr (L::kVRow == 128) off = sw128_chunk(row, piece);
+                    else off = row * 64 + (((piece ^ (row >> 1)) & 3) << 4);  // 64-byte rows
+                    uint32_t f[4];
+                    ldsm4t(f, smem_u32(st + L::V) + off);
+                    dob[2 * hf][n][0] = f[0];
+                    dob[2 * hf][n][1] = f[1];
+                    dob[2 * hf + 1][n][0] = f[2];
+                    dob[2 * hf + 1][n][1] = f[3];
+                }
+            // dU = e K X + P^T dO, P in two terms (block rows k of P from the diagonal down)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const float e0 = gs[kVecEo + 16 * m + g], e1 = gs[kVecEo + 16 * m + g + 8];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    u[m][n][0] *= e0;
+                    u[m][n][1] *= e0;
+                    u[m][n][2] *= e1;
+                    u[m][n][3] *= e1;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t ah[4][4], al[4][4];
+#pragma unroll
+                for (int m = 0; m <= k; ++m) {
+                    ldsm4t(ah[m], ib + kImgP + sw128_chunk(16 * k + tr, 2 * m + tc));
+                    ldsm4t(al[m], ib + kImgPl + sw128_chunk(16 * k + tr, 2 * m + tc));
+                }
+#pragma unroll
+                for (int m = 0; m <= k; ++m)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma16(u[m][n], ah[m], dob[k][n][0], dob[k][n][1]);
+#pragma unroll
+                for (int m = 0; m <= k; ++m)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma16(u[m][n], al[m], dob[k][n][0], dob[k][n][1]);
+            }
+            // W = T^T dU, both in two terms
+            float w[4][NT][4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[m][n][e] = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                BTerms b[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) b[n] = b_terms(u[k][n]);
+                uint32_t ah[4][4], al[4][4];
+#pragma unroll
+                for (int m = 0; m <= k; ++m) {
+                    ldsm4t(ah[m], ib + kImgTh + sw128_chunk(16 * k + tr, 2 * m + tc));
+                    ldsm4t(al[m], ib + kImgTl + sw128_chunk(16 * k + tr, 2 * m + tc));
+                }
+#pragma unroll
+                for (int m = 0; m <= k; ++m)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma16(w[m][n], ah[m], b[n].h0, b[n].h1);
+#pragma unroll
+                for (int m = 0; m <= k; ++m)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma16(w[m][n], ah[m], b[n].l0, b[n].l1);
+#pragma unroll
+                for (int m = 0; m <= k; ++m)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma16(w[m][n], al[m], b[n].h0, b[n].h1);
+            }
+            // X <- e^gC X + K^T (-e^g b W) + Q^T (e^g dO)
+            const float gc = gs[kVecEc];
+#pragma unroll
+            for (int m = 0; m < 8; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) X[m][n][e] *= gc;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r0 = 16 * k + g;
+                const float z0 = -gs[kVecEg + r0] * gs[kVecB + r0], z1 = -gs[kVecEg + r0 + 8] * gs[kVecB + r0 + 8];
+                const float2 ga = *reinterpret_cast<const float2*>(gs + kVecEg + 16 * k + 2 * t);
+                const float2 gb = *reinterpret_cast<const float2*>(gs + kVecEg + 16 * k + 8 + 2 * t);
+                BTerms b[NT], d[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float x[4] = {w[k][n][0] * z0, w[k][n][1] * z0, w[k][n][2] * z1, w[k][n][3] * z1};
+                    b[n] = b_terms(x);
+                    const float2 y0 = unpack_bf16(dob[k][n][0]), y1 = unpack_bf16(dob[k][n][1]);
+                    split2(y0.x * ga.x, y0.y * ga.y, d[n].h0, d[n].l0);
+                    split2(y1.x * gb.x, y1.y * gb.y, d[n].h1, d[n].l1);
+                }
+#pragma unroll
+                for (int mh = 0; mh < 2; ++mh) {
+                    uint32_t a[4][4];
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) ldsm4t(a[m], kb + mh * 8192 + sw128_chunk(16 * k + tr, 2 * m + tc));
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma16(X[4 * mh + m][n], a[m], b[n].h0, b[n].h1);
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma16(X[4 * mh + m][n], a[m], b[n].l0, b[n].l1);
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) ldsm4t(a[m], qb + mh * 8192 + sw128_chunk(16 * k + tr, 2 * m + tc));
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma16(X[4 * mh + m][n], a[m], d[n].h0, d[n].h1);
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma16(X[4 * mh + m][n], a[m], d[n].l0, d[n].l1);
+                }
+            }
+            float bs[4][2];
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) bs[m][e] = gs[kVecB + 16 * m + g + 8 * e];
+            if (Lc < C) fence_async_smem();  // the cleared rows, before the stage's next copies
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[s]);  // the warp has read all it takes of this stage
+            __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(gr.grad_v) + (t0 * Hv + h) * D + col;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) put_record(w[m][n], rec + kRecW, 8192, 16384, 16 * m + g, col + 8 * n);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int row = 16 * m + g + 8 * e;
+                    if (row < Lc) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            *reinterpret_cast<uint32_t*>(dv + static_cast<int64_t>(row) * Hv * D + 8 * n) =
+                                pack_bf16(bs[m][e] * w[m][n][2 * e], bs[m][e] * w[m][n][2 * e + 1]);
+                    }
+                }
+            }
+        }
+        if (gr.grad_S0 && !*abort_s) {
+#pragma unroll
+            for (int m = 0; m < 8; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        *reinterpret_cast<float2*>(gr.grad_S0 + sbase + static_cast<size_t>(16 * m + g + 8 * e) * D + col +
+                                                   8 * n) = make_float2(X[m][n][2 * e], X[m][n][2 * e + 1]);
+        }
+    }
+    __syncthreads();
+    if (tid == 0 && *abort_s && p.device_status) atomicOr(p.device_status, KDA_DEV_TIMEOUT);
+}
+
+// ============================================================== the rest ==
+// One CTA of 8 warps per (chunk, q/k head).  Warp (mr, nh): tokens 16 mr, channels 64 nh of dq and dk.
+// Of the 64 x 64 products the warps nh = 0 form dP and Q K^T, the others dA and K K^T; the two warps of an
+// SM quarter have row blocks mr and 3 - mr, so that the quarters' triangles are even.
+constexpr int kRestThreads = 256;
+struct RestSmem {
+    static constexpr uint32_t S = 0, X = 65536, U = 131072, W = 163840;  // as in the record
+    static constexpr uint32_t K = 196608, Q = 212992;
+    static constexpr uint32_t G = 229376;            // the image's vectors
+    static constexpr uint32_t BARS = G + 1328;       // u64: K and Q, S and W, X and U
+    static constexpr uint32_t TOTAL = BARS + 32;
+    static constexpr uint32_t ALLOC = TOTAL + 1024;
+    // over S once it and X have been read
+    static constexpr uint32_t M = 0, E = 8192;       // bf16 [64][64], 128B-swizzled
+    static constexpr uint32_t P = 16384;             // f32: parts of the sums, below
+};
+static_assert(RestSmem::ALLOC <= 232448 && RestSmem::BARS % 8 == 0, "shared memory");
+// parts (floats): a per nh [2][64], w per nh [2][64], the pairs' sums per warp [8][64], db [64],
+// <X, S> per warp [8]
+constexpr int kPtA = 0, kPtW = 128, kPtC = 256, kPtB = 768, kPtI = 832;
+
+__global__ void __launch_bounds__(kRestThreads, 1)
+    kda_gdn_grad_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const GdnArgs p,
+                        const GdnBackwardArgs gr, const int32_t* __restrict__ co, const uint8_t* __restrict__ images,
+                        int64_t chunk_slots, const uint8_t* __restrict__ records) {
+    using L = RestSmem;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int N = p.num_seqs, Hv = p.Hv, group = Hv / p.Hk;
+    const int j = blockIdx.x / p.Hk, hk = blockIdx.x - j * p.Hk;
+    if (co[N + 1] == 0 || j >= co[N]) return;
+    int seq;
+    {  // the largest n with co[n] <= j
+        int lo = 0, hi = N - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (co[mid] <= j) lo = mid;
+            else hi = mid - 1;
+        }
+        seq = lo;
+    }
+    const int64_t t0 = static_cast<int64_t>(p.cu_seqlens[seq]) + static_cast<int64_t>(j - co[seq]) * C;
+    const int64_t rem = p.cu_seqlens[seq + 1] - t0;
+    const int Lc = static_cast<int>(rem < C ? rem : C);
+    if (!KDA_BOUNDS(seq >= 0 && seq < N && j < chunk_slots && t0 >= 0 && Lc >= 1 && t0 + Lc <= p.total_tokens,
+                    p.device_status))
+        return;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BARS);
+    float* const gs = reinterpret_cast<float*>(sm + L::G);
+    float* const parts = reinterpret_cast<float*>(sm + L::P);
+    const size_t unit0 = static_cast<size_t>(j) * Hv + static_cast<size_t>(hk) * group;
+    auto issue = [&](int hh) {  // a value head's record
+        const uint8_t* rec = records + (unit0 + hh) * kRecStride;
+        mbar_arrive_expect_tx(&bars[1], 65536 + 32768);
+        bulk_g2s(sm + L::S, rec + kRecS, 65536, &bars[1]);
+        bulk_g2s(sm + L::W, rec + kRecW, 32768, &bars[1]);
+        mbar_arrive_expect_tx(&bars[2], 65536 + 32768);
+        bulk_g2s(sm + L::X, rec + kRecX, 65536, &bars[2]);
+        bulk_g2s(sm + L::U, rec + kRecU, 32768, &bars[2]);
+    };
+    if (tid == 0) {
+        for (int i = 0; i < 3; ++i) mbar_init(&bars[i], 1);
+        fence_mbar_init();
+        mbar_arrive_expect_tx(&bars[0], 32768);
+#pragma unroll
+        for (int kh = 0; kh < 2; ++kh) {
+            tma_load_3d(sm + L::K + kh * 8192, &tm_k, &bars[0], 64 * kh, hk, static_cast<int32_t>(t0));
+            tma_load_3d(sm + L::Q + kh * 8192, &tm_q, &bars[0], 64 * kh, hk, static_cast<int32_t>(t0));
+        }
+        issue(0);
+    }
+    __syncthreads();
+    bool ok = mbar_wait_pipe(&bars[0], 0);
+    if (Lc < C) {  // rows behind the sequence's end
+        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+        for (int e = tid; e < (C - Lc) * 16; e += kRestThreads) {
+            const uint32_t off = (e & 1) * 8192 + sw128_chunk(Lc + (e >> 4), (e >> 1) & 7);
+            *reinterpret_cast<uint4*>(sm + L::K + off) = z;
+            *reinterpret_cast<uint4*>(sm + L::Q + off) = z;
+        }
+    }
+    const int g = lane >> 2, t = lane & 3;
+    const int nh = warp >> 2, mr = nh ? 7 - warp : warp;
+    const int lr = lane & 15, lc = lane >> 4;                                      // row-major A operand
+    const int br = (lane & 7) + ((lane >> 4) << 3), bc = (lane >> 3) & 1;          // B operand from [n][k] rows
+    const int kr = (lane & 7) + (((lane >> 3) & 1) << 3), kc = lane >> 4;          // B operand from [k][n] rows
+    const uint32_t base = smem_u32(sm);
+    float dq[8][4], dk[8][4];
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dq[n][e] = dk[n][e] = 0.f;
+
+    for (int hh = 0; hh < group; ++hh) {
+        const int h = hk * group + hh;
+        const uint32_t par = hh & 1;
+        const float* vec = reinterpret_cast<const float*>(images + (unit0 + hh) * kImgStrideBwd + kImgG);
+        for (int e = tid; e < 5 * C + 4; e += kRestThreads) gs[e] = vec[e];
+        uint32_t dof[8][4];  // dO rows 16 mr as A operand
+        {
+            const __nv_bfloat16* d0 = static_cast<const __nv_bfloat16*>(gr.grad_o) + ((t0 + 16 * mr + g) * Hv + h) * D + 2 * t;
+            const bool r0 = 16 * mr + g < Lc, r1 = 16 * mr + g + 8 < Lc;
+            const int64_t step = static_cast<int64_t>(8) * Hv * D;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                dof[k][0] = r0 ? *reinterpret_cast<const uint32_t*>(d0 + 16 * k) : 0u;
+                dof[k][1] = r1 ? *reinterpret_cast<const uint32_t*>(d0 + step + 16 * k) : 0u;
+                dof[k][2] = r0 ? *reinterpret_cast<const uint32_t*>(d0 + 16 * k + 8) : 0u;
+                dof[k][3] = r1 ? *reinterpret_cast<const uint32_t*>(d0 + step + 16 * k + 8) : 0u;
+            }
+        }
+        ok = mbar_wait_pipe(&bars[1], par) && ok;
+        __syncthreads();  // the vectors (and the cleared rows) are there
+        float eg[2], eo[2], be[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            eg[e] = gs[kVecEg + 16 * mr + g + 8 * e];
+            eo[e] = gs[kVecEo + 16 * mr + g + 8 * e];
+            be[e] = gs[kVecB + 16 * mr + g + 8 * e];
+        }
+        // an accumulator's rows against the same rows of q or k, over this warp's channels
+        auto row_dots = [&](const float (&acc)[8][4], uint32_t tile, float (&d)[2]) {
+            d[0] = d[1] = 0.f;
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float2 x = unpack_bf16(*reinterpret_cast<const uint32_t*>(
+                        sm + tile + nh * 8192 + sw128_chunk(16 * mr + g + 8 * e, n) + 4 * t));
+                    d[e] = fmaf(acc[n][2 * e], x.x, fmaf(acc[n][2 * e + 1], x.y, d[e]));
+                }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                d[e] += __shfl_xor_sync(0xffffffffu, d[e], 1);
+                d[e] += __shfl_xor_sync(0xffffffffu, d[e], 2);
+            }
+        };
+        float row_a[2], row_w[2];
+        {  // dO S^T and W S^T
+            float a1[8][4], a2[8][4];
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a1[n][e] = a2[n][e] = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                uint32_t wh[4], wl[4];
+                const uint32_t wa = base + L::W + (k >> 2) * 8192 + sw128_chunk(16 * mr + lr, 2 * (k & 3) + lc);
+                ldsm4(wh, wa);
+                ldsm4(wl, wa + 16384);
+#pragma unroll
+                for (int np = 0; np < 4; ++np) {
+                    uint32_t sh[4], sl[4];
+                    const uint32_t sa = base + L::S + (k >> 2) * 16384 + sw128_chunk(64 * nh + 16 * np + br, 2 * (k & 3) + bc);
+                    ldsm4(sh, sa);
+                    ldsm4(sl, sa + 32768);
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        mma16(a1[2 * np + n], dof[k], sh[2 * n], sh[2 * n + 1]);
+                        mma16(a2[2 * np + n], wh, sh[2 * n], sh[2 * n + 1]);
+                        mma16(a1[2 * np + n], dof[k], sl[2 * n], sl[2 * n + 1]);
+                        mma16(a2[2 * np + n], wh, sl[2 * n], sl[2 * n + 1]);
+                        mma16(a2[2 * np + n], wl, sh[2 * n], sh[2 * n + 1]);
+                    }
+                }
+            }
+            float d1[2], d2[2];
+            row_dots(a1, L::Q, d1);
+            row_dots(a2, L::K, d2);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) row_a[e] = eg[e] * (d1[e] - be[e] * d2[e]);
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    dq[n][e] = fmaf(eg[e >> 1], a1[n][e], dq[n][e]);
+                    dk[n][e] = fmaf(-eg[e >> 1] * be[e >> 1], a2[n][e], dk[n][e]);
+                }
+        }
+        ok = mbar_wait_pipe(&bars[2], par) && ok;
+        {  // U X^T
+            float a1[8][4];
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a1[n][e] = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                uint32_t uh[4], ul[4];
+                const uint32_t ua = base + L::U + (k >> 2) * 8192 + sw128_chunk(16 * mr + lr, 2 * (k & 3) + lc);
+                ldsm4(uh, ua);
+                ldsm4(ul, ua + 16384);
+#pragma unroll
+                for (int np = 0; np < 4; ++np) {
+                    uint32_t xh[4], xl[4];
+                    const uint32_t xa = base + L::X + (k >> 2) * 16384 + sw128_chunk(64 * nh + 16 * np + br, 2 * (k & 3) + bc);
+                    ldsm4(xh, xa);
+                    ldsm4(xl, xa + 32768);
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        mma16(a1[2 * np + n], uh, xh[2 * n], xh[2 * n + 1]);
+                        mma16(a1[2 * np + n], uh, xl[2 * n], xl[2 * n + 1]);
+                        mma16(a1[2 * np + n], ul, xh[2 * n], xh[2 * n + 1]);
+                    }
+                }
+            }
+            row_dots(a1, L::K, row_w);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) row_w[e] *= eo[e];
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dk[n][e] = fmaf(eo[e >> 1], a1[n][e], dk[n][e]);
+        }
+        float inner = 0.f;  // <X, S>
+        for (int e = tid; e < 2048; e += kRestThreads) {
+            const uint4 sh = *reinterpret_cast<const uint4*>(sm + L::S + 16 * e), sl = *reinterpret_cast<const uint4*>(sm + L::S + 32768 + 16 * e);
+            const uint4 xh = *reinterpret_cast<const uint4*>(sm + L::X + 16 * e), xl = *reinterpret_cast<const uint4*>(sm + L::X + 32768 + 16 * e);
+            const uint32_t* a = &sh.x;
+            const uint32_t* b = &sl.x;
+            const uint32_t* c = &xh.x;
+            const uint32_t* d = &xl.x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 s1 = unpack_bf16(a[i]), s2 = unpack_bf16(b[i]), x1 = unpack_bf16(c[i]), x2 = unpack_bf16(d[i]);
+                inner = fmaf(s1.x + s2.x, x1.x + x2.x, inner);
+                inner = fmaf(s1.y + s2.y, x1.y + x2.y, inner);
+            }
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, off);
+        __syncthreads();  // S and X have been read: M, E and the parts take S's place
+        if (t == 0) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                parts[kPtA + 64 * nh + 16 * mr + g + 8 * e] = row_a[e];
+                parts[kPtW + 64 * nh + 16 * mr + g + 8 * e] = row_w[e];
+            }
+        }
+        if (lane == 0) parts[kPtI + warp] = inner;
+        {  // the 64 x 64 products: dP = dO U^T with Q K^T, or W U^T with K K^T
+            float a1[8][4], kk[8][4];
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a1[n][e] = kk[n][e] = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                uint32_t wh[4], wl[4], ga[4];
+                if (nh) {
+                    const uint32_t wa = base + L::W + (k >> 2) * 8192 + sw128_chunk(16 * mr + lr, 2 * (k & 3) + lc);
+                    ldsm4(wh, wa);
+                    ldsm4(wl, wa + 16384);
+                }
+                ldsm4(ga, base + (nh ? L::K : L::Q) + (k >> 2) * 8192 + sw128_chunk(16 * mr + lr, 2 * (k & 3) + lc));
+#pragma unroll
+                for (int np = 0; np < 4; ++np) {
+                    if (np > mr) break;
+                    uint32_t uh[4], ul[4], kf[4];
+                    const uint32_t off = (k >> 2) * 8192 + sw128_chunk(16 * np + br, 2 * (k & 3) + bc);
+                    ldsm4(uh, base + L::U + off);
+                    ldsm4(ul, base + L::U + 16384 + off);
+                    ldsm4(kf, base + L::K + off);
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        mma16(kk[2 * np + n], ga, kf[2 * n], kf[2 * n + 1]);
+                        if (nh) {
+                            mma16(a1[2 * np + n], wh, uh[2 * n], uh[2 * n + 1]);
+                            mma16(a1[2 * np + n], wh, ul[2 * n], ul[2 * n + 1]);
+                            mma16(a1[2 * np + n], wl, uh[2 * n], uh[2 * n + 1]);
+                        } else {
+                            mma16(a1[2 * np + n], dof[k], uh[2 * n], uh[2 * n + 1]);
+                            mma16(a1[2 * np + n], dof[k], ul[2 * n], ul[2 * n + 1]);
+                        }
+                    }
+                }
+            }
+            float left[2] = {0.f, 0.f};  // of rows g and g + 8: the sums of the tiles so far
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                float cs[2] = {0.f, 0.f};  // over rows i >= t of the sums over columns j < t, t = 8 n + 2 t (+ 1)
+                if (n <= 2 * mr + 1) {
+                    const float2 ch = *reinterpret_cast<const float2*>(gs + kVecGh + 8 * n + 2 * t);
+                    const float2 cl = *reinterpret_cast<const float2*>(gs + kVecGl + 8 * n + 2 * t);
+#pragma unroll
+                    for (int e2 = 0; e2 < 2; ++e2) {
+                        const int i = 16 * mr + g + 8 * e2, jj = 8 * n + 2 * t;
+                        const float gh = gs[kVecGh + i], gl = gs[kVecGl + i];
+                        float m[2], d[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float x = (gh - (e ? ch.y : ch.x)) + (gl - (e ? cl.y : cl.x));
+                            const bool in = i < Lc && (nh ? jj + e < i : jj + e <= i);
+                            float gam = in ? exp2_sfu(x) : 0.f;
+                            float v = a1[n][2 * e2 + e];
+                            if (nh) {
+                                if (jj + e == i) parts[kPtB + i] = v / be[e2];
+                                v = -v;
+                                gam *= be[e2];
+                            }
+                            d[e] = in ? v * (gam * kk[n][2 * e2 + e]) : 0.f;
+                            m[e] = in ? gam * v : 0.f;
+                        }
+                        float sum = d[0] + d[1];  // of the lanes up to this one in the row
+                        float y = __shfl_up_sync(0xffffffffu, sum, 1, 4);
+                        if (t >= 1) sum += y;
+                        y = __shfl_up_sync(0xffffffffu, sum, 2, 4);
+                        if (t >= 2) sum += y;
+                        y = __shfl_up_sync(0xffffffffu, sum, 1, 4);
+                        const float before = left[e2] + (t >= 1 ? y : 0.f);
+                        left[e2] += __shfl_sync(0xffffffffu, sum, 3, 4);
+                        if (jj <= i) cs[0] += before;
+                        if (jj + 1 <= i) cs[1] += before + d[0];
+                        *reinterpret_cast<uint32_t*>(sm + (nh ? L::E : L::M) + sw128_chunk(i, n) + 4 * t) = pack_bf16(m[0], m[1]);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) cs[e] += __shfl_xor_sync(0xffffffffu, cs[e], off);
+                }
+                if (g == 0) *reinterpret_cast<float2*>(parts + kPtC + 64 * warp + 8 * n + 2 * t) = make_float2(cs[0], cs[1]);
+            }
+        }
+        __syncthreads();
+        // dq += M K, dk += (E + E^T) K + M^T Q
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint32_t am[4], ae[4], tm[4], te[4];
+            const bool below = k <= mr, above = k >= mr;
+            if (below) {
+                ldsm4(am, base + L::M + sw128_chunk(16 * mr + lr, 2 * k + lc));
+                ldsm4(ae, base + L::E + sw128_chunk(16 * mr + lr, 2 * k + lc));
+            }
+            if (above) {
+                ldsm4t(tm, base + L::M + sw128_chunk(16 * k + br, 2 * mr + bc));
+                ldsm4t(te, base + L::E + sw128_chunk(16 * k + br, 2 * mr + bc));
+            }
+#pragma unroll
+            for (int np = 0; np < 4; ++np) {
+                uint32_t kf[4], qf[4];
+                const uint32_t off = nh * 8192 + sw128_chunk(16 * k + kr, 2 * np + kc);
+                ldsm4t(kf, base + L::K + off);
+                if (above) ldsm4t(qf, base + L::Q + off);
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    if (below) {
+                        mma16(dq[2 * np + n], am, kf[2 * n], kf[2 * n + 1]);
+                        mma16(dk[2 * np + n], ae, kf[2 * n], kf[2 * n + 1]);
+                    }
+                    if (above) {
+                        mma16(dk[2 * np + n], te, kf[2 * n], kf[2 * n + 1]);
+                        mma16(dk[2 * np + n], tm, qf[2 * n], qf[2 * n + 1]);
+                    }
+                }
+            }
+        }
+        if (warp == 0) {  // the decays' and b's gradients, two tokens a lane
+            float ra[2], rw[2], pairs[2], in = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 2 * lane + e;
+                ra[e] = parts[kPtA + r] + parts[kPtA + 64 + r];
+                rw[e] = parts[kPtW + r] + parts[kPtW + 64 + r];
+                pairs[e] = 0.f;
+#pragma unroll
+                for (int w = 0; w < 8; ++w) pairs[e] += parts[kPtC + 64 * w + r];
+            }
+            if (lane < 8) in = parts[kPtI + lane];
+#pragma unroll
+            for (int off = 4; off > 0; off >>= 1) in += __shfl_xor_sync(0xffffffffu, in, off);
+            in = __shfl_sync(0xffffffffu, in, 0) * gs[kVecEc];
+            float sa = ra[0] + ra[1], sw = rw[0] + rw[1];  // from this lane's tokens on; up to them
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const float ya = __shfl_down_sync(0xffffffffu, sa, off), yw = __shfl_up_sync(0xffffffffu, sw, off);
+                if (lane + off < 32) sa += ya;
+                if (lane >= off) sw += yw;
+            }
+            float after = __shfl_down_sync(0xffffffffu, sa, 1), before = __shfl_up_sync(0xffffffffu, sw, 1);
+            if (lane == 31) after = 0.f;
+            if (lane == 0) before = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 2 * lane + e;
+                const float a_on = after + (e ? ra[1] : ra[0] + ra[1]), w_before = e ? before + rw[0] : before;
+                if (r < Lc) {
+                    gr.grad_log_decay[(t0 + r) * Hv + h] = (pairs[e] + a_on) + (w_before + in);
+                    gr.grad_beta[(t0 + r) * Hv + h] = parts[kPtB + r];
+                }
+            }
+        }
+        fence_async_smem();  // M, E, the parts and the vectors, before the next record's copies
+        __syncthreads();
+        if (tid == 0 && hh + 1 < group) issue(hh + 1);
+    }
+    if (!ok && p.device_status) atomicOr(p.device_status, KDA_DEV_TIMEOUT);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int row = 16 * mr + g + 8 * e;
+        if (row >= Lc) continue;
+        const int64_t off = ((t0 + row) * p.Hk + hk) * D + 64 * nh + 2 * t;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(gr.grad_q) + off + 8 * n) =
+                pack_bf16(dq[n][2 * e], dq[n][2 * e + 1]);
+            *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(gr.grad_k) + off + 8 * n) =
+                pack_bf16(dk[n][2 * e], dk[n][2 * e + 1]);
+        }
+    }
+}
+
+template <int NT, int ST>
+cudaError_t launch_walk_back(const GdnArgs& a, const GdnBackwardArgs& b, const GdnWorkspace& w, const CUtensorMap& tm_q,
+                             const CUtensorMap& tm_k, cudaStream_t stream) {
+    using L = BackCfg<NT, ST>;
+    static int configured[64];
+    const cudaError_t err = set_smem(kda_gdn_walk_back_kernel<NT, ST>, L::ALLOC, configured);
+    if (err != cudaSuccess) return err;
+    CUtensorMap tm_do;
+    if (!make_tensor_map(&tm_do, b.grad_o, a.Hv, a.total_tokens, L::kCols, C,
+                         L::kVRow == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+        return cudaErrorInvalidValue;
+    const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(a.num_seqs) * a.Hv * (D / L::kCols));
+    kda_gdn_walk_back_kernel<NT, ST><<<blocks, L::kThreads, L::ALLOC, stream>>>(tm_q, tm_k, tm_do, a, b, w.table, w.order,
+                                                                                w.images, w.chunks, w.records);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_gdn_backward(const GdnArgs& a, const GdnBackwardArgs& b, const GdnWorkspace& w, cudaStream_t stream) {
+    CUtensorMap tm_q, tm_k;
+    if (!make_tensor_map(&tm_q, a.q, a.Hk, a.total_tokens, 64, C, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_tensor_map(&tm_k, a.k, a.Hk, a.total_tokens, 64, C, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    // columns a CTA as in the walk forward
+    cudaError_t err = static_cast<int64_t>(a.num_seqs) * a.Hv * 4 <= device_sm_count()
+                          ? launch_walk_back<1, 3>(a, b, w, tm_q, tm_k, stream)
+                          : launch_walk_back<2, 3>(a, b, w, tm_q, tm_k, stream);
+    static int configured[64];
+    if (err == cudaSuccess) err = set_smem(kda_gdn_grad_kernel, RestSmem::ALLOC, configured);
+    if (err != cudaSuccess) return err;
+    kda_gdn_grad_kernel<<<static_cast<unsigned>(w.chunks * a.Hk), kRestThreads, RestSmem::ALLOC, stream>>>(
+        tm_q, tm_k, a, b, w.table, w.images, w.chunks, w.records);
+    return cudaGetLastError();
+}
+
+}  // namespace kda

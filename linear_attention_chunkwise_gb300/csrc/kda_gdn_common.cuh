@@ -1,0 +1,111 @@
+// kda_gdn_common.cuh -- what the gated delta rule's chunkwise kernels share: the layout of a
+// (chunk, value head)'s image and the warp-level pieces (ldmatrix, mma.sync, two-term operands).
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "kda_args.h"
+#include "kda_internal.h"
+#include "kda_ptx.cuh"
+
+namespace kda {
+namespace gdn {
+
+constexpr int C = kChunk;    // 64
+constexpr int D = kHeadDim;  // 128
+
+// Image of a (chunk, value head): T's two terms and P's first as 128B-swizzled [64][64] bf16 tiles (16 x 16
+// blocks above the diagonal are neither written nor read), fp32 vectors, and, for the gradient, P's
+// second term.
+constexpr uint32_t kImgTh = 0, kImgTl = 8192, kImgP = 16384, kImgG = 24576;
+constexpr uint32_t kImgPl = kImgG + 1536;
+// the vectors: e^g [64], e^(gC - g) [64], b [64], e^gC (and 3 floats unused), then g in base 2 as two terms
+constexpr int kVecEg = 0, kVecEo = C, kVecB = 2 * C, kVecEc = 3 * C, kVecGh = 3 * C + 4, kVecGl = 4 * C + 4;
+constexpr uint32_t kImgScanBytes = kImgG + (3 * C + 4) * 4;  // what the forward scan takes
+constexpr size_t kImgStride = kImgPl, kImgStrideBwd = kImgPl + 8192;
+static_assert((5 * C + 4) * 4 <= 1536 && kImgStride % kAlign == 0 && kImgScanBytes % 16 == 0, "image layout");
+
+// The gradient's record of a (chunk, value head): the state at the chunk's start, the adjoint of the state
+// at its end ([128 channels][128 columns]), U and W ([64 tokens][128 columns]), each as two bf16 terms in
+// 128B-swizzled tiles of 64 columns.
+constexpr uint32_t kRecS = 0, kRecX = 65536, kRecU = 131072, kRecW = 163840;
+constexpr size_t kRecStride = 196608;
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+// d += a b for one 16 x 8 tile (m16n8k16).  With g = lane / 4, t = lane % 4: a = A(g, 2t..), A(g + 8, 2t..),
+// A(g, 2t + 8..), A(g + 8, 2t + 8..); b = B(2t.., g), B(2t + 8.., g); d = D(g, 2t..), D(g + 8, 2t..).
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two bf16 terms of a pair of floats.
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+    hi = pack_bf16(x, y);
+    lo = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+}
+// 2^x by the special function unit (2 ulp); x is a difference of decays in base 2.
+__device__ __forceinline__ float exp2_sfu(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// An accumulator tile's two terms into a record: rows row and row + 8, columns col and col + 1 of tiles
+// `block` bytes apart, the second term `lo` bytes after the first.
+__device__ __forceinline__ void put_record(const float (&c)[4], uint8_t* rec, int block, uint32_t lo, int row, int col) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        uint32_t h, l;
+        split2(c[2 * e], c[2 * e + 1], h, l);
+        uint8_t* p = rec + sw128_off(row + 8 * e, col, block);
+        *reinterpret_cast<uint32_t*>(p) = h;
+        *reinterpret_cast<uint32_t*>(p + lo) = l;
+    }
+}
+// An accumulator tile (16 rows of k, 8 columns) as the B operand of the next product, in two terms.
+struct BTerms {
+    uint32_t h0, h1, l0, l1;
+};
+__device__ __forceinline__ BTerms b_terms(const float (&c)[4]) {
+    BTerms b;
+    uint32_t h0, h1, l0, l1;
+    split2(c[0], c[1], h0, l0);
+    split2(c[2], c[3], h1, l1);
+    b.h0 = transpose8(h0);
+    b.h1 = transpose8(h1);
+    b.l0 = transpose8(l0);
+    b.l1 = transpose8(l1);
+    return b;
+}
+
+template <typename K>
+inline cudaError_t set_smem(K kernel, uint32_t bytes, int* configured) {  // on first use per device
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess || (dev >= 0 && dev < 64 && configured[dev])) return err;
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (err == cudaSuccess && dev >= 0 && dev < 64) configured[dev] = 1;
+    return err;
+}
+
+}  // namespace gdn
+}  // namespace kda

@@ -2,8 +2,8 @@
 //
 // With g the inclusive cumulative log decay of a 64-token chunk, S0 the state at its start, and
 // G_ij = exp(g_i - g_j) (i >= j):
-//   A_ij = b_i G_ij (k_i . k_j)  (i > j),   T = (I + A)^-1 Diag(b),   P_ij = G_ij (q_i . k_j)  (i >= j)
-//   U = T (V - Diag(e^g) K S0),   O = Diag(e^g) Q S0 + P U,   S1 = e^gC S0 + K^T Diag(e^(gC - g)) U
+//   A_ij = b_i G_ij (k_i . k_j)  (i > j),   T = (I + A)^-1,   P_ij = G_ij (q_i . k_j)  (i >= j)
+//   U = T Diag(b) (V - Diag(e^g) K S0),   O = Diag(e^g) Q S0 + P U,   S1 = e^gC S0 + K^T Diag(e^(gC - g)) U
 // (the chunk form of "Understanding Kimi Delta Attention" (pyshine), "The Chunkwise DPLR Algorithm",
 // with its scalar gate).  Unlike the channel-wise gate, the scalar one multiplies the Gram matrices
 // afterwards, so every product has the raw bf16 k or q as one operand, and the decays enter as
@@ -18,71 +18,12 @@
 //         operand by a pack and an 8 x 8 transpose (movmatrix), and there is no barrier between warps
 //         beyond the arrival of the next chunk's tiles.  (tcgen05 would put a TMEM round trip and a
 //         write to shared memory for each of the three chained products on the sequential path.)
-#include <cuda_bf16.h>
-
-#include "kda_args.h"
-#include "kda_internal.h"
-#include "kda_ptx.cuh"
+#include "kda_gdn_common.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int C = kChunk;    // 64
-constexpr int D = kHeadDim;  // 128
-
-// Image of a (chunk, value head): T's two terms and P as 128B-swizzled [64][64] bf16 tiles (16 x 16
-// blocks above the diagonal are neither written nor read), then e^g [64], e^(gC - g) [64], e^gC.
-constexpr uint32_t kImgTh = 0, kImgTl = 8192, kImgP = 16384, kImgG = 24576;
-constexpr uint32_t kImgBytes = kImgG + 528;
-constexpr size_t kImgStride = 25344;
-static_assert(kImgStride % kAlign == 0 && kImgStride >= kImgBytes && kImgBytes % 16 == 0, "image layout");
-
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
-    uint32_t r;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-    return r;
-}
-// d += a b for one 16 x 8 tile (m16n8k16).  With g = lane / 4, t = lane % 4: a = A(g, 2t..), A(g + 8, 2t..),
-// A(g, 2t + 8..), A(g + 8, 2t + 8..); b = B(2t.., g), B(2t + 8.., g); d = D(g, 2t..), D(g + 8, 2t..).
-__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// Two bf16 terms of a pair of floats.
-__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
-    hi = pack_bf16(x, y);
-    lo = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
-}
-// An accumulator tile (16 rows of k, 8 columns) as the B operand of the next product, in two terms.
-struct BTerms {
-    uint32_t h0, h1, l0, l1;
-};
-__device__ __forceinline__ BTerms b_terms(const float (&c)[4]) {
-    BTerms b;
-    uint32_t h0, h1, l0, l1;
-    split2(c[0], c[1], h0, l0);
-    split2(c[2], c[3], h1, l1);
-    b.h0 = transpose8(h0);
-    b.h1 = transpose8(h1);
-    b.l0 = transpose8(l0);
-    b.l1 = transpose8(l1);
-    return b;
-}
+using namespace gdn;
 
 // =============================================================== pass 1 ==
 // One CTA of four warps for a (chunk, q/k head) and `hp` of its value heads, which share the Gram
@@ -108,19 +49,16 @@ struct PrepSmem {
 // log decays below this (a decay of 0 in fp32, as -inf) are taken as this, so that differences of the
 // cumulative sums stay numbers.
 constexpr float kDecayFloor = -1e4f;
-
-// 2^x by the special function unit (2 ulp); x is a difference of decays in base 2.
-__device__ __forceinline__ float exp2_sfu(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
+// In the gradient's images a smaller b, 0 too, is taken as this: U / b is then still what the rows of U
+// hold before b multiplies them, and b's own part in every sum is below fp32's rounding.
+constexpr float kBetaFloor = 8.271806e-25f;  // 2^-80
 
 __global__ void __launch_bounds__(kPrepThreads, 4)
     kda_gdn_prep_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const GdnArgs p, const int32_t* __restrict__ co, uint8_t* images, int64_t chunk_slots,
-                        int32_t hp) {
+                        int32_t hp, bool bwd) {
     using L = PrepSmem;
+    const size_t stride = bwd ? kImgStrideBwd : kImgStride;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -172,6 +110,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
                 b = p.beta[(t0 + r) * Hv + h];
             }
             x[e] = static_cast<double>(ld < kDecayFloor ? kDecayFloor : ld) * 1.4426950408889634;
+            if (bwd && fabsf(b) < kBetaFloor) b = kBetaFloor;
             beta_s[r] = b;
         }
         double s = x[0] + x[1];
@@ -181,18 +120,24 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
             if (lane >= off) s += y;
         }
         const double last = __shfl_sync(0xffffffffu, s, 31);
-        float* gv = reinterpret_cast<float*>(images + (static_cast<size_t>(j) * Hv + h) * kImgStride + kImgG);
+        float* gv = reinterpret_cast<float*>(images + (static_cast<size_t>(j) * Hv + h) * stride + kImgG);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int r = 2 * lane + e;
             const double g = e ? s : s - x[1];
             const float hi = static_cast<float>(g);
+            const float lo = static_cast<float>(g - hi);
             g_hi[r] = hi;
-            g_lo[r] = static_cast<float>(g - hi);
-            gv[r] = exp2f(static_cast<float>(g));
-            gv[C + r] = exp2f(static_cast<float>(last - g));
+            g_lo[r] = lo;
+            gv[kVecEg + r] = exp2f(static_cast<float>(g));
+            gv[kVecEo + r] = exp2f(static_cast<float>(last - g));
+            gv[kVecB + r] = beta_s[r];
+            if (bwd) {
+                gv[kVecGh + r] = hi;
+                gv[kVecGl + r] = lo;
+            }
         }
-        if (lane == 0) gv[2 * C] = exp2f(static_cast<float>(last));
+        if (lane == 0) gv[kVecEc] = exp2f(static_cast<float>(last));
     };
     if (warp == 1) decays(h0);
     bool ok = true;
@@ -234,7 +179,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     float* const dg = reinterpret_cast<float*>(sm + L::DG);
     for (int hh = 0; hh < hp; ++hh) {
         const int h = h0 + hh;
-        uint8_t* const img = images + (static_cast<size_t>(j) * Hv + h) * kImgStride;
+        uint8_t* const img = images + (static_cast<size_t>(j) * Hv + h) * stride;
         __syncthreads();  // K and Q, or the previous head's A and decays, have been read
         if (hh > 0) {
             if (warp == 1) decays(h);
@@ -255,7 +200,10 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
                 const float d0 = exp2_sfu((gi - ch.x) + (gl - cl.x)), d1 = exp2_sfu((gi - ch.y) + (gl - cl.y));
                 const float p0 = row && jj <= i ? d0 * qk[n][2 * e2] : 0.f;
                 const float p1 = row && jj + 1 <= i ? d1 * qk[n][2 * e2 + 1] : 0.f;
-                *reinterpret_cast<uint32_t*>(img + kImgP + sw128_chunk(i, n) + 4 * t) = pack_bf16(p0, p1);
+                uint32_t ph, pl;
+                split2(p0, p1, ph, pl);
+                *reinterpret_cast<uint32_t*>(img + kImgP + sw128_chunk(i, n) + 4 * t) = ph;
+                if (bwd) *reinterpret_cast<uint32_t*>(img + kImgPl + sw128_chunk(i, n) + 4 * t) = pl;
                 const float a0 = row && jj < i ? b * d0 * kk[n][2 * e2] : 0.f;
                 const float a1 = row && jj + 1 < i ? b * d1 * kk[n][2 * e2 + 1] : 0.f;
                 if ((n >> 1) == mr) {
@@ -310,15 +258,13 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
                     for (int n = 0; n < 2; ++n)  // every slot below the diagonal is overwritten before its use
                         T[k][n] = BTerms{bh[2 * n], bh[2 * n + 1], bl[2 * n], bl[2 * n + 1]};
             }
-            const float b0 = beta_s[16 * w + 2 * t], b1 = beta_s[16 * w + 2 * t + 1];
-            const float b2 = beta_s[16 * w + 8 + 2 * t], b3 = beta_s[16 * w + 9 + 2 * t];
-            auto store = [&](int i, const float (&x)[2][4]) {  // block (i, w), times b of its columns
+            auto store = [&](int i, const float (&x)[2][4]) {  // block (i, w)
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
                     for (int e2 = 0; e2 < 2; ++e2) {
                         uint32_t hi, lo;
-                        split2(x[n][2 * e2] * (n ? b2 : b0), x[n][2 * e2 + 1] * (n ? b3 : b1), hi, lo);
+                        split2(x[n][2 * e2], x[n][2 * e2 + 1], hi, lo);
                         const uint32_t off = sw128_chunk(16 * i + g + 8 * e2, 2 * w + n) + 4 * t;
                         *reinterpret_cast<uint32_t*>(img + kImgTh + off) = hi;
                         *reinterpret_cast<uint32_t*>(img + kImgTl + off) = lo;
@@ -392,7 +338,7 @@ struct ScanCfg {
     static constexpr int kThreads = 32 * (NW + 1);
     static constexpr uint32_t kVRow = kCols >= 64 ? 128 : kCols * 2;  // bytes of a v row in a block
     static constexpr int kVBlocks = kCols >= 64 ? kCols / 64 : 1;
-    static constexpr uint32_t K = 0, Q = 16384, IMG = 32768, V = IMG + 25600;
+    static constexpr uint32_t K = 0, Q = 16384, IMG = 32768, V = IMG + 26624;
     static constexpr uint32_t STAGE = V + C * kVRow * kVBlocks;
     static constexpr uint32_t BARS = ST * STAGE;  // full[ST], empty[ST]
     static constexpr uint32_t ABORT = BARS + 16 * ST;
@@ -400,11 +346,13 @@ struct ScanCfg {
     static_assert(STAGE % 1024 == 0 && ALLOC <= 232448, "stages");
 };
 
-template <int NT, int NW, int ST>
+// REC: the gradient's walk, which leaves every chunk's start state and U in two bf16 terms and no outputs.
+template <int NT, int NW, int ST, bool REC>
 __global__ void __launch_bounds__(ScanCfg<NT, NW, ST>::kThreads, 1)
     kda_gdn_scan_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const GdnArgs p, const int32_t* __restrict__ co,
-                        const int32_t* __restrict__ order, const uint8_t* __restrict__ images, int64_t chunk_slots) {
+                        const int32_t* __restrict__ order, const uint8_t* __restrict__ images, int64_t chunk_slots,
+                        uint8_t* records) {
     using L = ScanCfg<NT, NW, ST>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -450,15 +398,17 @@ __global__ void __launch_bounds__(ScanCfg<NT, NW, ST>::kThreads, 1)
                 }
                 uint8_t* st = sm + s * L::STAGE;
                 const int32_t tok = static_cast<int32_t>(t_begin + static_cast<int64_t>(c) * C);
-                mbar_arrive_expect_tx(&full[s], 32768 + kImgBytes + C * L::kVRow * L::kVBlocks);
+                mbar_arrive_expect_tx(&full[s], (REC ? 16384 : 32768) + kImgScanBytes + C * L::kVRow * L::kVBlocks);
 #pragma unroll
                 for (int kh = 0; kh < 2; ++kh) tma_load_3d(st + L::K + kh * 8192, &tm_k, &full[s], 64 * kh, hk, tok);
 #pragma unroll
                 for (int b = 0; b < L::kVBlocks; ++b)
                     tma_load_3d(st + L::V + b * C * L::kVRow, &tm_v, &full[s], slice * L::kCols + 64 * b, h, tok);
-                bulk_g2s(st + L::IMG, images + (static_cast<size_t>(jb + c) * Hv + h) * kImgStride, kImgBytes, &full[s]);
+                bulk_g2s(st + L::IMG, images + (static_cast<size_t>(jb + c) * Hv + h) * (REC ? kImgStrideBwd : kImgStride),
+                         kImgScanBytes, &full[s]);
 #pragma unroll
-                for (int kh = 0; kh < 2; ++kh) tma_load_3d(st + L::Q + kh * 8192, &tm_q, &full[s], 64 * kh, hk, tok);
+                for (int kh = 0; kh < (REC ? 0 : 2); ++kh)
+                    tma_load_3d(st + L::Q + kh * 8192, &tm_q, &full[s], 64 * kh, hk, tok);
             }
             for (int d = max(0, c - ST); d < c; ++d)  // no copy is left in flight
                 (void)mbar_wait(&full[d % ST], (d / ST) & 1, kDrainLimit);
@@ -469,11 +419,11 @@ __global__ void __launch_bounds__(ScanCfg<NT, NW, ST>::kThreads, 1)
         const int j0 = slice * L::kCols + wc + 2 * t;  // this thread's first state column
         const size_t sbase = (static_cast<size_t>(seq) * Hv + h) * D * D;
         float S[8][NT][4];  // rows 16 m + g (+ 8), columns j0 + 8 n (+ 1)
-    #pragma unroll
+#pragma unroll
         for (int m = 0; m < 8; ++m)
-    #pragma unroll
+#pragma unroll
             for (int n = 0; n < NT; ++n)
-    #pragma unroll
+#pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const size_t off = sbase + static_cast<size_t>(16 * m + g + 8 * e) * D + j0 + 8 * n;
                     const float2 x = p.S0 ? *reinterpret_cast<const float2*>(p.S0 + off) : make_float2(0.f, 0.f);
@@ -501,48 +451,58 @@ __global__ void __launch_bounds__(ScanCfg<NT, NW, ST>::kThreads, 1)
             }
             const uint32_t kb = smem_u32(st + L::K), qb = smem_u32(st + L::Q), ib = smem_u32(st + L::IMG);
             const float* gs = reinterpret_cast<const float*>(st + L::IMG + kImgG);
+            uint8_t* const rec = REC ? records + (static_cast<size_t>(jb + c) * Hv + h) * kRecStride : nullptr;
+            const int rcol = slice * L::kCols + wc + 2 * t;
             float ks[4][NT][4], qs[4][NT][4];
-    #pragma unroll
+#pragma unroll
             for (int m = 0; m < 4; ++m)
-    #pragma unroll
+#pragma unroll
                 for (int n = 0; n < NT; ++n)
-    #pragma unroll
+#pragma unroll
                     for (int e = 0; e < 4; ++e) ks[m][n][e] = qs[m][n][e] = 0.f;
             // K S, the state in two terms; the first one is kept for Q S (the output is rounded to bf16 too)
             uint32_t sh[8][NT][2];
-    #pragma unroll
+#pragma unroll
             for (int k = 0; k < 8; ++k) {
                 BTerms b[NT];
-    #pragma unroll
+#pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    b[n] = b_terms(S[k][n]);
+                    if constexpr (REC) {
+                        put_record(S[k][n], rec + kRecS, 16384, 32768, 16 * k + g, rcol + 8 * n);
+                        b[n] = b_terms(S[k][n]);
+                    } else {
+                        b[n] = b_terms(S[k][n]);
+                    }
                     sh[k][n][0] = b[n].h0;
                     sh[k][n][1] = b[n].h1;
                 }
                 uint32_t a[4][4];
-    #pragma unroll
+#pragma unroll
                 for (int m = 0; m < 4; ++m)
                     ldsm4(a[m], kb + (k >> 2) * 8192 + sw128_chunk(16 * m + lr, 2 * (k & 3) + lc));
-    #pragma unroll
+#pragma unroll
                 for (int m = 0; m < 4; ++m)
-    #pragma unroll
+#pragma unroll
                     for (int n = 0; n < NT; ++n) mma16(ks[m][n], a[m], b[n].h0, b[n].h1);
-    #pragma unroll
+#pragma unroll
                 for (int m = 0; m < 4; ++m)
-    #pragma unroll
+#pragma unroll
                     for (int n = 0; n < NT; ++n) mma16(ks[m][n], a[m], b[n].l0, b[n].l1);
             }
-            // R = V - e^g K S; Q S runs beside it, a quarter for each 16 rows of R
-            float eg[4][2];
+            // R = b (V - e^g K S); Q S runs beside it, a quarter for each 16 rows of R
+            float eg[4][2], be[2];
             BTerms r[4][NT];
-    #pragma unroll
+#pragma unroll
             for (int k = 0; k < 4; ++k) {
-    #pragma unroll
-                for (int e = 0; e < 2; ++e) eg[k][e] = gs[16 * k + g + 8 * e];
-    #pragma unroll
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    eg[k][e] = gs[kVecEg + 16 * k + g + 8 * e];
+                    be[e] = gs[kVecB + 16 * k + g + 8 * e];
+                }
+#pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float x[4];
-    #pragma unroll
+#pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int row = 16 * k + g + 8 * e;
                         const uint32_t piece = static_cast<uint32_t>((wc + 8 * n) >> 3);  // 16 bytes: 8 columns
@@ -550,130 +510,139 @@ __global__ void __launch_bounds__(ScanCfg<NT, NW, ST>::kThreads, 1)
                         if constexpr (L::kVRow == 128) off = (piece >> 3) * (C * 128) + sw128_chunk(row, piece & 7);
                         else off = row * 64 + (((piece ^ (row >> 1)) & 3) << 4);  // 64-byte rows
                         const uint32_t vv = *reinterpret_cast<const uint32_t*>(st + L::V + off + 4 * t);
-                        x[2 * e] = fmaf(-eg[k][e], ks[k][n][2 * e], __uint_as_float(vv << 16));
-                        x[2 * e + 1] = fmaf(-eg[k][e], ks[k][n][2 * e + 1], __uint_as_float(vv & 0xffff0000u));
+                        x[2 * e] = be[e] * fmaf(-eg[k][e], ks[k][n][2 * e], __uint_as_float(vv << 16));
+                        x[2 * e + 1] = be[e] * fmaf(-eg[k][e], ks[k][n][2 * e + 1], __uint_as_float(vv & 0xffff0000u));
                         if (row >= Lc) x[2 * e] = x[2 * e + 1] = 0.f;
                     }
                     r[k][n] = b_terms(x);
                 }
-    #pragma unroll
-                for (int kq = 2 * k; kq < 2 * k + 2; ++kq) {
+#pragma unroll
+                for (int kq = 2 * k; kq < (REC ? 0 : 2 * k + 2); ++kq) {
                     uint32_t a[4][4];
-    #pragma unroll
+#pragma unroll
                     for (int m = 0; m < 4; ++m)
                         ldsm4(a[m], qb + (kq >> 2) * 8192 + sw128_chunk(16 * m + lr, 2 * (kq & 3) + lc));
-    #pragma unroll
+#pragma unroll
                     for (int m = 0; m < 4; ++m)
-    #pragma unroll
+#pragma unroll
                         for (int n = 0; n < NT; ++n) mma16(qs[m][n], a[m], sh[kq][n][0], sh[kq][n][1]);
                 }
             }
             // U = T R, both in two terms
             float u[4][NT][4];
-    #pragma unroll
+#pragma unroll
             for (int m = 0; m < 4; ++m)
-    #pragma unroll
+#pragma unroll
                 for (int n = 0; n < NT; ++n)
-    #pragma unroll
+#pragma unroll
                     for (int e = 0; e < 4; ++e) u[m][n][e] = 0.f;
-    #pragma unroll
+#pragma unroll
             for (int k = 0; k < 4; ++k) {
                 uint32_t ah[4][4], al[4][4];
-    #pragma unroll
+#pragma unroll
                 for (int m = k; m < 4; ++m) {
                     ldsm4(ah[m], ib + kImgTh + sw128_chunk(16 * m + lr, 2 * k + lc));
                     ldsm4(al[m], ib + kImgTl + sw128_chunk(16 * m + lr, 2 * k + lc));
                 }
-    #pragma unroll
+#pragma unroll
                 for (int m = k; m < 4; ++m)
-    #pragma unroll
+#pragma unroll
                     for (int n = 0; n < NT; ++n) mma16(u[m][n], ah[m], r[k][n].h0, r[k][n].h1);
-    #pragma unroll
+#pragma unroll
                 for (int m = k; m < 4; ++m)
-    #pragma unroll
+#pragma unroll
                     for (int n = 0; n < NT; ++n) mma16(u[m][n], ah[m], r[k][n].l0, r[k][n].l1);
-    #pragma unroll
+#pragma unroll
                 for (int m = k; m < 4; ++m)
-    #pragma unroll
+#pragma unroll
                     for (int n = 0; n < NT; ++n) mma16(u[m][n], al[m], r[k][n].h0, r[k][n].h1);
             }
             // S <- e^gC S + K^T (e^(gC - g) U), U in two terms
-            const float gc = gs[2 * C];
-    #pragma unroll
+            const float gc = gs[kVecEc];
+#pragma unroll
             for (int m = 0; m < 8; ++m)
-    #pragma unroll
+#pragma unroll
                 for (int n = 0; n < NT; ++n)
-    #pragma unroll
+#pragma unroll
                     for (int e = 0; e < 4; ++e) S[m][n][e] *= gc;
-    #pragma unroll
+#pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float e0 = gs[C + 16 * k + g], e1 = gs[C + 16 * k + g + 8];
+                const float e0 = gs[kVecEo + 16 * k + g], e1 = gs[kVecEo + 16 * k + g + 8];
                 BTerms b[NT];
-    #pragma unroll
+#pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     const float x[4] = {u[k][n][0] * e0, u[k][n][1] * e0, u[k][n][2] * e1, u[k][n][3] * e1};
                     b[n] = b_terms(x);
                 }
-    #pragma unroll
+#pragma unroll
                 for (int mh = 0; mh < 2; ++mh) {
                     uint32_t a[4][4];
-    #pragma unroll
+#pragma unroll
                     for (int m = 0; m < 4; ++m) ldsm4t(a[m], kb + mh * 8192 + sw128_chunk(16 * k + tr, 2 * m + tc));
-    #pragma unroll
+#pragma unroll
                     for (int m = 0; m < 4; ++m)
-    #pragma unroll
+#pragma unroll
                         for (int n = 0; n < NT; ++n) mma16(S[4 * mh + m][n], a[m], b[n].h0, b[n].h1);
-    #pragma unroll
+#pragma unroll
                     for (int m = 0; m < 4; ++m)
-    #pragma unroll
+#pragma unroll
                         for (int n = 0; n < NT; ++n) mma16(S[4 * mh + m][n], a[m], b[n].l0, b[n].l1);
                 }
             }
-            // O = e^g Q S + P U
-    #pragma unroll
-            for (int m = 0; m < 4; ++m)
-    #pragma unroll
-                for (int n = 0; n < NT; ++n)
-    #pragma unroll
-                    for (int e = 0; e < 4; ++e) qs[m][n][e] *= eg[m][e >> 1];
-    #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint32_t b0[NT], b1[NT];
-    #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    b0[n] = transpose8(pack_bf16(u[k][n][0], u[k][n][1]));
-                    b1[n] = transpose8(pack_bf16(u[k][n][2], u[k][n][3]));
-                }
-    #pragma unroll
-                for (int m = k; m < 4; ++m) {
-                    uint32_t a[4];
-                    ldsm4(a, ib + kImgP + sw128_chunk(16 * m + lr, 2 * k + lc));
-    #pragma unroll
-                    for (int n = 0; n < NT; ++n) mma16(qs[m][n], a, b0[n], b1[n]);
+            if constexpr (REC) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) put_record(u[k][n], rec + kRecU, 8192, 16384, 16 * k + g, rcol + 8 * n);
+            } else {
+                // O = e^g Q S + P U
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) qs[m][n][e] *= eg[m][e >> 1];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t b0[NT], b1[NT];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        b0[n] = transpose8(pack_bf16(u[k][n][0], u[k][n][1]));
+                        b1[n] = transpose8(pack_bf16(u[k][n][2], u[k][n][3]));
+                    }
+#pragma unroll
+                    for (int m = k; m < 4; ++m) {
+                        uint32_t a[4];
+                        ldsm4(a, ib + kImgP + sw128_chunk(16 * m + lr, 2 * k + lc));
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma16(qs[m][n], a, b0[n], b1[n]);
+                    }
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);  // the warp has read all it takes of this stage
-            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + (t0 * Hv + h) * D + j0;
-    #pragma unroll
-            for (int m = 0; m < 4; ++m)
-    #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int row = 16 * m + g + 8 * e;
-                    if (row < Lc) {
-    #pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            *reinterpret_cast<uint32_t*>(o + static_cast<int64_t>(row) * Hv * D + 8 * n) =
-                                pack_bf16(qs[m][n][2 * e], qs[m][n][2 * e + 1]);
+            if constexpr (!REC) {
+                __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + (t0 * Hv + h) * D + j0;
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int row = 16 * m + g + 8 * e;
+                        if (row < Lc) {
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                *reinterpret_cast<uint32_t*>(o + static_cast<int64_t>(row) * Hv * D + 8 * n) =
+                                    pack_bf16(qs[m][n][2 * e], qs[m][n][2 * e + 1]);
+                        }
                     }
-                }
+            }
         }
         if (p.S_final && !*abort_s) {
-    #pragma unroll
+#pragma unroll
             for (int m = 0; m < 8; ++m)
-    #pragma unroll
+#pragma unroll
                 for (int n = 0; n < NT; ++n)
-    #pragma unroll
+#pragma unroll
                     for (int e = 0; e < 2; ++e)
                         *reinterpret_cast<float2*>(p.S_final + sbase + static_cast<size_t>(16 * m + g + 8 * e) * D + j0 +
                                                    8 * n) = make_float2(S[m][n][2 * e], S[m][n][2 * e + 1]);
@@ -683,71 +652,72 @@ __global__ void __launch_bounds__(ScanCfg<NT, NW, ST>::kThreads, 1)
     if (tid == 0 && *abort_s && p.device_status) atomicOr(p.device_status, KDA_DEV_TIMEOUT);
 }
 
-template <typename K>
-cudaError_t set_smem(K kernel, uint32_t bytes, int* configured) {  // on first use per device
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err != cudaSuccess || (dev >= 0 && dev < 64 && configured[dev])) return err;
-    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-    if (err == cudaSuccess && dev >= 0 && dev < 64) configured[dev] = 1;
-    return err;
-}
-
-template <int NT, int NW, int ST>
-cudaError_t launch_scan(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const GdnArgs& a, const int32_t* table,
-                        const int32_t* order, const uint8_t* images, int64_t slots, cudaStream_t stream) {
+template <int NT, int NW, int ST, bool REC>
+cudaError_t launch_scan(const GdnArgs& a, const GdnWorkspace& w, cudaStream_t stream) {
     using L = ScanCfg<NT, NW, ST>;
     static int configured[64];
-    cudaError_t err = set_smem(kda_gdn_scan_kernel<NT, NW, ST>, L::ALLOC, configured);
+    cudaError_t err = set_smem(kda_gdn_scan_kernel<NT, NW, ST, REC>, L::ALLOC, configured);
     if (err != cudaSuccess) return err;
-    CUtensorMap tm_v;
-    if (!make_tensor_map(&tm_v, a.v, a.Hv, a.total_tokens, L::kVRow / 2, C,
+    CUtensorMap tm_q, tm_k, tm_v;
+    if (!make_tensor_map(&tm_q, a.q, a.Hk, a.total_tokens, 64, C, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_tensor_map(&tm_k, a.k, a.Hk, a.total_tokens, 64, C, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_tensor_map(&tm_v, a.v, a.Hv, a.total_tokens, L::kVRow / 2, C,
                          L::kVRow == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
         return cudaErrorInvalidValue;
     const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(a.num_seqs) * a.Hv * (D / L::kCols));
-    kda_gdn_scan_kernel<NT, NW, ST><<<blocks, L::kThreads, L::ALLOC, stream>>>(tm_q, tm_k, tm_v, a, table, order, images,
-                                                                               slots);
+    kda_gdn_scan_kernel<NT, NW, ST, REC><<<blocks, L::kThreads, L::ALLOC, stream>>>(
+        tm_q, tm_k, tm_v, a, w.table, w.order, w.images, w.chunks, w.records);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-GdnLayout gdn_layout(int32_t num_seqs, int64_t total_tokens, int32_t Hv) {
-    GdnLayout l;
-    l.chunks = (total_tokens + C - 1) / C + num_seqs;
-    l.table = round_up(static_cast<size_t>(num_seqs > 0 ? num_seqs : 1) * 4, kAlign);
-    l.images = l.table + round_up((static_cast<size_t>(num_seqs) + 2) * 4, kAlign);
-    l.total = l.images + static_cast<size_t>(l.chunks) * Hv * kImgStride;
-    return l;
+cudaError_t launch_gdn_tables(const GdnArgs& a, const GdnWorkspace& w, cudaStream_t stream) {
+    cudaError_t err = launch_chunk_table(a.cu_seqlens, a.num_seqs, a.total_tokens, w.table, a.device_status, nullptr, nullptr,
+                                         0, stream);
+    if (err == cudaSuccess && w.order)
+        err = launch_schedule(a.cu_seqlens, a.num_seqs, a.total_tokens, w.order, a.device_status, stream);
+    return err;
 }
 
-cudaError_t launch_gdn_chunked(const GdnArgs& a, const GdnLayout& lay, uint8_t* workspace, cudaStream_t stream) {
-    if (a.num_seqs == 0) return cudaSuccess;
-    int32_t* order = reinterpret_cast<int32_t*>(workspace + lay.order);
-    int32_t* table = reinterpret_cast<int32_t*>(workspace + lay.table);
-    uint8_t* images = workspace + lay.images;
+cudaError_t launch_gdn_prep(const GdnArgs& a, const GdnWorkspace& w, cudaStream_t stream) {
     CUtensorMap tm_q, tm_k;
     if (!make_tensor_map(&tm_q, a.q, a.Hk, a.total_tokens, 64, C, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_tensor_map(&tm_k, a.k, a.Hk, a.total_tokens, 64, C, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
-    cudaError_t err = launch_chunk_table(a.cu_seqlens, a.num_seqs, a.total_tokens, table, a.device_status, nullptr, nullptr,
-                                         0, stream);
-    if (err == cudaSuccess && a.num_seqs > 1)
-        err = launch_schedule(a.cu_seqlens, a.num_seqs, a.total_tokens, order, a.device_status, stream);
     static int configured[64];
-    if (err == cudaSuccess) err = set_smem(kda_gdn_prep_kernel, PrepSmem::ALLOC, configured);
+    const cudaError_t err = set_smem(kda_gdn_prep_kernel, PrepSmem::ALLOC, configured);
     if (err != cudaSuccess) return err;
     // the value heads of a group share a CTA's Gram matrices where that leaves a CTA for every SM
     const int m = a.Hv / a.Hk;
-    const int hp = lay.chunks * a.Hk >= device_sm_count() ? m : 1;
-    kda_gdn_prep_kernel<<<static_cast<unsigned>(lay.chunks * (a.Hv / hp)), kPrepThreads, PrepSmem::ALLOC, stream>>>(
-        tm_q, tm_k, a, table, images, lay.chunks, hp);
-    err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
-    const int32_t* ord = a.num_seqs > 1 ? order : nullptr;
+    const int hp = w.chunks * a.Hk >= device_sm_count() ? m : 1;
+    kda_gdn_prep_kernel<<<static_cast<unsigned>(w.chunks * (a.Hv / hp)), kPrepThreads, PrepSmem::ALLOC, stream>>>(
+        tm_q, tm_k, a, w.table, w.images, w.chunks, hp, w.records != nullptr);
+    return cudaGetLastError();
+}
+
+// 32 columns a CTA while that many CTAs find an SM each (the shortest chain: 1.54 us a chunk), else 64
+// (packed 24.6 k tokens x 32 heads: 663 us against 701 us).
+cudaError_t launch_gdn_scan(const GdnArgs& a, const GdnWorkspace& w, cudaStream_t stream) {
     if (static_cast<int64_t>(a.num_seqs) * a.Hv * 4 <= device_sm_count())
-        return launch_scan<1, 4, 3>(tm_q, tm_k, a, table, ord, images, lay.chunks, stream);
-    return launch_scan<2, 4, 3>(tm_q, tm_k, a, table, ord, images, lay.chunks, stream);
+        return w.records ? launch_scan<1, 4, 3, true>(a, w, stream) : launch_scan<1, 4, 3, false>(a, w, stream);
+    return w.records ? launch_scan<2, 4, 3, true>(a, w, stream) : launch_scan<2, 4, 3, false>(a, w, stream);
+}
+
+size_t gdn_workspace(int32_t num_seqs, int64_t total_tokens, int32_t Hv, bool bwd, uint8_t* base, GdnWorkspace* w) {
+    const int64_t chunks = (total_tokens + C - 1) / C + num_seqs;
+    const size_t units = static_cast<size_t>(chunks) * Hv;
+    const size_t table = round_up(static_cast<size_t>(num_seqs > 0 ? num_seqs : 1) * 4, kAlign);
+    const size_t images = table + round_up((static_cast<size_t>(num_seqs) + 2) * 4, kAlign);
+    const size_t records = images + units * (bwd ? kImgStrideBwd : kImgStride);
+    if (w) {
+        w->order = num_seqs > 1 ? reinterpret_cast<int32_t*>(base) : nullptr;
+        w->table = reinterpret_cast<int32_t*>(base + table);
+        w->images = base + images;
+        w->records = bwd ? base + records : nullptr;
+        w->chunks = chunks;
+    }
+    return records + (bwd ? units * kRecStride : 0);
 }
 
 }  // namespace kda
