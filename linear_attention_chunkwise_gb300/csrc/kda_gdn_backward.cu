@@ -34,13 +34,13 @@ struct BackCfg {
     static constexpr int kCols = 8 * NT * kWarps;
     static constexpr int kThreads = 32 * (kWarps + 1);
     static constexpr uint32_t kVRow = 2 * kCols;  // bytes of a dO row
-    static constexpr uint32_t K = 0, Q = 16384, IMG = 32768, V = IMG + 34816;
+    static constexpr uint32_t K = 0, Q = 16384, IMG = 32768, V = IMG + 27648;
     static constexpr uint32_t STAGE = V + C * kVRow;
     static constexpr uint32_t BARS = ST * STAGE;  // full[ST], empty[ST]
     static constexpr uint32_t ABORT = BARS + 16 * ST;
     static constexpr uint32_t ALLOC = ABORT + 16 + 1024;
     static_assert(kVRow == 64 || kVRow == 128, "swizzled rows");
-    static_assert(STAGE % 1024 == 0 && ALLOC <= 232448 && kImgStrideBwd <= 34816, "stages");
+    static_assert(STAGE % 1024 == 0 && ALLOC <= 232448 && kImgStrideBwd <= 27648, "stages");
 };
 
 template <int NT, int ST>
@@ -126,6 +126,7 @@ __global__ void __launch_bounds__(BackCfg<NT, ST>::kThreads, 1)
         // ldmatrix addresses: rows of tokens, and transposed [channels or columns][tokens] blocks
         const int lr = lane & 15, lc = lane >> 4;
         const int tr = (lane & 7) + ((lane >> 4) << 3), tc = (lane >> 3) & 1;
+        const int lt = (lane & 7) | ((lane & 8) << 1) | ((lane & 16) >> 1);  // an image block's, transposed
         for (int i = 0; i < nch; ++i) {
             const int s = i % ST, c = nch - 1 - i;
             uint8_t* st = sm + s * L::STAGE;
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(BackCfg<NT, ST>::kThreads, 1)
                     *reinterpret_cast<uint4*>(st + L::V + e) = z;
                 __syncwarp();
             }
-            const uint32_t kb = smem_u32(st + L::K), qb = smem_u32(st + L::Q), ib = smem_u32(st + L::IMG);
+            const uint32_t kb = smem_u32(st + L::K), qb = smem_u32(st + L::Q), ib = smem_u32(st + L::IMG) + 16 * lt;
             const float* gs = reinterpret_cast<const float*>(st + L::IMG + kImgG);
             uint8_t* const rec = records + (static_cast<size_t>(jb + c) * Hv + h) * kRecStride;
             // K X
@@ -195,7 +196,8 @@ __global__ void __launch_bounds__(BackCfg<NT, ST>::kThreads, 1)
                     dob[2 * hf + 1][n][0] = f[2];
                     dob[2 * hf + 1][n][1] = f[3];
                 }
-            // dU = e K X + P^T dO, P in two terms (block rows k of P from the diagonal down)
+            // dU = e K X + P^T dO, P in three terms: an entry's error is that of a whole row of W, and of b's
+            // gradient with it
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 const float e0 = gs[kVecEo + 16 * m + g], e1 = gs[kVecEo + 16 * m + g + 8];
@@ -209,11 +211,12 @@ __global__ void __launch_bounds__(BackCfg<NT, ST>::kThreads, 1)
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                uint32_t ah[4][4], al[4][4];
+                uint32_t ah[4][4], al[4][4], am[4][4];
 #pragma unroll
                 for (int m = 0; m <= k; ++m) {
-                    ldsm4t(ah[m], ib + kImgP + sw128_chunk(16 * k + tr, 2 * m + tc));
-                    ldsm4t(al[m], ib + kImgPl + sw128_chunk(16 * k + tr, 2 * m + tc));
+                    ldsm4t(ah[m], ib + kImgP + tri_blk(k, m));
+                    ldsm4t(al[m], ib + kImgPl + tri_blk(k, m));
+                    ldsm4t(am[m], ib + kImgPl2 + tri_blk(k, m));
                 }
 #pragma unroll
                 for (int m = 0; m <= k; ++m)
@@ -223,8 +226,12 @@ __global__ void __launch_bounds__(BackCfg<NT, ST>::kThreads, 1)
                 for (int m = 0; m <= k; ++m)
 #pragma unroll
                     for (int n = 0; n < NT; ++n) mma16(u[m][n], al[m], dob[k][n][0], dob[k][n][1]);
+#pragma unroll
+                for (int m = 0; m <= k; ++m)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma16(u[m][n], am[m], dob[k][n][0], dob[k][n][1]);
             }
-            // W = T^T dU, both in two terms
+            // W = T^T dU, T in two terms, dU in three
             float w[4][NT][4];
 #pragma unroll
             for (int m = 0; m < 4; ++m)
@@ -234,27 +241,31 @@ __global__ void __launch_bounds__(BackCfg<NT, ST>::kThreads, 1)
                     for (int e = 0; e < 4; ++e) w[m][n][e] = 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                BTerms b[NT];
+                BTerms3 b3[NT];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) b[n] = b_terms(u[k][n]);
+                for (int n = 0; n < NT; ++n) b3[n] = b_terms3(u[k][n]);
                 uint32_t ah[4][4], al[4][4];
 #pragma unroll
                 for (int m = 0; m <= k; ++m) {
-                    ldsm4t(ah[m], ib + kImgTh + sw128_chunk(16 * k + tr, 2 * m + tc));
-                    ldsm4t(al[m], ib + kImgTl + sw128_chunk(16 * k + tr, 2 * m + tc));
+                    ldsm4t(ah[m], ib + kImgTh + tri_blk(k, m));
+                    ldsm4t(al[m], ib + kImgTl + tri_blk(k, m));
                 }
 #pragma unroll
                 for (int m = 0; m <= k; ++m)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) mma16(w[m][n], ah[m], b[n].h0, b[n].h1);
+                    for (int n = 0; n < NT; ++n) mma16(w[m][n], ah[m], b3[n].b.h0, b3[n].b.h1);
 #pragma unroll
                 for (int m = 0; m <= k; ++m)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) mma16(w[m][n], ah[m], b[n].l0, b[n].l1);
+                    for (int n = 0; n < NT; ++n) mma16(w[m][n], ah[m], b3[n].b.l0, b3[n].b.l1);
 #pragma unroll
                 for (int m = 0; m <= k; ++m)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) mma16(w[m][n], al[m], b[n].h0, b[n].h1);
+                    for (int n = 0; n < NT; ++n) mma16(w[m][n], ah[m], b3[n].m0, b3[n].m1);
+#pragma unroll
+                for (int m = 0; m <= k; ++m)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma16(w[m][n], al[m], b3[n].b.h0, b3[n].b.h1);
             }
             // X <- e^gC X + K^T (-e^g b W) + Q^T (e^g dO)
             const float gc = gs[kVecEc];

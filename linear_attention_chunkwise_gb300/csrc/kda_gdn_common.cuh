@@ -14,16 +14,23 @@ namespace gdn {
 constexpr int C = kChunk;    // 64
 constexpr int D = kHeadDim;  // 128
 
-// Image of a (chunk, value head): T's two terms and P's first as 128B-swizzled [64][64] bf16 tiles (16 x 16
-// blocks above the diagonal are neither written nor read), fp32 vectors, and, for the gradient, P's
-// second term.
-constexpr uint32_t kImgTh = 0, kImgTl = 8192, kImgP = 16384, kImgG = 24576;
-constexpr uint32_t kImgPl = kImgG + 1536;
+// Image of a (chunk, value head): T's two terms and P's first, the ten 16 x 16 blocks on and below the
+// diagonal of each; fp32 vectors; and, for the gradient, P's second and third term.  A block is its four
+// 8 x 8 matrices (rows 0..7 and 8..15 of columns 0..7, then of columns 8..15), so that ldmatrix reads it
+// with lane l's address at 16 l and a warp's fragment stores fill whole 128-byte lines.
+constexpr uint32_t kBlkBytes = 512, kTriBytes = 10 * kBlkBytes;
+constexpr uint32_t kImgTh = 0, kImgTl = kTriBytes, kImgP = 2 * kTriBytes, kImgG = 3 * kTriBytes;
+constexpr uint32_t kImgPl = kImgG + 1536, kImgPl2 = kImgPl + kTriBytes;
 // the vectors: e^g [64], e^(gC - g) [64], b [64], e^gC (and 3 floats unused), then g in base 2 as two terms
 constexpr int kVecEg = 0, kVecEo = C, kVecB = 2 * C, kVecEc = 3 * C, kVecGh = 3 * C + 4, kVecGl = 4 * C + 4;
 constexpr uint32_t kImgScanBytes = kImgG + (3 * C + 4) * 4;  // what the forward scan takes
-constexpr size_t kImgStride = kImgPl, kImgStrideBwd = kImgPl + 8192;
-static_assert((5 * C + 4) * 4 <= 1536 && kImgStride % kAlign == 0 && kImgScanBytes % 16 == 0, "image layout");
+constexpr size_t kImgStride = kImgPl, kImgStrideBwd = kImgPl2 + kTriBytes;
+static_assert((5 * C + 4) * 4 <= 1536 && kImgStride % kAlign == 0 && kImgStrideBwd % kAlign == 0 &&
+                  kImgScanBytes % 16 == 0,
+              "image layout");
+// Block (i, j), j <= i, and within it the pair of columns 2 t, 2 t + 1 of its half n in row g (+ 8 e).
+__device__ __forceinline__ constexpr uint32_t tri_blk(int i, int j) { return (i * (i + 1) / 2 + j) * kBlkBytes; }
+__device__ __forceinline__ uint32_t blk_pair(int g, int e, int n, int t) { return (2 * n + e) * 128 + 16 * g + 4 * t; }
 
 // The gradient's record of a (chunk, value head): the state at the chunk's start, the adjoint of the state
 // at its end ([128 channels][128 columns]), U and W ([64 tokens][128 columns]), each as two bf16 terms in
@@ -57,7 +64,8 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Two bf16 terms of a pair of floats.
+// Two bf16 terms of a pair of floats.  The first is off by at most 2^(e-8) for 2^e <= |x| <
+// 2^(e+1); the second, rounding that, leaves at most 2^(e-17): 2^-17 of |x|.
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
     hi = pack_bf16(x, y);
     lo = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
@@ -69,6 +77,10 @@ __device__ __forceinline__ float exp2_sfu(float x) {
     return r;
 }
 
+__device__ __forceinline__ uint32_t third2(float x, float y, uint32_t hi, uint32_t lo) {  // what two terms leave
+    return pack_bf16((x - __uint_as_float(hi << 16)) - __uint_as_float(lo << 16),
+                     (y - __uint_as_float(hi & 0xffff0000u)) - __uint_as_float(lo & 0xffff0000u));
+}
 // An accumulator tile's two terms into a record: rows row and row + 8, columns col and col + 1 of tiles
 // `block` bytes apart, the second term `lo` bytes after the first.
 __device__ __forceinline__ void put_record(const float (&c)[4], uint8_t* rec, int block, uint32_t lo, int row, int col) {
@@ -95,6 +107,25 @@ __device__ __forceinline__ BTerms b_terms(const float (&c)[4]) {
     b.l0 = transpose8(l0);
     b.l1 = transpose8(l1);
     return b;
+}
+
+// The same with a third term, the rest to 2^-25.
+struct BTerms3 {
+    BTerms b;
+    uint32_t m0, m1;
+};
+__device__ __forceinline__ BTerms3 b_terms3(const float (&c)[4]) {
+    BTerms3 r;
+    uint32_t h0, h1, l0, l1;
+    split2(c[0], c[1], h0, l0);
+    split2(c[2], c[3], h1, l1);
+    r.m0 = transpose8(third2(c[0], c[1], h0, l0));
+    r.m1 = transpose8(third2(c[2], c[3], h1, l1));
+    r.b.h0 = transpose8(h0);
+    r.b.h1 = transpose8(h1);
+    r.b.l0 = transpose8(l0);
+    r.b.l1 = transpose8(l1);
+    return r;
 }
 
 template <typename K>

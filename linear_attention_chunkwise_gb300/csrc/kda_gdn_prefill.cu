@@ -8,7 +8,7 @@
 // with its scalar gate).  Unlike the channel-wise gate, the scalar one multiplies the Gram matrices
 // afterwards, so every product has the raw bf16 k or q as one operand, and the decays enter as
 // exponentials of differences: no lower limit on log_decay, and fp32 accuracy when the other operand
-// (state, right-hand side, U) is split into two bf16 terms, x = hi + lo with |x - hi - lo| <= 2^-18 |x|.
+// (state, right-hand side, U) is split into two bf16 terms, x = hi + lo with |x - hi - lo| <= 2^-17 |x|.
 //
 // pass 0  chunk table (launch_chunk_table)
 // pass 1  one CTA per (chunk, value head): Gram matrices, T, P, decays -> an image in the workspace
@@ -37,8 +37,8 @@ constexpr int kPrepThreads = 128;
 
 struct PrepSmem {
     static constexpr uint32_t K = 0, Q = 16384;  // 2 x [64][128 B] each, 128B-swizzled
-    static constexpr uint32_t AH = 0;            // A's and the diagonal inverses' two terms: [64][128 B] bf16
-    static constexpr uint32_t AL = 8192;         // (over K and Q once the Gram matrices are out)
+    static constexpr uint32_t AH = 0;            // two terms of A's blocks, the diagonal ones inverted (over K and
+    static constexpr uint32_t AL = kTriBytes;    // Q once the Gram matrices are out)
     static constexpr uint32_t DG = 16384;        // f32 [4][16][17]: diagonal blocks of A
     static constexpr uint32_t G = 32768;         // f32 [3][64]: g (two terms, base 2), beta
     static constexpr uint32_t BAR = G + 3 * C * 4;
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
             }
         }
     }
-    const uint32_t ah_base = smem_u32(sm + L::AH), al_base = smem_u32(sm + L::AL);
+    const uint32_t ah_base = smem_u32(sm + L::AH) + 16 * lane, al_base = smem_u32(sm + L::AL) + 16 * lane;
     float* const dg = reinterpret_cast<float*>(sm + L::DG);
     for (int hh = 0; hh < hp; ++hh) {
         const int h = h0 + hh;
@@ -198,12 +198,17 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
                 const int jj = 8 * n + 2 * t;
                 const bool row = i < Lc;
                 const float d0 = exp2_sfu((gi - ch.x) + (gl - cl.x)), d1 = exp2_sfu((gi - ch.y) + (gl - cl.y));
+                const uint32_t pair = blk_pair(g, e2, n & 1, t);
                 const float p0 = row && jj <= i ? d0 * qk[n][2 * e2] : 0.f;
                 const float p1 = row && jj + 1 <= i ? d1 * qk[n][2 * e2 + 1] : 0.f;
                 uint32_t ph, pl;
                 split2(p0, p1, ph, pl);
-                *reinterpret_cast<uint32_t*>(img + kImgP + sw128_chunk(i, n) + 4 * t) = ph;
-                if (bwd) *reinterpret_cast<uint32_t*>(img + kImgPl + sw128_chunk(i, n) + 4 * t) = pl;
+                uint8_t* const pp = img + tri_blk(mr, n >> 1) + pair;
+                *reinterpret_cast<uint32_t*>(pp + kImgP) = ph;
+                if (bwd) {
+                    *reinterpret_cast<uint32_t*>(pp + kImgPl) = pl;
+                    *reinterpret_cast<uint32_t*>(pp + kImgPl2) = third2(p0, p1, ph, pl);
+                }
                 const float a0 = row && jj < i ? b * d0 * kk[n][2 * e2] : 0.f;
                 const float a1 = row && jj + 1 < i ? b * d1 * kk[n][2 * e2 + 1] : 0.f;
                 if ((n >> 1) == mr) {
@@ -213,8 +218,9 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
                 } else {
                     uint32_t hi, lo;
                     split2(a0, a1, hi, lo);
-                    *reinterpret_cast<uint32_t*>(sm + L::AH + sw128_chunk(i, n) + 4 * t) = hi;
-                    *reinterpret_cast<uint32_t*>(sm + L::AL + sw128_chunk(i, n) + 4 * t) = lo;
+                    uint8_t* const ap = sm + tri_blk(mr, n >> 1) + pair;
+                    *reinterpret_cast<uint32_t*>(ap + L::AH) = hi;
+                    *reinterpret_cast<uint32_t*>(ap + L::AL) = lo;
                 }
             }
         }
@@ -235,7 +241,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const uint32_t off = sw128_chunk(16 * b + i, 2 * b + (c >> 3)) + 2 * (c & 7);
+                const uint32_t off = tri_blk(b, b) + blk_pair(i & 7, i >> 3, c >> 3, 0) + 2 * (c & 7);
                 const __nv_bfloat16 hi = __float2bfloat16_rn(x[i]);
                 *reinterpret_cast<__nv_bfloat16*>(sm + L::AH + off) = hi;
                 *reinterpret_cast<__nv_bfloat16*>(sm + L::AL + off) = __float2bfloat16_rn(x[i] - __bfloat162float(hi));
@@ -245,13 +251,11 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
         // Block column w of the inverse by warp w.  T_ww = D_w from shared memory, the others from the products.
         {
             const int w = mr;
-            const int lr = lane & 15, lc = lane >> 4;
-            const int tr = (lane & 7) + (((lane >> 3) & 1) << 3), tc = lane >> 4;
             BTerms T[4][2];  // blocks (k, w) as B operands, two 8-column halves
             {
                 uint32_t bh[4], bl[4];
-                ldsm4t(bh, ah_base + sw128_chunk(16 * w + tr, 2 * w + tc));
-                ldsm4t(bl, al_base + sw128_chunk(16 * w + tr, 2 * w + tc));
+                ldsm4t(bh, ah_base + tri_blk(w, w));
+                ldsm4t(bl, al_base + tri_blk(w, w));
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -265,9 +269,9 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
                     for (int e2 = 0; e2 < 2; ++e2) {
                         uint32_t hi, lo;
                         split2(x[n][2 * e2], x[n][2 * e2 + 1], hi, lo);
-                        const uint32_t off = sw128_chunk(16 * i + g + 8 * e2, 2 * w + n) + 4 * t;
-                        *reinterpret_cast<uint32_t*>(img + kImgTh + off) = hi;
-                        *reinterpret_cast<uint32_t*>(img + kImgTl + off) = lo;
+                        uint8_t* const tp = img + tri_blk(i, w) + blk_pair(g, e2, n, t);
+                        *reinterpret_cast<uint32_t*>(tp + kImgTh) = hi;
+                        *reinterpret_cast<uint32_t*>(tp + kImgTl) = lo;
                     }
             };
             {  // the diagonal block itself, as accumulators hold it
@@ -276,7 +280,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
                     for (int e2 = 0; e2 < 2; ++e2) {
-                        const uint32_t off = sw128_chunk(16 * w + g + 8 * e2, 2 * w + n) + 4 * t;
+                        const uint32_t off = tri_blk(w, w) + blk_pair(g, e2, n, t);
                         const float2 hi = unpack_bf16(*reinterpret_cast<const uint32_t*>(sm + L::AH + off));
                         const float2 lo = unpack_bf16(*reinterpret_cast<const uint32_t*>(sm + L::AL + off));
                         x[n][2 * e2] = hi.x + lo.x;
@@ -296,8 +300,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
 #pragma unroll
                 for (int k = 0; k < 3; ++k) {
                     if (k < w || k >= i) continue;
-                    ldsm4(ah, ah_base + sw128_chunk(16 * i + lr, 2 * k + lc));
-                    ldsm4(al, al_base + sw128_chunk(16 * i + lr, 2 * k + lc));
+                    ldsm4(ah, ah_base + tri_blk(i, k));
+                    ldsm4(al, al_base + tri_blk(i, k));
 #pragma unroll
                     for (int n = 0; n < 2; ++n) mma16(x[n], ah, T[k][n].h0, T[k][n].h1);
 #pragma unroll
@@ -314,8 +318,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
                 }
-                ldsm4(ah, ah_base + sw128_chunk(16 * i + lr, 2 * i + lc));
-                ldsm4(al, al_base + sw128_chunk(16 * i + lr, 2 * i + lc));
+                ldsm4(ah, ah_base + tri_blk(i, i));
+                ldsm4(al, al_base + tri_blk(i, i));
 #pragma unroll
                 for (int n = 0; n < 2; ++n) mma16(x[n], ah, X[n].h0, X[n].h1);
 #pragma unroll
@@ -338,12 +342,12 @@ struct ScanCfg {
     static constexpr int kThreads = 32 * (NW + 1);
     static constexpr uint32_t kVRow = kCols >= 64 ? 128 : kCols * 2;  // bytes of a v row in a block
     static constexpr int kVBlocks = kCols >= 64 ? kCols / 64 : 1;
-    static constexpr uint32_t K = 0, Q = 16384, IMG = 32768, V = IMG + 26624;
+    static constexpr uint32_t K = 0, Q = 16384, IMG = 32768, V = IMG + 16384;
     static constexpr uint32_t STAGE = V + C * kVRow * kVBlocks;
     static constexpr uint32_t BARS = ST * STAGE;  // full[ST], empty[ST]
     static constexpr uint32_t ABORT = BARS + 16 * ST;
     static constexpr uint32_t ALLOC = ABORT + 16 + 1024;
-    static_assert(STAGE % 1024 == 0 && ALLOC <= 232448, "stages");
+    static_assert(STAGE % 1024 == 0 && ALLOC <= 232448 && kImgScanBytes <= 16384, "stages");
 };
 
 // REC: the gradient's walk, which leaves every chunk's start state and U in two bf16 terms and no outputs.
@@ -449,7 +453,7 @@ __global__ void __launch_bounds__(ScanCfg<NT, NW, ST>::kThreads, 1)
                         make_uint4(0u, 0u, 0u, 0u);
                 __syncwarp();
             }
-            const uint32_t kb = smem_u32(st + L::K), qb = smem_u32(st + L::Q), ib = smem_u32(st + L::IMG);
+            const uint32_t kb = smem_u32(st + L::K), qb = smem_u32(st + L::Q), ib = smem_u32(st + L::IMG) + 16 * lane;
             const float* gs = reinterpret_cast<const float*>(st + L::IMG + kImgG);
             uint8_t* const rec = REC ? records + (static_cast<size_t>(jb + c) * Hv + h) * kRecStride : nullptr;
             const int rcol = slice * L::kCols + wc + 2 * t;
@@ -492,6 +496,7 @@ __global__ void __launch_bounds__(ScanCfg<NT, NW, ST>::kThreads, 1)
             // R = b (V - e^g K S); Q S runs beside it, a quarter for each 16 rows of R
             float eg[4][2], be[2];
             BTerms r[4][NT];
+            uint32_t r2[REC ? 4 : 1][NT][2];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
 #pragma unroll
@@ -514,7 +519,14 @@ __global__ void __launch_bounds__(ScanCfg<NT, NW, ST>::kThreads, 1)
                         x[2 * e + 1] = be[e] * fmaf(-eg[k][e], ks[k][n][2 * e + 1], __uint_as_float(vv & 0xffff0000u));
                         if (row >= Lc) x[2 * e] = x[2 * e + 1] = 0.f;
                     }
-                    r[k][n] = b_terms(x);
+                    if constexpr (REC) {
+                        const BTerms3 x3 = b_terms3(x);
+                        r[k][n] = x3.b;
+                        r2[k][n][0] = x3.m0;
+                        r2[k][n][1] = x3.m1;
+                    } else {
+                        r[k][n] = b_terms(x);
+                    }
                 }
 #pragma unroll
                 for (int kq = 2 * k; kq < (REC ? 0 : 2 * k + 2); ++kq) {
@@ -541,13 +553,19 @@ __global__ void __launch_bounds__(ScanCfg<NT, NW, ST>::kThreads, 1)
                 uint32_t ah[4][4], al[4][4];
 #pragma unroll
                 for (int m = k; m < 4; ++m) {
-                    ldsm4(ah[m], ib + kImgTh + sw128_chunk(16 * m + lr, 2 * k + lc));
-                    ldsm4(al[m], ib + kImgTl + sw128_chunk(16 * m + lr, 2 * k + lc));
+                    ldsm4(ah[m], ib + kImgTh + tri_blk(m, k));
+                    ldsm4(al[m], ib + kImgTl + tri_blk(m, k));
                 }
 #pragma unroll
                 for (int m = k; m < 4; ++m)
 #pragma unroll
                     for (int n = 0; n < NT; ++n) mma16(u[m][n], ah[m], r[k][n].h0, r[k][n].h1);
+                if constexpr (REC) {  // the gradient of b takes U . W: the right-hand side in three terms
+#pragma unroll
+                    for (int m = k; m < 4; ++m)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma16(u[m][n], ah[m], r2[k][n][0], r2[k][n][1]);
+                }
 #pragma unroll
                 for (int m = k; m < 4; ++m)
 #pragma unroll
@@ -613,7 +631,7 @@ __global__ void __launch_bounds__(ScanCfg<NT, NW, ST>::kThreads, 1)
 #pragma unroll
                     for (int m = k; m < 4; ++m) {
                         uint32_t a[4];
-                        ldsm4(a, ib + kImgP + sw128_chunk(16 * m + lr, 2 * k + lc));
+                        ldsm4(a, ib + kImgP + tri_blk(m, k));
 #pragma unroll
                         for (int n = 0; n < NT; ++n) mma16(qs[m][n], a, b0[n], b1[n]);
                     }

@@ -1,9 +1,9 @@
 """Gradient of the gated delta rule on the GPU against the fp64 oracle's (the KDA gradient with the decay
 broadcast: its log_alpha gradient summed over channels, q and k gradients summed over a group's heads).
 
-Tolerances.  A product has at most two operands in two bf16 terms, each off by at most 2^-18 of the value; ten
+Tolerances.  A product has at most two operands in two bf16 terms, each off by at most 2^-17 of the value; ten
 products at most lie between an input and a gradient (K S, T R, K^T U, K X, T^T dU, Q^T dO, K^T W and the three
-of the last step): 20 x 2^-18, spread evenly to F32 = 20 x 2^-18 / sqrt(3) of the 2-norm of what they make, the
+of the last step): 20 x 2^-17, spread evenly to F32 = 20 x 2^-17 / sqrt(3) of the 2-norm of what they make, the
 states S and their adjoints G among it.  grad_S0 is held to that.  grad_log_decay = <G, S> and grad_beta =
 (G^T k) . e are inner products whose terms cancel: an error of F32 |G| in G has no preferred direction among its
 128 x 128, and is felt in them as F32 |G| |S| / 128 (F32 |G| |e| / 128, F32 |S| |G^T k| / 128) in the mean; 8 times
@@ -22,7 +22,7 @@ from tests.test_gpu_gdn import inputs
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not cuda_ok(), reason="needs a CUDA GPU")]
 
-F32 = 20 * 2.0 ** -18 / 3 ** 0.5
+F32 = 20 * 2.0 ** -17 / 3 ** 0.5
 BF16 = 4 * 2.0 ** -8 / 3 ** 0.5
 NAMES = ("q", "k", "v", "log_decay", "beta", "S0")
 
