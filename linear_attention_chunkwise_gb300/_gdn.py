@@ -14,10 +14,19 @@ from . import _binding as _b
 _NORM_OUT = {None: (_b.KDA_NORM_OUT_SAME, None), "e4m3": (_b.KDA_NORM_OUT_E4M3, torch.float8_e4m3fn),
              "int8": (_b.KDA_NORM_OUT_INT8, torch.int8)}
 _same_device = contextlib.nullcontext()
+# the current stream's handle without the Stream object that torch.cuda.current_stream makes of it (2 us)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _check(t, name, dtype, shape, dev):
     """t: a contiguous CUDA tensor of this type, shape and device."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
+            and t.is_contiguous()):
+        _refuse(t, name, dtype, shape, dev)
+
+
+def _refuse(t, name, dtype, shape, dev):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -28,8 +37,7 @@ def _check(t, name, dtype, shape, dev):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _first(t, name, dims):
@@ -55,7 +63,7 @@ def _on(dev):
 def _stream(stream, dev, *mine):
     """The stream's handle; tensors that this call allocated are kept alive on a stream of the caller's."""
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return _current_stream(dev.index)
     if stream.device != dev:
         raise ValueError(f"stream is on {stream.device}, expected {dev}")
     for t in mine:

@@ -32,4 +32,16 @@ inline bool sizes_ok(int64_t a, int64_t b, int64_t c, int64_t d) {
 
 inline size_t esize_of(kda_dtype t) { return t == KDA_DTYPE_F32 ? 4 : 2; }
 
+// Lets a kernel have `bytes` of dynamic shared memory (48 KB need no leave), on first use per device.
+template <typename K>
+inline cudaError_t set_smem(K kernel, uint32_t bytes, int* configured) {
+    if (bytes <= 48 * 1024) return cudaSuccess;
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess || (dev >= 0 && dev < 64 && configured[dev])) return err;
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (err == cudaSuccess && dev >= 0 && dev < 64) configured[dev] = 1;
+    return err;
+}
+
 }  // namespace kda

@@ -128,15 +128,5 @@ __device__ __forceinline__ BTerms3 b_terms3(const float (&c)[4]) {
     return r;
 }
 
-template <typename K>
-inline cudaError_t set_smem(K kernel, uint32_t bytes, int* configured) {  // on first use per device
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err != cudaSuccess || (dev >= 0 && dev < 64 && configured[dev])) return err;
-    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-    if (err == cudaSuccess && dev >= 0 && dev < 64) configured[dev] = 1;
-    return err;
-}
-
 }  // namespace gdn
 }  // namespace kda
