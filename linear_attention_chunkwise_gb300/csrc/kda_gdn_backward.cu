@@ -469,9 +469,11 @@ __global__ void __launch_bounds__(kRestThreads, 1)
         }
         ok = mbar_wait_pipe(&bars[1], par) && ok;
         __syncthreads();  // the vectors (and the cleared rows) are there
-        float eg[2], eo[2], be[2];
+        float eg[2], eo[2], be[2], gh[2], gl[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+            gh[e] = gs[kVecGh + 16 * mr + g + 8 * e];
+            gl[e] = gs[kVecGl + 16 * mr + g + 8 * e];
             eg[e] = gs[kVecEg + 16 * mr + g + 8 * e];
             eo[e] = gs[kVecEo + 16 * mr + g + 8 * e];
             be[e] = gs[kVecB + 16 * mr + g + 8 * e];
@@ -596,120 +598,146 @@ __global__ void __launch_bounds__(kRestThreads, 1)
             }
         }
         if (lane == 0) parts[kPtI + warp] = inner;
-        {  // the 64 x 64 products: dP = dO U^T with Q K^T, or W U^T with K K^T
-            float a1[8][4], kk[8][4];
+        // The 64 x 64 products, 32 columns (two blocks) at a time: dP = dO U^T with Q K^T, or W U^T with K K^T.
+        float left[2] = {0.f, 0.f};  // of rows g and g + 8: the sums of the columns so far
+#pragma unroll 1
+        for (int ph = 0; ph < 2; ++ph) {
+            if (2 * ph > mr) {  // above the diagonal
+                if (g == 0) {
 #pragma unroll
-            for (int n = 0; n < 8; ++n)
+                    for (int n = 0; n < 4; ++n)
+                        *reinterpret_cast<float2*>(parts + kPtC + 64 * warp + 32 * ph + 8 * n + 2 * t) = make_float2(0.f, 0.f);
+                }
+                continue;
+            }
+            float a1[4][4], kk[4][4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) a1[n][e] = kk[n][e] = 0.f;
+            if (nh) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                uint32_t wh[4], wl[4], ga[4];
-                if (nh) {
-                    const uint32_t wa = base + L::W + (k >> 2) * 8192 + sw128_chunk(16 * mr + lr, 2 * (k & 3) + lc);
-                    ldsm4(wh, wa);
-                    ldsm4(wl, wa + 16384);
-                }
-                ldsm4(ga, base + (nh ? L::K : L::Q) + (k >> 2) * 8192 + sw128_chunk(16 * mr + lr, 2 * (k & 3) + lc));
+                for (int k = 0; k < 8; ++k) {
+                    uint32_t wh[4], wl[4], ga[4];
+                    const uint32_t aoff = (k >> 2) * 8192 + sw128_chunk(16 * mr + lr, 2 * (k & 3) + lc);
+                    ldsm4(wh, base + L::W + aoff);
+                    ldsm4(wl, base + L::W + 16384 + aoff);
+                    ldsm4(ga, base + L::K + aoff);
 #pragma unroll
-                for (int np = 0; np < 4; ++np) {
-                    if (np > mr) break;
-                    uint32_t uh[4], ul[4], kf[4];
-                    const uint32_t off = (k >> 2) * 8192 + sw128_chunk(16 * np + br, 2 * (k & 3) + bc);
-                    ldsm4(uh, base + L::U + off);
-                    ldsm4(ul, base + L::U + 16384 + off);
-                    ldsm4(kf, base + L::K + off);
+                    for (int np = 0; np < 2; ++np) {
+                        uint32_t uh[4], ul[4], kf[4];
+                        const uint32_t off = (k >> 2) * 8192 + sw128_chunk(32 * ph + 16 * np + br, 2 * (k & 3) + bc);
+                        ldsm4(uh, base + L::U + off);
+                        ldsm4(ul, base + L::U + 16384 + off);
+                        ldsm4(kf, base + L::K + off);
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        mma16(kk[2 * np + n], ga, kf[2 * n], kf[2 * n + 1]);
-                        if (nh) {
+                        for (int n = 0; n < 2; ++n) {
+                            mma16(kk[2 * np + n], ga, kf[2 * n], kf[2 * n + 1]);
                             mma16(a1[2 * np + n], wh, uh[2 * n], uh[2 * n + 1]);
                             mma16(a1[2 * np + n], wh, ul[2 * n], ul[2 * n + 1]);
                             mma16(a1[2 * np + n], wl, uh[2 * n], uh[2 * n + 1]);
-                        } else {
+                        }
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    uint32_t ga[4];
+                    ldsm4(ga, base + L::Q + (k >> 2) * 8192 + sw128_chunk(16 * mr + lr, 2 * (k & 3) + lc));
+#pragma unroll
+                    for (int np = 0; np < 2; ++np) {
+                        uint32_t uh[4], ul[4], kf[4];
+                        const uint32_t off = (k >> 2) * 8192 + sw128_chunk(32 * ph + 16 * np + br, 2 * (k & 3) + bc);
+                        ldsm4(uh, base + L::U + off);
+                        ldsm4(ul, base + L::U + 16384 + off);
+                        ldsm4(kf, base + L::K + off);
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            mma16(kk[2 * np + n], ga, kf[2 * n], kf[2 * n + 1]);
                             mma16(a1[2 * np + n], dof[k], uh[2 * n], uh[2 * n + 1]);
                             mma16(a1[2 * np + n], dof[k], ul[2 * n], ul[2 * n + 1]);
                         }
                     }
                 }
             }
-            float left[2] = {0.f, 0.f};  // of rows g and g + 8: the sums of the tiles so far
+            // M or E, and the pairs' sums: over rows i >= t of the sums over columns j < t
+            const float sgn = nh ? -1.f : 1.f;
 #pragma unroll
-            for (int n = 0; n < 8; ++n) {
-                float cs[2] = {0.f, 0.f};  // over rows i >= t of the sums over columns j < t, t = 8 n + 2 t (+ 1)
-                if (n <= 2 * mr + 1) {
-                    const float2 ch = *reinterpret_cast<const float2*>(gs + kVecGh + 8 * n + 2 * t);
-                    const float2 cl = *reinterpret_cast<const float2*>(gs + kVecGl + 8 * n + 2 * t);
+            for (int n = 0; n < 4; ++n) {
+                float cs[2] = {0.f, 0.f};
+                const int jj = 32 * ph + 8 * n + 2 * t;
+                const float2 ch = *reinterpret_cast<const float2*>(gs + kVecGh + jj);
+                const float2 cl = *reinterpret_cast<const float2*>(gs + kVecGl + jj);
 #pragma unroll
-                    for (int e2 = 0; e2 < 2; ++e2) {
-                        const int i = 16 * mr + g + 8 * e2, jj = 8 * n + 2 * t;
-                        const float gh = gs[kVecGh + i], gl = gs[kVecGl + i];
-                        float m[2], d[2];
+                for (int e2 = 0; e2 < 2; ++e2) {
+                    const int i = 16 * mr + g + 8 * e2;
+                    const int last = i < Lc ? i - nh : -1;  // columns up to this one count
+                    const float f = nh ? be[e2] : 1.f;
+                    float m[2], d[2];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float x = (gh - (e ? ch.y : ch.x)) + (gl - (e ? cl.y : cl.x));
-                            const bool in = i < Lc && (nh ? jj + e < i : jj + e <= i);
-                            float gam = in ? exp2_sfu(x) : 0.f;
-                            float v = a1[n][2 * e2 + e];
-                            if (nh) {
-                                if (jj + e == i) parts[kPtB + i] = v / be[e2];
-                                v = -v;
-                                gam *= be[e2];
-                            }
-                            d[e] = in ? v * (gam * kk[n][2 * e2 + e]) : 0.f;
-                            m[e] = in ? gam * v : 0.f;
-                        }
-                        float sum = d[0] + d[1];  // of the lanes up to this one in the row
-                        float y = __shfl_up_sync(0xffffffffu, sum, 1, 4);
-                        if (t >= 1) sum += y;
-                        y = __shfl_up_sync(0xffffffffu, sum, 2, 4);
-                        if (t >= 2) sum += y;
-                        y = __shfl_up_sync(0xffffffffu, sum, 1, 4);
-                        const float before = left[e2] + (t >= 1 ? y : 0.f);
-                        left[e2] += __shfl_sync(0xffffffffu, sum, 3, 4);
-                        if (jj <= i) cs[0] += before;
-                        if (jj + 1 <= i) cs[1] += before + d[0];
-                        *reinterpret_cast<uint32_t*>(sm + (nh ? L::E : L::M) + sw128_chunk(i, n) + 4 * t) = pack_bf16(m[0], m[1]);
+                    for (int e = 0; e < 2; ++e) {
+                        const float x = (gh[e2] - (e ? ch.y : ch.x)) + (gl[e2] - (e ? cl.y : cl.x));
+                        const bool in = jj + e <= last;
+                        const float gam = f * exp2_sfu(in ? x : 0.f);
+                        const float v = sgn * a1[n][2 * e2 + e];
+                        if (nh && jj + e == i) parts[kPtB + i] = a1[n][2 * e2 + e] / be[e2];
+                        d[e] = in ? v * (gam * kk[n][2 * e2 + e]) : 0.f;
+                        m[e] = in ? gam * v : 0.f;
                     }
+                    float sum = d[0] + d[1];  // of the lanes up to this one in the row
+                    float y = __shfl_up_sync(0xffffffffu, sum, 1, 4);
+                    if (t >= 1) sum += y;
+                    y = __shfl_up_sync(0xffffffffu, sum, 2, 4);
+                    if (t >= 2) sum += y;
+                    y = __shfl_up_sync(0xffffffffu, sum, 1, 4);
+                    const float before = left[e2] + (t >= 1 ? y : 0.f);
+                    left[e2] += __shfl_sync(0xffffffffu, sum, 3, 4);
+                    if (jj <= i) cs[0] += before;
+                    if (jj + 1 <= i) cs[1] += before + d[0];
+                    *reinterpret_cast<uint32_t*>(sm + (nh ? L::E : L::M) + sw128_chunk(i, 4 * ph + n) + 4 * t) =
+                        pack_bf16(m[0], m[1]);
                 }
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                    for (int off = 4; off < 32; off <<= 1) cs[e] += __shfl_xor_sync(0xffffffffu, cs[e], off);
+                for (int off = 4; off < 32; off <<= 1) {
+                    cs[0] += __shfl_xor_sync(0xffffffffu, cs[0], off);
+                    cs[1] += __shfl_xor_sync(0xffffffffu, cs[1], off);
                 }
-                if (g == 0) *reinterpret_cast<float2*>(parts + kPtC + 64 * warp + 8 * n + 2 * t) = make_float2(cs[0], cs[1]);
+                if (g == 0) *reinterpret_cast<float2*>(parts + kPtC + 64 * warp + jj) = make_float2(cs[0], cs[1]);
             }
         }
         __syncthreads();
-        // dq += M K, dk += (E + E^T) K + M^T Q
+        // dq += M K, dk += E K (columns up to the own rows), dk += E^T K + M^T Q (rows from the own columns on)
+#pragma unroll 1
+        for (int k = 0; k <= mr; ++k) {
+            uint32_t am[4], ae[4];
+            ldsm4(am, base + L::M + sw128_chunk(16 * mr + lr, 2 * k + lc));
+            ldsm4(ae, base + L::E + sw128_chunk(16 * mr + lr, 2 * k + lc));
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            uint32_t am[4], ae[4], tm[4], te[4];
-            const bool below = k <= mr, above = k >= mr;
-            if (below) {
-                ldsm4(am, base + L::M + sw128_chunk(16 * mr + lr, 2 * k + lc));
-                ldsm4(ae, base + L::E + sw128_chunk(16 * mr + lr, 2 * k + lc));
+            for (int np = 0; np < 4; ++np) {
+                uint32_t kf[4];
+                ldsm4t(kf, base + L::K + nh * 8192 + sw128_chunk(16 * k + kr, 2 * np + kc));
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    mma16(dq[2 * np + n], am, kf[2 * n], kf[2 * n + 1]);
+                    mma16(dk[2 * np + n], ae, kf[2 * n], kf[2 * n + 1]);
+                }
             }
-            if (above) {
-                ldsm4t(tm, base + L::M + sw128_chunk(16 * k + br, 2 * mr + bc));
-                ldsm4t(te, base + L::E + sw128_chunk(16 * k + br, 2 * mr + bc));
-            }
+        }
+#pragma unroll 1
+        for (int k = mr; k < 4; ++k) {
+            uint32_t tm[4], te[4];
+            ldsm4t(tm, base + L::M + sw128_chunk(16 * k + br, 2 * mr + bc));
+            ldsm4t(te, base + L::E + sw128_chunk(16 * k + br, 2 * mr + bc));
 #pragma unroll
             for (int np = 0; np < 4; ++np) {
                 uint32_t kf[4], qf[4];
                 const uint32_t off = nh * 8192 + sw128_chunk(16 * k + kr, 2 * np + kc);
                 ldsm4t(kf, base + L::K + off);
-                if (above) ldsm4t(qf, base + L::Q + off);
+                ldsm4t(qf, base + L::Q + off);
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    if (below) {
-                        mma16(dq[2 * np + n], am, kf[2 * n], kf[2 * n + 1]);
-                        mma16(dk[2 * np + n], ae, kf[2 * n], kf[2 * n + 1]);
-                    }
-                    if (above) {
-                        mma16(dk[2 * np + n], te, kf[2 * n], kf[2 * n + 1]);
-                        mma16(dk[2 * np + n], tm, qf[2 * n], qf[2 * n + 1]);
-                    }
+                    mma16(dk[2 * np + n], te, kf[2 * n], kf[2 * n + 1]);
+                    mma16(dk[2 * np + n], tm, qf[2 * n], qf[2 * n + 1]);
                 }
             }
         }
