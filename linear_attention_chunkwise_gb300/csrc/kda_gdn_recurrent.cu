@@ -116,16 +116,45 @@ __global__ void __launch_bounds__(kDecThreads, 2)
 // The state's columns never mix, so a CTA takes 16 of them for one (sequence, value head): 8 lanes
 // hold a column, 16 rows each (rows 4 (8 i + part) .. + 3, i = 0..3, so that the 8 lanes of a column
 // read 128 consecutive bytes of a k or q row, and the warp's other columns the same ones).  A token
-// is a chain of about 80 multiply-adds, three shuffles and the update, with no barrier; the rows of
-// kTB tokens are staged at a time, the next ones in flight meanwhile.
+// is a chain of multiply-adds, three shuffles and the update, with no barrier; the rows of kTB tokens
+// are staged at a time, with their k . q, the next ones in flight meanwhile.  Bound by instructions
+// issued, so the arithmetic is on pairs of floats (512 fp32 tokens x 32 heads: 158 us with single
+// ones and k . q in every lane, 163 instructions a token and warp).
 constexpr int kTB = 16;          // tokens staged at a time
 constexpr int kRecThreads = 128;
 constexpr int kRecCols = 16;     // state columns of a CTA
 
+// Two floats in a 64-bit register.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float sum_pair(uint64_t p) {
+    float x, y;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
+    return x + y;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 template <typename IoT>
 __global__ void __launch_bounds__(kRecThreads) kda_gdn_recurrent_kernel(const GdnArgs a) {
     __shared__ __align__(16) float k_s[2][kTB][D], q_s[2][kTB][D], v_s[2][kTB][kRecCols];
-    __shared__ float a_s[2][kTB], b_s[2][kTB];
+    __shared__ float4 g_s[2][kTB];  // decay, beta, k . q
     const int tid = threadIdx.x, part = tid & 7, col = tid >> 3;
     constexpr int NSL = D / kRecCols;
     const int slice = blockIdx.x % NSL;
@@ -142,11 +171,12 @@ __global__ void __launch_bounds__(kRecThreads) kda_gdn_recurrent_kernel(const Gd
     const IoT* const k = static_cast<const IoT*>(a.k);
     const IoT* const v = static_cast<const IoT*>(a.v);
 
-    float S[16];
+    uint64_t S[8];  // rows 4 (8 (i / 2) + part) + 2 (i % 2) and the next
     const size_t st = ((static_cast<size_t>(n) * a.Hv + h) * D) * D + j0 + col;
+    auto row_of = [&](int i) { return static_cast<size_t>(4 * (8 * (i >> 1) + part) + 2 * (i & 1)); };
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        S[i] = a.S0 ? a.S0[st + static_cast<size_t>(4 * (8 * (i >> 2) + part) + (i & 3)) * D] : 0.f;
+    for (int i = 0; i < 8; ++i)
+        S[i] = a.S0 ? pair(a.S0[st + row_of(i) * D], a.S0[st + (row_of(i) + 1) * D]) : 0ull;
 
     // this thread's share of a batch of rows: four quads of k and of q, two values of v, one gate
     float4 kr[4], qr[4];
@@ -178,12 +208,16 @@ __global__ void __launch_bounds__(kRecThreads) kda_gdn_recurrent_kernel(const Gd
             const int r = (tid + e * kRecThreads) >> 5, c = 4 * (tid & 31);
             *reinterpret_cast<float4*>(&k_s[buf][r][c]) = kr[e];
             *reinterpret_cast<float4*>(&q_s[buf][r][c]) = qr[e];
+            float kq = fmaf(kr[e].x, qr[e].x, fmaf(kr[e].y, qr[e].y, fmaf(kr[e].z, qr[e].z, kr[e].w * qr[e].w)));
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) kq += __shfl_xor_sync(0xffffffffu, kq, off);
+            if (c == 0) g_s[buf][r].z = kq;  // a warp holds whole rows
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) v_s[buf][(tid + e * kRecThreads) >> 4][tid & 15] = vr[e];
         if (tid < kTB) {
-            a_s[buf][tid] = expf(ar);
-            b_s[buf][tid] = br;
+            g_s[buf][tid].x = expf(ar);
+            g_s[buf][tid].y = br;
         }
     };
     if (t_begin < t_end) fetch(t_begin);
@@ -193,43 +227,48 @@ __global__ void __launch_bounds__(kRecThreads) kda_gdn_recurrent_kernel(const Gd
         __syncthreads();  // the other buffer's readers are past it too
         if (t0 + kTB < t_end) fetch(t0 + kTB);
         const int nt = static_cast<int>(t_end - t0 < kTB ? t_end - t0 : kTB);
+#pragma unroll 2
         for (int t = 0; t < nt; ++t) {
-            float4 kk[4];
-            float y[4] = {0.f, 0.f, 0.f, 0.f}, p[4] = {0.f, 0.f, 0.f, 0.f}, kq[4] = {0.f, 0.f, 0.f, 0.f};
+            uint64_t kk[8], y[2] = {0ull, 0ull}, p[2] = {0ull, 0ull};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                kk[i] = *reinterpret_cast<const float4*>(&k_s[buf][t][4 * (8 * i + part)]);
-                const float4 qq = *reinterpret_cast<const float4*>(&q_s[buf][t][4 * (8 * i + part)]);
-                y[i] = fmaf(kk[i].x, S[4 * i], fmaf(kk[i].y, S[4 * i + 1], fmaf(kk[i].z, S[4 * i + 2], kk[i].w * S[4 * i + 3])));
-                p[i] = fmaf(qq.x, S[4 * i], fmaf(qq.y, S[4 * i + 1], fmaf(qq.z, S[4 * i + 2], qq.w * S[4 * i + 3])));
-                kq[i] = fmaf(kk[i].x, qq.x, fmaf(kk[i].y, qq.y, fmaf(kk[i].z, qq.z, kk[i].w * qq.w)));
+                const ulonglong2 k2 = *reinterpret_cast<const ulonglong2*>(&k_s[buf][t][4 * (8 * i + part)]);
+                const ulonglong2 q2 = *reinterpret_cast<const ulonglong2*>(&q_s[buf][t][4 * (8 * i + part)]);
+                kk[2 * i] = k2.x;
+                kk[2 * i + 1] = k2.y;
+                y[0] = fma2(k2.x, S[2 * i], y[0]);
+                y[1] = fma2(k2.y, S[2 * i + 1], y[1]);
+                p[0] = fma2(q2.x, S[2 * i], p[0]);
+                p[1] = fma2(q2.y, S[2 * i + 1], p[1]);
             }
-            float ys = (y[0] + y[1]) + (y[2] + y[3]), ps = (p[0] + p[1]) + (p[2] + p[3]);
-            float kqs = (kq[0] + kq[1]) + (kq[2] + kq[3]);
+            const float4 gv = g_s[buf][t];
+            const float vv = v_s[buf][t][col];
+            const uint64_t al = pair(gv.x, gv.x);
+            float ys = sum_pair(add2(y[0], y[1])), ps = sum_pair(add2(p[0], p[1]));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) S[i] = mul2(al, S[i]);
 #pragma unroll
             for (int off = 4; off > 0; off >>= 1) {
                 ys += __shfl_xor_sync(0xffffffffu, ys, off);
                 ps += __shfl_xor_sync(0xffffffffu, ps, off);
-                kqs += __shfl_xor_sync(0xffffffffu, kqs, off);
             }
-            const float al = a_s[buf][t];
-            const float u = b_s[buf][t] * (v_s[buf][t][col] - al * ys);
+            const float u = gv.y * (vv - gv.x * ys);
+            const uint64_t uu = pair(u, u);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                S[4 * i] = fmaf(kk[i].x, u, al * S[4 * i]);
-                S[4 * i + 1] = fmaf(kk[i].y, u, al * S[4 * i + 1]);
-                S[4 * i + 2] = fmaf(kk[i].z, u, al * S[4 * i + 2]);
-                S[4 * i + 3] = fmaf(kk[i].w, u, al * S[4 * i + 3]);
-            }
+            for (int i = 0; i < 8; ++i) S[i] = fma2(kk[i], uu, S[i]);
             if (part == 0)
                 st_f32(static_cast<IoT*>(a.o) + (static_cast<size_t>(t0 + t) * a.Hv + h) * D + j0 + col,
-                       fmaf(kqs, u, al * ps));
+                       fmaf(gv.z, u, gv.x * ps));
         }
     }
     if (a.S_final) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            a.S_final[st + static_cast<size_t>(4 * (8 * (i >> 2) + part) + (i & 3)) * D] = S[i];
+        for (int i = 0; i < 8; ++i) {
+            float x, y;
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(S[i]));
+            a.S_final[st + row_of(i) * D] = x;
+            a.S_final[st + (row_of(i) + 1) * D] = y;
+        }
     }
 }
 
