@@ -34,6 +34,11 @@ kda_status gdn_shape(kda_dtype t, int64_t rows, int32_t states, int32_t Hk, int3
     return KDA_OK;
 }
 
+bool qk_maps(const kda::GdnArgs& a, CUtensorMap* tm_q, CUtensorMap* tm_k) {
+    return kda::make_tensor_map(tm_q, a.q, a.Hk, a.total_tokens, 64, kda::kChunk, CU_TENSOR_MAP_SWIZZLE_128B) &&
+           kda::make_tensor_map(tm_k, a.k, a.Hk, a.total_tokens, 64, kda::kChunk, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 // fp32 inputs and short sequences go token by token.
 bool chunked(kda_dtype t, int32_t num_seqs, int64_t total_tokens) {
     return t == KDA_DTYPE_BF16 && total_tokens > 16 * static_cast<int64_t>(num_seqs);
@@ -107,9 +112,11 @@ kda_status kda_gdn_prefill(const void* q, const void* k, const void* v, kda_dtyp
     if (chunked(qkv_dtype, num_seqs, total_tokens)) {
         kda::GdnWorkspace w;
         kda::gdn_workspace(num_seqs, total_tokens, Hv, false, static_cast<uint8_t*>(workspace), &w);
+        CUtensorMap tm_q, tm_k;
+        if (!qk_maps(a, &tm_q, &tm_k)) return KDA_ERR_CUDA;
         err = kda::launch_gdn_tables(a, w, s);
-        if (err == cudaSuccess) err = kda::launch_gdn_prep(a, w, s);
-        if (err == cudaSuccess) err = kda::launch_gdn_scan(a, w, s);
+        if (err == cudaSuccess) err = kda::launch_gdn_prep(a, w, tm_q, tm_k, s);
+        if (err == cudaSuccess) err = kda::launch_gdn_scan(a, w, tm_q, tm_k, s);
     } else {
         err = kda::launch_gdn_recurrent(qkv_dtype == KDA_DTYPE_F32, a, s);
     }
@@ -201,10 +208,11 @@ kda_status kda_gdn_prefill_backward(const void* q, const void* k, const void* v,
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     kda::GdnWorkspace w;
     kda::gdn_workspace(num_seqs, total_tokens, Hv, true, static_cast<uint8_t*>(workspace), &w);
+    CUtensorMap tm_q, tm_k;
+    if (!qk_maps(a, &tm_q, &tm_k)) return KDA_ERR_CUDA;
     cudaError_t err = kda::launch_gdn_tables(a, w, s);
-    if (err == cudaSuccess) err = kda::launch_gdn_prep(a, w, s);
-    if (err == cudaSuccess) err = kda::launch_gdn_scan(a, w, s);
-    if (err == cudaSuccess) err = kda::launch_gdn_backward(a, b, w, s);
+    if (err == cudaSuccess) err = kda::launch_gdn_prep(a, w, tm_q, tm_k, s);
+    if (err == cudaSuccess) err = kda::launch_gdn_backward(a, b, w, tm_q, tm_k, s);
     return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

@@ -15,341 +15,351 @@
 // (As the sums, from t on, of one gradient for each g_i it would need a difference of large sums; here a
 // decay of 0 gives exactly 0.)
 //
-// Kernels: the prefill's prep and its walk over the chunks (leaving S and U), a walk back (leaving X and
-// W, writing dv and the start state's gradient), and one CTA per (chunk, q/k head) for the rest, which adds
+// Kernels: the prefill's prep; a walk over the chunks (leaving S and U) and beside it one back (leaving X and
+// W, writing dv and the start state's gradient); and one CTA per (chunk, q/k head) for the rest, which adds
 // up the value heads of a group in its registers.  Operands that are not raw bf16 inputs are two bf16 terms
 // wherever the result is kept in fp32 (states, decays, b); M and E, which only reach the bf16 dq and dk,
 // are one.
-#include "kda_gdn_common.cuh"
+#include "kda_gdn_walk.cuh"
 
 namespace kda {
 namespace {
 
 using namespace gdn;
 
-// =========================================================== walk back ==
-template <int NT, int ST>
+// ============================================================== walks ==
+// Four warps walk forward and four back, each group with tiles and a copying thread of its own: a warp of
+// either is a chain that leaves the SM's issue slots and tensor cores half idle, and the two do not wait for
+// each other.  The copying warps' registers go to the walks': launched with 168 a thread, 3 x 168 = 216 + 248 + 40.
+template <int NT>
 struct BackCfg {
-    static constexpr int kWarps = 4;
-    static constexpr int kCols = 8 * NT * kWarps;
-    static constexpr int kThreads = 32 * (kWarps + 1);
+    static constexpr int ST = 2;
+    static constexpr int kCols = 32 * NT;
     static constexpr uint32_t kVRow = 2 * kCols;  // bytes of a dO row
     static constexpr uint32_t K = 0, Q = 16384, IMG = 32768, V = IMG + 27648;
     static constexpr uint32_t STAGE = V + C * kVRow;
-    static constexpr uint32_t BARS = ST * STAGE;  // full[ST], empty[ST]
-    static constexpr uint32_t ABORT = BARS + 16 * ST;
+    static_assert(STAGE % 1024 == 0 && kImgStrideBwd <= 27648, "stages");
+};
+template <int NT>
+struct WalksCfg {
+    using F = ForwardCfg<NT, 4, 2, true>;
+    using B = BackCfg<NT>;
+    static constexpr int kThreads = 384;
+    static constexpr uint32_t BACK = F::ST * F::STAGE;
+    static constexpr uint32_t BARS = BACK + B::ST * B::STAGE;  // full, empty of each
+    static constexpr uint32_t ABORT = BARS + 16 * (F::ST + B::ST);
     static constexpr uint32_t ALLOC = ABORT + 16 + 1024;
-    static_assert(kVRow == 64 || kVRow == 128, "swizzled rows");
-    static_assert(STAGE % 1024 == 0 && ALLOC <= 232448 && kImgStrideBwd <= 27648, "stages");
+    static_assert(ALLOC <= 232448, "shared memory");
 };
 
-template <int NT, int ST>
-__global__ void __launch_bounds__(BackCfg<NT, ST>::kThreads, 1)
-    kda_gdn_walk_back_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                             const __grid_constant__ CUtensorMap tm_do, const GdnArgs p, const GdnBackwardArgs gr,
-                             const int32_t* __restrict__ co, const int32_t* __restrict__ order,
-                             const uint8_t* __restrict__ images, int64_t chunk_slots, uint8_t* records) {
-    using L = BackCfg<NT, ST>;
-    constexpr int NW = L::kWarps;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int N = p.num_seqs, Hv = p.Hv;
-    constexpr int NSL = D / L::kCols;
-    const int slice = blockIdx.x % NSL;
-    const int h = (blockIdx.x / NSL) % Hv;
-    const int pos = blockIdx.x / (NSL * Hv);
-    if (co[N + 1] == 0) return;
-    const int seq = order ? order[pos] : pos;
-    const int nch = co[seq + 1] - co[seq], jb = co[seq];
-    const int64_t t_begin = p.cu_seqlens[seq], t_end = p.cu_seqlens[seq + 1];
-    if (!KDA_BOUNDS(seq >= 0 && seq < N && h < Hv && t_begin >= 0 && t_end <= p.total_tokens && jb >= 0 &&
-                        static_cast<int64_t>(jb) + nch <= chunk_slots &&
-                        static_cast<int64_t>(nch) * C >= t_end - t_begin,
-                    p.device_status))
-        return;
-    uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::BARS);
-    uint64_t* empty = full + ST;
-    volatile int* abort_s = reinterpret_cast<volatile int*>(sm + L::ABORT);
-    if (tid == 0) {
-        *abort_s = 0;
-        for (int i = 0; i < ST; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], NW);
-        }
-        fence_mbar_init();
-    }
-    __syncthreads();
+template <typename L>
+__device__ __forceinline__ void back_copies(const WalkUnit& u, const WalkPipe& pipe, const GdnArgs& p,
+                                            const CUtensorMap* tm_q, const CUtensorMap* tm_k, const CUtensorMap* tm_do,
+                                            const uint8_t* images) {
+    pipe_copies<L::ST>(pipe, u.nch, [&](int i, int s) {  // step i takes chunk nch - 1 - i
+        const int c = u.nch - 1 - i;
+        uint8_t* st = pipe.sm + s * L::STAGE;
+        uint64_t* bar = &pipe.full[s];
+        const int32_t tok = static_cast<int32_t>(u.t_begin + static_cast<int64_t>(c) * C);
+        mbar_arrive_expect_tx(bar, 32768 + static_cast<uint32_t>(kImgStrideBwd) + C * L::kVRow);
+#pragma unroll
+        for (int kh = 0; kh < 2; ++kh) tma_load_3d(st + L::K + kh * 8192, tm_k, bar, 64 * kh, u.hk, tok);
+        tma_load_3d(st + L::V, tm_do, bar, u.col0, u.h, tok);
+        bulk_g2s(st + L::IMG, images + (static_cast<size_t>(u.jb + c) * p.Hv + u.h) * kImgStrideBwd,
+                 static_cast<uint32_t>(kImgStrideBwd), bar);
+#pragma unroll
+        for (int kh = 0; kh < 2; ++kh) tma_load_3d(st + L::Q + kh * 8192, tm_q, bar, 64 * kh, u.hk, tok);
+    });
+}
 
-    if (warp == NW) {  // the copies: step i takes chunk nch - 1 - i, into stage i mod ST
-        if (lane == 0) {
-            const int hk = h / (Hv / p.Hk);
-            int i = 0;
-            for (; i < nch && !*abort_s; ++i) {
-                const int s = i % ST, c = nch - 1 - i;
-                if (i >= ST && !mbar_wait_pipe(&empty[s], ((i / ST) - 1) & 1)) {
-                    *abort_s = 1;
-                    break;
-                }
-                uint8_t* st = sm + s * L::STAGE;
-                const int32_t tok = static_cast<int32_t>(t_begin + static_cast<int64_t>(c) * C);
-                mbar_arrive_expect_tx(&full[s], 32768 + static_cast<uint32_t>(kImgStrideBwd) + C * L::kVRow);
+template <typename L, int NT>
+__device__ __forceinline__ void walk_back(const WalkUnit& wu, const WalkPipe& pipe, const GdnArgs& p,
+                                          const GdnBackwardArgs& gr, uint8_t* records, int warp, int lane) {
+    constexpr int ST = L::ST;
+    const int Hv = p.Hv;
+    const int g = lane >> 2, t = lane & 3;
+    const int wc = 8 * NT * warp;               // the warp's first column in the CTA's
+    const int col = wu.col0 + wc + 2 * t;  // this thread's first column
+    const size_t sbase = (static_cast<size_t>(wu.seq) * Hv + wu.h) * D * D;
+    float X[8][NT][4];  // rows 16 m + g (+ 8), columns col + 8 n (+ 1)
 #pragma unroll
-                for (int kh = 0; kh < 2; ++kh) tma_load_3d(st + L::K + kh * 8192, &tm_k, &full[s], 64 * kh, hk, tok);
-                tma_load_3d(st + L::V, &tm_do, &full[s], slice * L::kCols, h, tok);
-                bulk_g2s(st + L::IMG, images + (static_cast<size_t>(jb + c) * Hv + h) * kImgStrideBwd,
-                         static_cast<uint32_t>(kImgStrideBwd), &full[s]);
+    for (int m = 0; m < 8; ++m)
 #pragma unroll
-                for (int kh = 0; kh < 2; ++kh) tma_load_3d(st + L::Q + kh * 8192, &tm_q, &full[s], 64 * kh, hk, tok);
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const size_t off = sbase + static_cast<size_t>(16 * m + g + 8 * e) * D + col + 8 * n;
+                const float2 x =
+                    gr.grad_S_final ? *reinterpret_cast<const float2*>(gr.grad_S_final + off) : make_float2(0.f, 0.f);
+                X[m][n][2 * e] = x.x;
+                X[m][n][2 * e + 1] = x.y;
             }
-            for (int d = max(0, i - ST); d < i; ++d)  // no copy is left in flight
-                (void)mbar_wait(&full[d % ST], (d / ST) & 1, kDrainLimit);
+    // ldmatrix addresses: rows of tokens, and transposed [channels or columns][tokens] blocks
+    const int lr = lane & 15, lc = lane >> 4;
+    const int tr = (lane & 7) + ((lane >> 4) << 3), tc = (lane >> 3) & 1;
+    const int lt = (lane & 7) | ((lane & 8) << 1) | ((lane & 16) >> 1);  // an image block's, transposed
+    for (int i = 0; i < wu.nch; ++i) {
+        const int s = i % ST, c = wu.nch - 1 - i;
+        uint8_t* st = pipe.sm + s * L::STAGE;
+        const bool landed = !*pipe.abort_s && mbar_wait_pipe(&pipe.full[s], (i / ST) & 1);
+        if (!__all_sync(0xffffffffu, landed)) {  // a bounded wait expired, here or elsewhere
+            *pipe.abort_s = 1;
+            break;
         }
-    } else {
-        const int g = lane >> 2, t = lane & 3;
-        const int wc = 8 * NT * warp;               // the warp's first column in the CTA's
-        const int col = slice * L::kCols + wc + 2 * t;  // this thread's first column
-        const size_t sbase = (static_cast<size_t>(seq) * Hv + h) * D * D;
-        float X[8][NT][4];  // rows 16 m + g (+ 8), columns col + 8 n (+ 1)
+        const int64_t t0 = wu.t_begin + static_cast<int64_t>(c) * C;
+        const int Lc = static_cast<int>(wu.t_end - t0 < C ? wu.t_end - t0 : C);
+        if (Lc < C) {  // rows behind the sequence's end: no tokens (every warp clears all it reads)
+            const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+            for (int e = lane; e < (C - Lc) * 16; e += 32) {
+                const uint32_t off = (e & 1) * 8192 + sw128_chunk(Lc + (e >> 4), (e >> 1) & 7);
+                *reinterpret_cast<uint4*>(st + L::K + off) = z;
+                *reinterpret_cast<uint4*>(st + L::Q + off) = z;
+            }
+            for (uint32_t e = Lc * L::kVRow + 16 * lane; e < C * L::kVRow; e += 512)
+                *reinterpret_cast<uint4*>(st + L::V + e) = z;
+            __syncwarp();
+        }
+        const uint32_t kb = smem_u32(st + L::K), qb = smem_u32(st + L::Q), ib = smem_u32(st + L::IMG) + 16 * lt;
+        const float* gs = reinterpret_cast<const float*>(st + L::IMG + kImgG);
+        uint8_t* const rec = records + (static_cast<size_t>(wu.jb + c) * Hv + wu.h) * kRecStride;
+        // K X
+        float u[4][NT][4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) u[m][n][e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            BTerms b[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                put_record(X[k][n], rec + kRecX, 16384, 32768, 16 * k + g, col + 8 * n);
+                b[n] = b_terms(X[k][n]);
+            }
+            uint32_t a[4][4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) ldsm4(a[m], kb + (k >> 2) * 8192 + sw128_chunk(16 * m + lr, 2 * (k & 3) + lc));
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16(u[m][n], a[m], b[n].h0, b[n].h1);
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16(u[m][n], a[m], b[n].l0, b[n].l1);
+        }
+        // dO as B operand: [k][n] registers of tokens 16 k + 2 t (+ 1) and 16 k + 8 + 2 t (+ 1)
+        uint32_t dob[4][NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int row = 32 * hf + lane, piece = (wc >> 3) + n;
+                uint32_t off;
+                if constexpr (L::kVRow == 128) off = sw128_chunk(row, piece);
+                else off = row * 64 + (((piece ^ (row >> 1)) & 3) << 4);  // 64-byte rows
+                uint32_t f[4];
+                ldsm4t(f, smem_u32(st + L::V) + off);
+                dob[2 * hf][n][0] = f[0];
+                dob[2 * hf][n][1] = f[1];
+                dob[2 * hf + 1][n][0] = f[2];
+                dob[2 * hf + 1][n][1] = f[3];
+            }
+        // dU = e K X + P^T dO, P in three terms: an entry's error is that of a whole row of W, and of b's
+        // gradient with it
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const float e0 = gs[kVecEo + 16 * m + g], e1 = gs[kVecEo + 16 * m + g + 8];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                u[m][n][0] *= e0;
+                u[m][n][1] *= e0;
+                u[m][n][2] *= e1;
+                u[m][n][3] *= e1;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint32_t ah[4][4], al[4][4], am[4][4];
+#pragma unroll
+            for (int m = 0; m <= k; ++m) {
+                ldsm4t(ah[m], ib + kImgP + tri_blk(k, m));
+                ldsm4t(al[m], ib + kImgPl + tri_blk(k, m));
+                ldsm4t(am[m], ib + kImgPl2 + tri_blk(k, m));
+            }
+#pragma unroll
+            for (int m = 0; m <= k; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16(u[m][n], ah[m], dob[k][n][0], dob[k][n][1]);
+#pragma unroll
+            for (int m = 0; m <= k; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16(u[m][n], al[m], dob[k][n][0], dob[k][n][1]);
+#pragma unroll
+            for (int m = 0; m <= k; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16(u[m][n], am[m], dob[k][n][0], dob[k][n][1]);
+        }
+        // W = T^T dU, T in two terms, dU in three
+        float w[4][NT][4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[m][n][e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            BTerms3 b3[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) b3[n] = b_terms3(u[k][n]);
+            uint32_t ah[4][4], al[4][4];
+#pragma unroll
+            for (int m = 0; m <= k; ++m) {
+                ldsm4t(ah[m], ib + kImgTh + tri_blk(k, m));
+                ldsm4t(al[m], ib + kImgTl + tri_blk(k, m));
+            }
+#pragma unroll
+            for (int m = 0; m <= k; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16(w[m][n], ah[m], b3[n].b.h0, b3[n].b.h1);
+#pragma unroll
+            for (int m = 0; m <= k; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16(w[m][n], ah[m], b3[n].b.l0, b3[n].b.l1);
+#pragma unroll
+            for (int m = 0; m <= k; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16(w[m][n], ah[m], b3[n].m0, b3[n].m1);
+#pragma unroll
+            for (int m = 0; m <= k; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16(w[m][n], al[m], b3[n].b.h0, b3[n].b.h1);
+        }
+        // X <- e^gC X + K^T (-e^g b W) + Q^T (e^g dO)
+        const float gc = gs[kVecEc];
 #pragma unroll
         for (int m = 0; m < 8; ++m)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const size_t off = sbase + static_cast<size_t>(16 * m + g + 8 * e) * D + col + 8 * n;
-                    const float2 x =
-                        gr.grad_S_final ? *reinterpret_cast<const float2*>(gr.grad_S_final + off) : make_float2(0.f, 0.f);
-                    X[m][n][2 * e] = x.x;
-                    X[m][n][2 * e + 1] = x.y;
-                }
-        // ldmatrix addresses: rows of tokens, and transposed [channels or columns][tokens] blocks
-        const int lr = lane & 15, lc = lane >> 4;
-        const int tr = (lane & 7) + ((lane >> 4) << 3), tc = (lane >> 3) & 1;
-        const int lt = (lane & 7) | ((lane & 8) << 1) | ((lane & 16) >> 1);  // an image block's, transposed
-        for (int i = 0; i < nch; ++i) {
-            const int s = i % ST, c = nch - 1 - i;
-            uint8_t* st = sm + s * L::STAGE;
-            const bool landed = !*abort_s && mbar_wait_pipe(&full[s], (i / ST) & 1);
-            if (!__all_sync(0xffffffffu, landed)) {  // a bounded wait expired, here or elsewhere
-                *abort_s = 1;
-                break;
+                for (int e = 0; e < 4; ++e) X[m][n][e] *= gc;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int r0 = 16 * k + g;
+            const float z0 = -gs[kVecEg + r0] * gs[kVecB + r0], z1 = -gs[kVecEg + r0 + 8] * gs[kVecB + r0 + 8];
+            const float2 ga = *reinterpret_cast<const float2*>(gs + kVecEg + 16 * k + 2 * t);
+            const float2 gb = *reinterpret_cast<const float2*>(gs + kVecEg + 16 * k + 8 + 2 * t);
+            BTerms b[NT], d[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float x[4] = {w[k][n][0] * z0, w[k][n][1] * z0, w[k][n][2] * z1, w[k][n][3] * z1};
+                b[n] = b_terms(x);
+                const float2 y0 = unpack_bf16(dob[k][n][0]), y1 = unpack_bf16(dob[k][n][1]);
+                split2(y0.x * ga.x, y0.y * ga.y, d[n].h0, d[n].l0);
+                split2(y1.x * gb.x, y1.y * gb.y, d[n].h1, d[n].l1);
             }
-            const int64_t t0 = t_begin + static_cast<int64_t>(c) * C;
-            const int Lc = static_cast<int>(t_end - t0 < C ? t_end - t0 : C);
-            if (Lc < C) {  // rows behind the sequence's end: no tokens (every warp clears all it reads)
-                const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-                for (int e = lane; e < (C - Lc) * 16; e += 32) {
-                    const uint32_t off = (e & 1) * 8192 + sw128_chunk(Lc + (e >> 4), (e >> 1) & 7);
-                    *reinterpret_cast<uint4*>(st + L::K + off) = z;
-                    *reinterpret_cast<uint4*>(st + L::Q + off) = z;
-                }
-                for (uint32_t e = Lc * L::kVRow + 16 * lane; e < C * L::kVRow; e += 512)
-                    *reinterpret_cast<uint4*>(st + L::V + e) = z;
-                __syncwarp();
-            }
-            const uint32_t kb = smem_u32(st + L::K), qb = smem_u32(st + L::Q), ib = smem_u32(st + L::IMG) + 16 * lt;
-            const float* gs = reinterpret_cast<const float*>(st + L::IMG + kImgG);
-            uint8_t* const rec = records + (static_cast<size_t>(jb + c) * Hv + h) * kRecStride;
-            // K X
-            float u[4][NT][4];
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) u[m][n][e] = 0.f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                BTerms b[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    put_record(X[k][n], rec + kRecX, 16384, 32768, 16 * k + g, col + 8 * n);
-                    b[n] = b_terms(X[k][n]);
-                }
+            for (int mh = 0; mh < 2; ++mh) {
                 uint32_t a[4][4];
 #pragma unroll
-                for (int m = 0; m < 4; ++m) ldsm4(a[m], kb + (k >> 2) * 8192 + sw128_chunk(16 * m + lr, 2 * (k & 3) + lc));
+                for (int m = 0; m < 4; ++m) ldsm4t(a[m], kb + mh * 8192 + sw128_chunk(16 * k + tr, 2 * m + tc));
 #pragma unroll
                 for (int m = 0; m < 4; ++m)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) mma16(u[m][n], a[m], b[n].h0, b[n].h1);
+                    for (int n = 0; n < NT; ++n) mma16(X[4 * mh + m][n], a[m], b[n].h0, b[n].h1);
 #pragma unroll
                 for (int m = 0; m < 4; ++m)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) mma16(u[m][n], a[m], b[n].l0, b[n].l1);
+                    for (int n = 0; n < NT; ++n) mma16(X[4 * mh + m][n], a[m], b[n].l0, b[n].l1);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) ldsm4t(a[m], qb + mh * 8192 + sw128_chunk(16 * k + tr, 2 * m + tc));
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma16(X[4 * mh + m][n], a[m], d[n].h0, d[n].h1);
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma16(X[4 * mh + m][n], a[m], d[n].l0, d[n].l1);
             }
-            // dO as B operand: [k][n] registers of tokens 16 k + 2 t (+ 1) and 16 k + 8 + 2 t (+ 1)
-            uint32_t dob[4][NT][2];
+        }
+        float bs[4][2];
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) bs[m][e] = gs[kVecB + 16 * m + g + 8 * e];
+        if (Lc < C) fence_async_smem();  // the cleared rows, before the stage's next copies
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pipe.empty[s]);  // the warp has read all it takes of this stage
+        __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(gr.grad_v) + (t0 * Hv + wu.h) * D + col;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) put_record(w[m][n], rec + kRecW, 8192, 16384, 16 * m + g, col + 8 * n);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = 16 * m + g + 8 * e;
+                if (row < Lc) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        *reinterpret_cast<uint32_t*>(dv + static_cast<int64_t>(row) * Hv * D + 8 * n) =
+                            pack_bf16(bs[m][e] * w[m][n][2 * e], bs[m][e] * w[m][n][2 * e + 1]);
+                }
+            }
+        }
+    }
+    if (gr.grad_S0 && !*pipe.abort_s) {
+#pragma unroll
+        for (int m = 0; m < 8; ++m)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const int row = 32 * hf + lane, piece = (wc >> 3) + n;
-                    uint32_t off;
-                    if constexpr (L::kVRow == 128) off = sw128_chunk(row, piece);
-                    else off = row * 64 + (((piece ^ (row >> 1)) & 3) << 4);  // 64-byte rows
-                    uint32_t f[4];
-                    ldsm4t(f, smem_u32(st + L::V) + off);
-                    dob[2 * hf][n][0] = f[0];
-                    dob[2 * hf][n][1] = f[1];
-                    dob[2 * hf + 1][n][0] = f[2];
-                    dob[2 * hf + 1][n][1] = f[3];
-                }
-            // dU = e K X + P^T dO, P in three terms: an entry's error is that of a whole row of W, and of b's
-            // gradient with it
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const float e0 = gs[kVecEo + 16 * m + g], e1 = gs[kVecEo + 16 * m + g + 8];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    u[m][n][0] *= e0;
-                    u[m][n][1] *= e0;
-                    u[m][n][2] *= e1;
-                    u[m][n][3] *= e1;
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint32_t ah[4][4], al[4][4], am[4][4];
-#pragma unroll
-                for (int m = 0; m <= k; ++m) {
-                    ldsm4t(ah[m], ib + kImgP + tri_blk(k, m));
-                    ldsm4t(al[m], ib + kImgPl + tri_blk(k, m));
-                    ldsm4t(am[m], ib + kImgPl2 + tri_blk(k, m));
-                }
-#pragma unroll
-                for (int m = 0; m <= k; ++m)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) mma16(u[m][n], ah[m], dob[k][n][0], dob[k][n][1]);
-#pragma unroll
-                for (int m = 0; m <= k; ++m)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) mma16(u[m][n], al[m], dob[k][n][0], dob[k][n][1]);
-#pragma unroll
-                for (int m = 0; m <= k; ++m)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) mma16(u[m][n], am[m], dob[k][n][0], dob[k][n][1]);
-            }
-            // W = T^T dU, T in two terms, dU in three
-            float w[4][NT][4];
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) w[m][n][e] = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                BTerms3 b3[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) b3[n] = b_terms3(u[k][n]);
-                uint32_t ah[4][4], al[4][4];
-#pragma unroll
-                for (int m = 0; m <= k; ++m) {
-                    ldsm4t(ah[m], ib + kImgTh + tri_blk(k, m));
-                    ldsm4t(al[m], ib + kImgTl + tri_blk(k, m));
-                }
-#pragma unroll
-                for (int m = 0; m <= k; ++m)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) mma16(w[m][n], ah[m], b3[n].b.h0, b3[n].b.h1);
-#pragma unroll
-                for (int m = 0; m <= k; ++m)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) mma16(w[m][n], ah[m], b3[n].b.l0, b3[n].b.l1);
-#pragma unroll
-                for (int m = 0; m <= k; ++m)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) mma16(w[m][n], ah[m], b3[n].m0, b3[n].m1);
-#pragma unroll
-                for (int m = 0; m <= k; ++m)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) mma16(w[m][n], al[m], b3[n].b.h0, b3[n].b.h1);
-            }
-            // X <- e^gC X + K^T (-e^g b W) + Q^T (e^g dO)
-            const float gc = gs[kVecEc];
-#pragma unroll
-            for (int m = 0; m < 8; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) X[m][n][e] *= gc;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int r0 = 16 * k + g;
-                const float z0 = -gs[kVecEg + r0] * gs[kVecB + r0], z1 = -gs[kVecEg + r0 + 8] * gs[kVecB + r0 + 8];
-                const float2 ga = *reinterpret_cast<const float2*>(gs + kVecEg + 16 * k + 2 * t);
-                const float2 gb = *reinterpret_cast<const float2*>(gs + kVecEg + 16 * k + 8 + 2 * t);
-                BTerms b[NT], d[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const float x[4] = {w[k][n][0] * z0, w[k][n][1] * z0, w[k][n][2] * z1, w[k][n][3] * z1};
-                    b[n] = b_terms(x);
-                    const float2 y0 = unpack_bf16(dob[k][n][0]), y1 = unpack_bf16(dob[k][n][1]);
-                    split2(y0.x * ga.x, y0.y * ga.y, d[n].h0, d[n].l0);
-                    split2(y1.x * gb.x, y1.y * gb.y, d[n].h1, d[n].l1);
-                }
-#pragma unroll
-                for (int mh = 0; mh < 2; ++mh) {
-                    uint32_t a[4][4];
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) ldsm4t(a[m], kb + mh * 8192 + sw128_chunk(16 * k + tr, 2 * m + tc));
-#pragma unroll
-                    for (int m = 0; m < 4; ++m)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) mma16(X[4 * mh + m][n], a[m], b[n].h0, b[n].h1);
-#pragma unroll
-                    for (int m = 0; m < 4; ++m)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) mma16(X[4 * mh + m][n], a[m], b[n].l0, b[n].l1);
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) ldsm4t(a[m], qb + mh * 8192 + sw128_chunk(16 * k + tr, 2 * m + tc));
-#pragma unroll
-                    for (int m = 0; m < 4; ++m)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) mma16(X[4 * mh + m][n], a[m], d[n].h0, d[n].h1);
-#pragma unroll
-                    for (int m = 0; m < 4; ++m)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) mma16(X[4 * mh + m][n], a[m], d[n].l0, d[n].l1);
-                }
-            }
-            float bs[4][2];
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) bs[m][e] = gs[kVecB + 16 * m + g + 8 * e];
-            if (Lc < C) fence_async_smem();  // the cleared rows, before the stage's next copies
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[s]);  // the warp has read all it takes of this stage
-            __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(gr.grad_v) + (t0 * Hv + h) * D + col;
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n) put_record(w[m][n], rec + kRecW, 8192, 16384, 16 * m + g, col + 8 * n);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int row = 16 * m + g + 8 * e;
-                    if (row < Lc) {
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            *reinterpret_cast<uint32_t*>(dv + static_cast<int64_t>(row) * Hv * D + 8 * n) =
-                                pack_bf16(bs[m][e] * w[m][n][2 * e], bs[m][e] * w[m][n][2 * e + 1]);
-                    }
-                }
-            }
-        }
-        if (gr.grad_S0 && !*abort_s) {
-#pragma unroll
-            for (int m = 0; m < 8; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        *reinterpret_cast<float2*>(gr.grad_S0 + sbase + static_cast<size_t>(16 * m + g + 8 * e) * D + col +
-                                                   8 * n) = make_float2(X[m][n][2 * e], X[m][n][2 * e + 1]);
-        }
+                for (int e = 0; e < 2; ++e)
+                    *reinterpret_cast<float2*>(gr.grad_S0 + sbase + static_cast<size_t>(16 * m + g + 8 * e) * D + col +
+                                               8 * n) = make_float2(X[m][n][2 * e], X[m][n][2 * e + 1]);
+    }
+}
+
+template <int NT>
+__global__ void __launch_bounds__(WalksCfg<NT>::kThreads, 1)
+    kda_gdn_walks_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do, const GdnArgs p,
+                         const GdnBackwardArgs gr, const int32_t* __restrict__ co, const int32_t* __restrict__ order,
+                         const uint8_t* __restrict__ images, int64_t chunk_slots, uint8_t* records) {
+    using L = WalksCfg<NT>;
+    using F = typename L::F;
+    using B = typename L::B;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint64_t* const bars = reinterpret_cast<uint64_t*>(sm + L::BARS);
+    volatile int* const abort_s = reinterpret_cast<volatile int*>(sm + L::ABORT);
+    const WalkPipe fwd{sm, bars, bars + F::ST, abort_s};
+    const WalkPipe back{sm + L::BACK, bars + 2 * F::ST, bars + 2 * F::ST + B::ST, abort_s};
+    if (tid == 0) {
+        *abort_s = 0;
+        pipe_init(fwd, F::ST, 4);
+        pipe_init(back, B::ST, 4);
+        fence_mbar_init();
+    }
+    grid_dependents();
+    grid_wait();  // the images, and the table and order, of the launches before
+    WalkUnit u;
+    if (!walk_unit<F::kCols>(p, co, order, chunk_slots, u)) return;
+    __syncthreads();
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (lane == 0 && warp == 8) forward_copies<F>(u, fwd, p, &tm_q, &tm_k, &tm_v, images);
+        if (lane == 0 && warp == 9) back_copies<B>(u, back, p, &tm_q, &tm_k, &tm_do, images);
+    } else if (warp >= 4) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 248;");
+        walk_back<B, NT>(u, back, p, gr, records, warp - 4, lane);
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        walk_forward<F, NT>(u, fwd, p, records, warp, lane);
     }
     __syncthreads();
     if (tid == 0 && *abort_s && p.device_status) atomicOr(p.device_status, KDA_DEV_TIMEOUT);
@@ -386,9 +396,10 @@ __global__ void __launch_bounds__(kRestThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int N = p.num_seqs, Hv = p.Hv, group = Hv / p.Hk;
     const int j = blockIdx.x / p.Hk, hk = blockIdx.x - j * p.Hk;
-    if (co[N + 1] == 0 || j >= co[N]) return;
-    int seq;
-    {  // the largest n with co[n] <= j
+    grid_wait();  // the walks' records
+    if (!table_ok(p, co) || j >= table_at(p, co, N)) return;
+    int seq = 0;
+    if (co) {  // the largest n with co[n] <= j
         int lo = 0, hi = N - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -397,7 +408,7 @@ __global__ void __launch_bounds__(kRestThreads, 1)
         }
         seq = lo;
     }
-    const int64_t t0 = static_cast<int64_t>(p.cu_seqlens[seq]) + static_cast<int64_t>(j - co[seq]) * C;
+    const int64_t t0 = static_cast<int64_t>(p.cu_seqlens[seq]) + static_cast<int64_t>(j - table_at(p, co, seq)) * C;
     const int64_t rem = p.cu_seqlens[seq + 1] - t0;
     const int Lc = static_cast<int>(rem < C ? rem : C);
     if (!KDA_BOUNDS(seq >= 0 && seq < N && j < chunk_slots && t0 >= 0 && Lc >= 1 && t0 + Lc <= p.total_tokens,
@@ -796,40 +807,36 @@ __global__ void __launch_bounds__(kRestThreads, 1)
     }
 }
 
-template <int NT, int ST>
-cudaError_t launch_walk_back(const GdnArgs& a, const GdnBackwardArgs& b, const GdnWorkspace& w, const CUtensorMap& tm_q,
-                             const CUtensorMap& tm_k, cudaStream_t stream) {
-    using L = BackCfg<NT, ST>;
+template <int NT>
+cudaError_t launch_walks(const GdnArgs& a, const GdnBackwardArgs& b, const GdnWorkspace& w, const CUtensorMap& tm_q,
+                         const CUtensorMap& tm_k, cudaStream_t stream) {
+    using L = WalksCfg<NT>;
+    using F = typename L::F;
     static int configured[64];
-    const cudaError_t err = set_smem(kda_gdn_walk_back_kernel<NT, ST>, L::ALLOC, configured);
+    const cudaError_t err = set_smem(kda_gdn_walks_kernel<NT>, L::ALLOC, configured);
     if (err != cudaSuccess) return err;
-    CUtensorMap tm_do;
-    if (!make_tensor_map(&tm_do, b.grad_o, a.Hv, a.total_tokens, L::kCols, C,
-                         L::kVRow == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+    CUtensorMap tm_v, tm_do;
+    const CUtensorMapSwizzle sw = F::kVRow == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    if (!make_tensor_map(&tm_v, a.v, a.Hv, a.total_tokens, F::kCols, C, sw) ||
+        !make_tensor_map(&tm_do, b.grad_o, a.Hv, a.total_tokens, F::kCols, C, sw))
         return cudaErrorInvalidValue;
-    const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(a.num_seqs) * a.Hv * (D / L::kCols));
-    kda_gdn_walk_back_kernel<NT, ST><<<blocks, L::kThreads, L::ALLOC, stream>>>(tm_q, tm_k, tm_do, a, b, w.table, w.order,
-                                                                                w.images, w.chunks, w.records);
-    return cudaGetLastError();
+    const int64_t blocks = static_cast<int64_t>(a.num_seqs) * a.Hv * (D / F::kCols);
+    return launch_dependent(kda_gdn_walks_kernel<NT>, blocks, L::kThreads, L::ALLOC, stream, tm_q, tm_k, tm_v, tm_do, a, b,
+                            w.table, w.order, w.images, w.chunks, w.records);
 }
 
 }  // namespace
 
-cudaError_t launch_gdn_backward(const GdnArgs& a, const GdnBackwardArgs& b, const GdnWorkspace& w, cudaStream_t stream) {
-    CUtensorMap tm_q, tm_k;
-    if (!make_tensor_map(&tm_q, a.q, a.Hk, a.total_tokens, 64, C, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_tensor_map(&tm_k, a.k, a.Hk, a.total_tokens, 64, C, CU_TENSOR_MAP_SWIZZLE_128B))
-        return cudaErrorInvalidValue;
-    // columns a CTA as in the walk forward
-    cudaError_t err = static_cast<int64_t>(a.num_seqs) * a.Hv * 4 <= device_sm_count()
-                          ? launch_walk_back<1, 3>(a, b, w, tm_q, tm_k, stream)
-                          : launch_walk_back<2, 3>(a, b, w, tm_q, tm_k, stream);
+cudaError_t launch_gdn_backward(const GdnArgs& a, const GdnBackwardArgs& b, const GdnWorkspace& w, const CUtensorMap& tm_q,
+                                const CUtensorMap& tm_k, cudaStream_t stream) {
+    // columns a CTA as in the prefill's scan
+    cudaError_t err = gdn_narrow(a.num_seqs, a.Hv) ? launch_walks<1>(a, b, w, tm_q, tm_k, stream)
+                                                   : launch_walks<2>(a, b, w, tm_q, tm_k, stream);
     static int configured[64];
     if (err == cudaSuccess) err = set_smem(kda_gdn_grad_kernel, RestSmem::ALLOC, configured);
     if (err != cudaSuccess) return err;
-    kda_gdn_grad_kernel<<<static_cast<unsigned>(w.chunks * a.Hk), kRestThreads, RestSmem::ALLOC, stream>>>(
-        tm_q, tm_k, a, b, w.table, w.images, w.chunks, w.records);
-    return cudaGetLastError();
+    return launch_dependent(kda_gdn_grad_kernel, w.chunks * a.Hk, kRestThreads, RestSmem::ALLOC, stream, tm_q, tm_k, a, b,
+                            w.table, w.images, w.chunks, w.records);
 }
 
 }  // namespace kda

@@ -200,8 +200,8 @@ struct GdnArgs {
 cudaError_t launch_gdn_recurrent(bool f32_io, const GdnArgs& a, cudaStream_t stream);
 // Chunkwise, bf16 (kda_gdn_prefill.cu, kda_gdn_backward.cu).
 struct GdnWorkspace {
-    int32_t* order = nullptr;    // sequences, longest first (NULL: one sequence)
-    int32_t* table = nullptr;    // chunk table
+    int32_t* order = nullptr;    // sequences, longest first (NULL: in index order)
+    int32_t* table = nullptr;    // chunk table (NULL: one sequence)
     uint8_t* images = nullptr;   // per (chunk, value head): the scans' operands
     uint8_t* records = nullptr;  // per (chunk, value head): states, adjoints, U and W (NULL: the prefill)
     int64_t chunks = 0;          // chunk entries: ceil(T / 64) + num_seqs
@@ -209,8 +209,13 @@ struct GdnWorkspace {
 // Bytes of the workspace, and (w not NULL) its regions from `base`; bwd: the gradient's.
 size_t gdn_workspace(int32_t num_seqs, int64_t total_tokens, int32_t Hv, bool bwd, uint8_t* base, GdnWorkspace* w);
 cudaError_t launch_gdn_tables(const GdnArgs& a, const GdnWorkspace& w, cudaStream_t stream);
-cudaError_t launch_gdn_prep(const GdnArgs& a, const GdnWorkspace& w, cudaStream_t stream);
-cudaError_t launch_gdn_scan(const GdnArgs& a, const GdnWorkspace& w, cudaStream_t stream);
+// Whether the walks take 32 columns a CTA (else 64).
+bool gdn_narrow(int32_t num_seqs, int32_t Hv);
+// tm_q, tm_k: maps of q and k with boxes of 64 tokens x 64 channels, 128B-swizzled.
+cudaError_t launch_gdn_prep(const GdnArgs& a, const GdnWorkspace& w, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                            cudaStream_t stream);
+cudaError_t launch_gdn_scan(const GdnArgs& a, const GdnWorkspace& w, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                            cudaStream_t stream);
 struct GdnBackwardArgs {
     const void* grad_o = nullptr;          // [T, Hv, 128]
     const float* grad_S_final = nullptr;   // NULL: zeros
@@ -221,7 +226,8 @@ struct GdnBackwardArgs {
     float* grad_beta = nullptr;
     float* grad_S0 = nullptr;              // NULL: not stored
 };
-cudaError_t launch_gdn_backward(const GdnArgs& a, const GdnBackwardArgs& b, const GdnWorkspace& w, cudaStream_t stream);
+cudaError_t launch_gdn_backward(const GdnArgs& a, const GdnBackwardArgs& b, const GdnWorkspace& w, const CUtensorMap& tm_q,
+                                const CUtensorMap& tm_k, cudaStream_t stream);
 cudaError_t launch_gdn_decode(bool f32_io, const void* q, const void* k, const void* v, const float* log_decay,
                               const float* beta, float* S, int32_t num_slots, const int32_t* state_indices, int32_t N,
                               int32_t Hk, int32_t Hv, void* o, int32_t* device_status, cudaStream_t stream);
