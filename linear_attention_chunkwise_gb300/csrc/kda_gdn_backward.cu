@@ -122,6 +122,7 @@ __device__ __forceinline__ void walk_back(const WalkUnit& wu, const WalkPipe& pi
         const uint32_t kb = smem_u32(st + L::K), qb = smem_u32(st + L::Q), ib = smem_u32(st + L::IMG) + 16 * lt;
         const float* gs = reinterpret_cast<const float*>(st + L::IMG + kImgG);
         uint8_t* const rec = records + (static_cast<size_t>(wu.jb + c) * Hv + wu.h) * kRecStride;
+        const int rcol = (wu.col0 + wc) >> 3;  // matrices of 8 columns
         // K X
         float u[4][NT][4];
 #pragma unroll
@@ -135,7 +136,7 @@ __device__ __forceinline__ void walk_back(const WalkUnit& wu, const WalkPipe& pi
             BTerms b[NT];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                put_record(X[k][n], rec + kRecX, 16384, 32768, 16 * k + g, col + 8 * n);
+                put_record(X[k][n], rec + kRecX, 32768, 2 * k, rcol + n, lane);
                 b[n] = b_terms(X[k][n]);
             }
             uint32_t a[4][4];
@@ -298,7 +299,7 @@ __device__ __forceinline__ void walk_back(const WalkUnit& wu, const WalkPipe& pi
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) put_record(w[m][n], rec + kRecW, 8192, 16384, 16 * m + g, col + 8 * n);
+            for (int n = 0; n < NT; ++n) put_record(w[m][n], rec + kRecW, 16384, 2 * m, rcol + n, lane);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int row = 16 * m + g + 8 * e;
@@ -374,7 +375,7 @@ struct RestSmem {
     static constexpr uint32_t S = 0, X = 65536, U = 131072, W = 163840;  // as in the record
     static constexpr uint32_t K = 196608, Q = 212992;
     static constexpr uint32_t G = 229376;            // the image's vectors
-    static constexpr uint32_t BARS = G + 1328;       // u64: K and Q, S and W, X and U
+    static constexpr uint32_t BARS = G + 1328;       // u64: K and Q, S and W, X and U, dO
     static constexpr uint32_t TOTAL = BARS + 32;
     static constexpr uint32_t ALLOC = TOTAL + 1024;
     // over S once it and X have been read
@@ -387,8 +388,8 @@ static_assert(RestSmem::ALLOC <= 232448 && RestSmem::BARS % 8 == 0, "shared memo
 constexpr int kPtA = 0, kPtW = 128, kPtC = 256, kPtB = 768, kPtI = 832;
 
 __global__ void __launch_bounds__(kRestThreads, 1)
-    kda_gdn_grad_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const GdnArgs p,
-                        const GdnBackwardArgs gr, const int32_t* __restrict__ co, const uint8_t* __restrict__ images,
+    kda_gdn_grad_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_do, const GdnArgs p, const GdnBackwardArgs gr, const int32_t* __restrict__ co, const uint8_t* __restrict__ images,
                         int64_t chunk_slots, const uint8_t* __restrict__ records) {
     using L = RestSmem;
     extern __shared__ uint8_t smem_raw[];
@@ -423,12 +424,20 @@ __global__ void __launch_bounds__(kRestThreads, 1)
         mbar_arrive_expect_tx(&bars[1], 65536 + 32768);
         bulk_g2s(sm + L::S, rec + kRecS, 65536, &bars[1]);
         bulk_g2s(sm + L::W, rec + kRecW, 32768, &bars[1]);
+        // dO's tile through X's place: X and U follow once its fragments are in registers
+        mbar_arrive_expect_tx(&bars[3], 16384);
+#pragma unroll
+        for (int kh = 0; kh < 2; ++kh)
+            tma_load_3d(sm + L::X + kh * 8192, &tm_do, &bars[3], 64 * kh, hk * group + hh, static_cast<int32_t>(t0));
+    };
+    auto issue_x = [&](int hh) {
+        const uint8_t* rec = records + (unit0 + hh) * kRecStride;
         mbar_arrive_expect_tx(&bars[2], 65536 + 32768);
         bulk_g2s(sm + L::X, rec + kRecX, 65536, &bars[2]);
         bulk_g2s(sm + L::U, rec + kRecU, 32768, &bars[2]);
     };
     if (tid == 0) {
-        for (int i = 0; i < 3; ++i) mbar_init(&bars[i], 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&bars[i], 1);
         fence_mbar_init();
         mbar_arrive_expect_tx(&bars[0], 32768);
 #pragma unroll
@@ -451,6 +460,8 @@ __global__ void __launch_bounds__(kRestThreads, 1)
     const int g = lane >> 2, t = lane & 3;
     const int nh = warp >> 2, mr = nh ? 7 - warp : warp;
     const int lr = lane & 15, lc = lane >> 4;                                      // row-major A operand
+    const uint32_t la = ((lane >> 3) & 1) * 2048 + (lane >> 4) * 128 + (lane & 7) * 16;  // the same, of a record
+    const uint32_t lb = (lane >> 4) * 2048 + ((lane >> 3) & 1) * 128 + (lane & 7) * 16;  // B from its [n][k] rows
     const int br = (lane & 7) + ((lane >> 4) << 3), bc = (lane >> 3) & 1;          // B operand from [n][k] rows
     const int kr = (lane & 7) + (((lane >> 3) & 1) << 3), kc = lane >> 4;          // B operand from [k][n] rows
     const uint32_t base = smem_u32(sm);
@@ -466,20 +477,17 @@ __global__ void __launch_bounds__(kRestThreads, 1)
         const float* vec = reinterpret_cast<const float*>(images + (unit0 + hh) * kImgStrideBwd + kImgG);
         for (int e = tid; e < 5 * C + 4; e += kRestThreads) gs[e] = vec[e];
         uint32_t dof[8][4];  // dO rows 16 mr as A operand
-        {
-            const __nv_bfloat16* d0 = static_cast<const __nv_bfloat16*>(gr.grad_o) + ((t0 + 16 * mr + g) * Hv + h) * D + 2 * t;
-            const bool r0 = 16 * mr + g < Lc, r1 = 16 * mr + g + 8 < Lc;
-            const int64_t step = static_cast<int64_t>(8) * Hv * D;
+        ok = mbar_wait_pipe(&bars[3], par) && ok;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                dof[k][0] = r0 ? *reinterpret_cast<const uint32_t*>(d0 + 16 * k) : 0u;
-                dof[k][1] = r1 ? *reinterpret_cast<const uint32_t*>(d0 + step + 16 * k) : 0u;
-                dof[k][2] = r0 ? *reinterpret_cast<const uint32_t*>(d0 + 16 * k + 8) : 0u;
-                dof[k][3] = r1 ? *reinterpret_cast<const uint32_t*>(d0 + step + 16 * k + 8) : 0u;
-            }
+        for (int k = 0; k < 8; ++k) {
+            ldsm4(dof[k], base + L::X + (k >> 2) * 8192 + sw128_chunk(16 * mr + lr, 2 * (k & 3) + lc));
+            const bool r0 = 16 * mr + g < Lc, r1 = 16 * mr + g + 8 < Lc;
+            if (!r0) dof[k][0] = dof[k][2] = 0u;
+            if (!r1) dof[k][1] = dof[k][3] = 0u;
         }
         ok = mbar_wait_pipe(&bars[1], par) && ok;
-        __syncthreads();  // the vectors (and the cleared rows) are there
+        __syncthreads();  // the vectors (and the cleared rows) are there, dO's tile has been read
+        if (tid == 0) issue_x(hh);
         float eg[2], eo[2], be[2], gh[2], gl[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -516,13 +524,13 @@ __global__ void __launch_bounds__(kRestThreads, 1)
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 uint32_t wh[4], wl[4];
-                const uint32_t wa = base + L::W + (k >> 2) * 8192 + sw128_chunk(16 * mr + lr, 2 * (k & 3) + lc);
+                const uint32_t wa = base + L::W + la + mr * 4096 + k * 256;
                 ldsm4(wh, wa);
                 ldsm4(wl, wa + 16384);
 #pragma unroll
                 for (int np = 0; np < 4; ++np) {
                     uint32_t sh[4], sl[4];
-                    const uint32_t sa = base + L::S + (k >> 2) * 16384 + sw128_chunk(64 * nh + 16 * np + br, 2 * (k & 3) + bc);
+                    const uint32_t sa = base + L::S + lb + (4 * nh + np) * 4096 + k * 256;
                     ldsm4(sh, sa);
                     ldsm4(sl, sa + 32768);
 #pragma unroll
@@ -558,13 +566,13 @@ __global__ void __launch_bounds__(kRestThreads, 1)
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 uint32_t uh[4], ul[4];
-                const uint32_t ua = base + L::U + (k >> 2) * 8192 + sw128_chunk(16 * mr + lr, 2 * (k & 3) + lc);
+                const uint32_t ua = base + L::U + la + mr * 4096 + k * 256;
                 ldsm4(uh, ua);
                 ldsm4(ul, ua + 16384);
 #pragma unroll
                 for (int np = 0; np < 4; ++np) {
                     uint32_t xh[4], xl[4];
-                    const uint32_t xa = base + L::X + (k >> 2) * 16384 + sw128_chunk(64 * nh + 16 * np + br, 2 * (k & 3) + bc);
+                    const uint32_t xa = base + L::X + lb + (4 * nh + np) * 4096 + k * 256;
                     ldsm4(xh, xa);
                     ldsm4(xl, xa + 32768);
 #pragma unroll
@@ -631,15 +639,15 @@ __global__ void __launch_bounds__(kRestThreads, 1)
                 for (int k = 0; k < 8; ++k) {
                     uint32_t wh[4], wl[4], ga[4];
                     const uint32_t aoff = (k >> 2) * 8192 + sw128_chunk(16 * mr + lr, 2 * (k & 3) + lc);
-                    ldsm4(wh, base + L::W + aoff);
-                    ldsm4(wl, base + L::W + 16384 + aoff);
+                    ldsm4(wh, base + L::W + la + mr * 4096 + k * 256);
+                    ldsm4(wl, base + L::W + 16384 + la + mr * 4096 + k * 256);
                     ldsm4(ga, base + L::K + aoff);
 #pragma unroll
                     for (int np = 0; np < 2; ++np) {
                         uint32_t uh[4], ul[4], kf[4];
                         const uint32_t off = (k >> 2) * 8192 + sw128_chunk(32 * ph + 16 * np + br, 2 * (k & 3) + bc);
-                        ldsm4(uh, base + L::U + off);
-                        ldsm4(ul, base + L::U + 16384 + off);
+                        ldsm4(uh, base + L::U + lb + (2 * ph + np) * 4096 + k * 256);
+                        ldsm4(ul, base + L::U + 16384 + lb + (2 * ph + np) * 4096 + k * 256);
                         ldsm4(kf, base + L::K + off);
 #pragma unroll
                         for (int n = 0; n < 2; ++n) {
@@ -659,8 +667,8 @@ __global__ void __launch_bounds__(kRestThreads, 1)
                     for (int np = 0; np < 2; ++np) {
                         uint32_t uh[4], ul[4], kf[4];
                         const uint32_t off = (k >> 2) * 8192 + sw128_chunk(32 * ph + 16 * np + br, 2 * (k & 3) + bc);
-                        ldsm4(uh, base + L::U + off);
-                        ldsm4(ul, base + L::U + 16384 + off);
+                        ldsm4(uh, base + L::U + lb + (2 * ph + np) * 4096 + k * 256);
+                        ldsm4(ul, base + L::U + 16384 + lb + (2 * ph + np) * 4096 + k * 256);
                         ldsm4(kf, base + L::K + off);
 #pragma unroll
                         for (int n = 0; n < 2; ++n) {
@@ -832,11 +840,14 @@ cudaError_t launch_gdn_backward(const GdnArgs& a, const GdnBackwardArgs& b, cons
     // columns a CTA as in the prefill's scan
     cudaError_t err = gdn_narrow(a.num_seqs, a.Hv) ? launch_walks<1>(a, b, w, tm_q, tm_k, stream)
                                                    : launch_walks<2>(a, b, w, tm_q, tm_k, stream);
+    CUtensorMap tm_do;
+    if (!make_tensor_map(&tm_do, b.grad_o, a.Hv, a.total_tokens, 64, C, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
     static int configured[64];
     if (err == cudaSuccess) err = set_smem(kda_gdn_grad_kernel, RestSmem::ALLOC, configured);
     if (err != cudaSuccess) return err;
-    return launch_dependent(kda_gdn_grad_kernel, w.chunks * a.Hk, kRestThreads, RestSmem::ALLOC, stream, tm_q, tm_k, a, b,
-                            w.table, w.images, w.chunks, w.records);
+    return launch_dependent(kda_gdn_grad_kernel, w.chunks * a.Hk, kRestThreads, RestSmem::ALLOC, stream, tm_q, tm_k, tm_do, a,
+                            b, w.table, w.images, w.chunks, w.records);
 }
 
 }  // namespace kda

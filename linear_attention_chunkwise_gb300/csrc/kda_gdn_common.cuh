@@ -33,8 +33,10 @@ __device__ __forceinline__ constexpr uint32_t tri_blk(int i, int j) { return (i 
 __device__ __forceinline__ uint32_t blk_pair(int g, int e, int n, int t) { return (2 * n + e) * 128 + 16 * g + 4 * t; }
 
 // The gradient's record of a (chunk, value head): the state at the chunk's start, the adjoint of the state
-// at its end ([128 channels][128 columns]), U and W ([64 tokens][128 columns]), each as two bf16 terms in
-// 128B-swizzled tiles of 64 columns.
+// at its end ([128 channels][128 columns]), U and W ([64 tokens][128 columns]), each as two bf16 terms, in
+// 8 x 8 matrices of 128 bytes, 16 of them to a row of matrices: a warp stores an accumulator's half as one
+// line (as 128B-swizzled tiles, 16 bytes in each of 8 lines: the two walks 512 us for 8192 tokens x 32 heads),
+// and ldmatrix reads it without conflicts.
 constexpr uint32_t kRecS = 0, kRecX = 65536, kRecU = 131072, kRecW = 163840;
 constexpr size_t kRecStride = 196608;
 
@@ -101,14 +103,14 @@ __device__ __forceinline__ uint32_t third2(float x, float y, uint32_t hi, uint32
     return pack_bf16((x - __uint_as_float(hi << 16)) - __uint_as_float(lo << 16),
                      (y - __uint_as_float(hi & 0xffff0000u)) - __uint_as_float(lo & 0xffff0000u));
 }
-// An accumulator tile's two terms into a record: rows row and row + 8, columns col and col + 1 of tiles
-// `block` bytes apart, the second term `lo` bytes after the first.
-__device__ __forceinline__ void put_record(const float (&c)[4], uint8_t* rec, int block, uint32_t lo, int row, int col) {
+// An accumulator tile's two terms into a record: matrices (rm, cm) and (rm + 1, cm), the second term `lo`
+// bytes after the first.
+__device__ __forceinline__ void put_record(const float (&c)[4], uint8_t* rec, uint32_t lo, int rm, int cm, int lane) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         uint32_t h, l;
         split2(c[2 * e], c[2 * e + 1], h, l);
-        uint8_t* p = rec + sw128_off(row + 8 * e, col, block);
+        uint8_t* p = rec + ((rm + e) * 16 + cm) * 128 + 4 * lane;
         *reinterpret_cast<uint32_t*>(p) = h;
         *reinterpret_cast<uint32_t*>(p + lo) = l;
     }

@@ -158,7 +158,7 @@ __device__ __forceinline__ void walk_forward(const WalkUnit& wu, const WalkPipe&
         const uint32_t kb = smem_u32(st + L::K), qb = smem_u32(st + L::Q), ib = smem_u32(st + L::IMG) + 16 * lane;
         const float* gs = reinterpret_cast<const float*>(st + L::IMG + kImgG);
         uint8_t* const rec = REC ? records + (static_cast<size_t>(wu.jb + c) * Hv + wu.h) * kRecStride : nullptr;
-        const int rcol = j0;
+        const int rcol = (wu.col0 + wc) >> 3;  // matrices of 8 columns
         float ks[4][NT][4], qs[4][NT][4];
 #pragma unroll
         for (int m = 0; m < 4; ++m)
@@ -174,7 +174,7 @@ __device__ __forceinline__ void walk_forward(const WalkUnit& wu, const WalkPipe&
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 if constexpr (REC) {
-                    put_record(S[k][n], rec + kRecS, 16384, 32768, 16 * k + g, rcol + 8 * n);
+                    put_record(S[k][n], rec + kRecS, 32768, 2 * k, rcol + n, lane);
                     b[n] = b_terms(S[k][n]);
                 } else {
                     b[n] = b_terms(S[k][n]);
@@ -313,7 +313,7 @@ __device__ __forceinline__ void walk_forward(const WalkUnit& wu, const WalkPipe&
 #pragma unroll
             for (int k = 0; k < 4; ++k)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) put_record(u[k][n], rec + kRecU, 8192, 16384, 16 * k + g, rcol + 8 * n);
+                for (int n = 0; n < NT; ++n) put_record(u[k][n], rec + kRecU, 16384, 2 * k, rcol + n, lane);
         } else {
             // O = e^g Q S + P U
 #pragma unroll
