@@ -22,21 +22,24 @@ using namespace gdn;
 
 // =============================================================== pass 1 ==
 // One CTA of four warps for a (chunk, q/k head) and `hp` of its value heads, which share the Gram
-// matrices: warp r holds rows 16 r of K K^T and Q K^T in registers.  Per value head: the decays and
+// matrices: K K^T's and Q K^T's ten 16 x 16 blocks on and below the diagonal stay in the warps' registers, at
+// most three of each to a warp.  Per value head: the decays and
 // b make A and P of them; the 16 x 16 diagonal blocks of I + A are inverted by forward substitution
 // in fp32 (stable for any A; a column for each of 64 threads); then warp j forms block column j of the
 // inverse, T_ij = -D_i sum_{j <= k < i} A_ik T_kj, by mma.sync on two-term operands, its blocks staying in
 // its registers.  (The block products in fp32 on the CUDA cores and one value head a CTA, 256 threads:
-// 109 us for 8192 tokens x 32 heads, 16.1 K warp instructions a (chunk, head).)
+// 109 us for 8192 tokens x 32 heads, 16.1 K warp instructions a (chunk, head); a warp for every row of blocks
+// and the decays of one value head after the other: 70 us.)
 constexpr int kPrepThreads = 128;
+constexpr int kPrepHeads = 4;  // most value heads of a CTA: a warp for each one's decays
 
 struct PrepSmem {
     static constexpr uint32_t K = 0, Q = 16384;  // 2 x [64][128 B] each, 128B-swizzled
     static constexpr uint32_t AH = 0;            // two terms of A's blocks, the diagonal ones inverted (over K and
     static constexpr uint32_t AL = kTriBytes;    // Q once the Gram matrices are out)
     static constexpr uint32_t DG = 16384;        // f32 [4][16][17]: diagonal blocks of A
-    static constexpr uint32_t G = 32768;         // f32 [3][64]: g (two terms, base 2), beta
-    static constexpr uint32_t BAR = G + 3 * C * 4;
+    static constexpr uint32_t G = 32768;         // f32 [heads][3][64]: g (two terms, base 2), beta
+    static constexpr uint32_t BAR = G + kPrepHeads * 3 * C * 4;
     static constexpr uint32_t TOTAL = BAR + 16;
     static constexpr uint32_t ALLOC = TOTAL + 1024;
 };
@@ -83,9 +86,6 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
         return;
 
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::BAR);
-    float* const g_hi = reinterpret_cast<float*>(sm + L::G);
-    float* const g_lo = g_hi + C;
-    float* const beta_s = g_lo + C;
     if (tid == 0) {
         mbar_init(bar, 1);
         fence_mbar_init();
@@ -97,9 +97,13 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
             tma_load_3d(sm + L::Q + kh * 8192, &tm_q, bar, 64 * kh, hk, static_cast<int32_t>(t0));
         }
     }
-    // Value head h's cumulative log decay (base 2, two tokens a lane, in fp64; kept as two fp32 terms), beta,
-    // and the image's decays.
-    auto decays = [&](int h) {
+    // A value head's cumulative log decay (base 2, two tokens a lane, in fp64; kept as two fp32 terms), beta, and
+    // the image's vectors.
+    if (warp < hp) {
+        const int h = h0 + warp;
+        float* const g_hi = reinterpret_cast<float*>(sm + L::G) + warp * 3 * C;
+        float* const g_lo = g_hi + C;
+        float* const beta_s = g_lo + C;
         double x[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -138,40 +142,45 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
             }
         }
         if (lane == 0) gv[kVecEc] = exp2f(static_cast<float>(last));
-    };
-    if (warp == 1) decays(h0);
+    }
     bool ok = true;
     if (tid == 0) ok = mbar_wait_pipe(bar, 0);
     if (!ok && p.device_status) atomicOr(p.device_status, KDA_DEV_TIMEOUT);
     __syncthreads();
 
-    // Gram rows up to the diagonal block.  The row block of a warp turns with the CTA, so that no quarter of
-    // the SM has the long rows of every CTA.
+    // The blocks of warp w (which turns with the CTA, so that no quarter of the SM has the long lists of every
+    // one): 0: (0, 0); 1: (1, 0), (1, 1), (3, 3); 2: (2, 0..2); 3: (3, 0..2).
     const int g = lane >> 2, t = lane & 3;
-    const int mr = (warp + blockIdx.x) & 3;
-    float kk[8][4], qk[8][4];
+    const int w = (warp + blockIdx.x) & 3;
+    const int row2 = w == 1 ? 3 : w, col2 = w == 1 ? 3 : 2;  // of the third one
+    float kk[3][2][4], qk[3][2][4];
 #pragma unroll
-    for (int n = 0; n < 8; ++n)
+    for (int s = 0; s < 3; ++s)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) kk[n][e] = qk[n][e] = 0.f;
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) kk[s][n][e] = qk[s][n][e] = 0.f;
     {
         const uint32_t kb = smem_u32(sm + L::K), qb = smem_u32(sm + L::Q);
-        const int ar = 16 * mr + (lane & 15), br = (lane & 7) + ((lane >> 4) << 3), bc = (lane >> 3) & 1;
+        const int ar = lane & 15, br = (lane & 7) + ((lane >> 4) << 3), bc = (lane >> 3) & 1;
 #pragma unroll
         for (int kt = 0; kt < 8; ++kt) {
-            uint32_t ak[4], aq[4];
             const uint32_t off = (kt >> 2) * 8192;
-            ldsm4(ak, kb + off + sw128_chunk(ar, 2 * (kt & 3) + (lane >> 4)));
-            ldsm4(aq, qb + off + sw128_chunk(ar, 2 * (kt & 3) + (lane >> 4)));
+            uint32_t ak[4], aq[4], b[4];
+            ldsm4(ak, kb + off + sw128_chunk(16 * w + ar, 2 * (kt & 3) + (lane >> 4)));
+            ldsm4(aq, qb + off + sw128_chunk(16 * w + ar, 2 * (kt & 3) + (lane >> 4)));
 #pragma unroll
-            for (int np = 0; np < 4; ++np) {
-                if (np > mr) break;
-                uint32_t b[4];
-                ldsm4(b, kb + off + sw128_chunk(16 * np + br, 2 * (kt & 3) + bc));
-                mma16(kk[2 * np], ak, b[0], b[1]);
-                mma16(kk[2 * np + 1], ak, b[2], b[3]);
-                mma16(qk[2 * np], aq, b[0], b[1]);
-                mma16(qk[2 * np + 1], aq, b[2], b[3]);
+            for (int s = 0; s < 3; ++s) {
+                if (s > 0 && w == 0) break;
+                if (s == 2 && w == 1) {
+                    ldsm4(ak, kb + off + sw128_chunk(48 + ar, 2 * (kt & 3) + (lane >> 4)));
+                    ldsm4(aq, qb + off + sw128_chunk(48 + ar, 2 * (kt & 3) + (lane >> 4)));
+                }
+                ldsm4(b, kb + off + sw128_chunk(16 * (s == 2 ? col2 : s) + br, 2 * (kt & 3) + bc));
+                mma16(kk[s][0], ak, b[0], b[1]);
+                mma16(kk[s][1], ak, b[2], b[3]);
+                mma16(qk[s][0], aq, b[0], b[1]);
+                mma16(qk[s][1], aq, b[2], b[3]);
             }
         }
     }
@@ -180,47 +189,50 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     for (int hh = 0; hh < hp; ++hh) {
         const int h = h0 + hh;
         uint8_t* const img = images + (static_cast<size_t>(j) * Hv + h) * stride;
-        __syncthreads();  // K and Q, or the previous head's A and decays, have been read
-        if (hh > 0) {
-            if (warp == 1) decays(h);
-            __syncthreads();
-        }
+        const float* const g_hi = reinterpret_cast<const float*>(sm + L::G) + hh * 3 * C;
+        const float* const g_lo = g_hi + C;
+        const float* const beta_s = g_lo + C;
+        __syncthreads();  // K and Q, or the previous head's A, have been read
         // A (two terms; its diagonal blocks in fp32) and P
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            if (n > 2 * mr + 1) break;
+        for (int s = 0; s < 3; ++s) {
+            if (s > 0 && w == 0) break;
+            const int bi = s == 2 ? row2 : w, bj = s == 2 ? col2 : s;
 #pragma unroll
-            for (int e2 = 0; e2 < 2; ++e2) {  // rows g and g + 8 of the tile
-                const int i = 16 * mr + g + 8 * e2;
-                const float2 ch = *reinterpret_cast<const float2*>(g_hi + 8 * n + 2 * t);
-                const float2 cl = *reinterpret_cast<const float2*>(g_lo + 8 * n + 2 * t);
-                const float gi = g_hi[i], gl = g_lo[i], b = beta_s[i];
-                const int jj = 8 * n + 2 * t;
-                const bool row = i < Lc;
-                const float d0 = exp2_sfu((gi - ch.x) + (gl - cl.x)), d1 = exp2_sfu((gi - ch.y) + (gl - cl.y));
-                const uint32_t pair = blk_pair(g, e2, n & 1, t);
-                const float p0 = row && jj <= i ? d0 * qk[n][2 * e2] : 0.f;
-                const float p1 = row && jj + 1 <= i ? d1 * qk[n][2 * e2 + 1] : 0.f;
-                uint32_t ph, pl;
-                split2(p0, p1, ph, pl);
-                uint8_t* const pp = img + tri_blk(mr, n >> 1) + pair;
-                *reinterpret_cast<uint32_t*>(pp + kImgP) = ph;
-                if (bwd) {
-                    *reinterpret_cast<uint32_t*>(pp + kImgPl) = pl;
-                    *reinterpret_cast<uint32_t*>(pp + kImgPl2) = third2(p0, p1, ph, pl);
-                }
-                const float a0 = row && jj < i ? b * d0 * kk[n][2 * e2] : 0.f;
-                const float a1 = row && jj + 1 < i ? b * d1 * kk[n][2 * e2 + 1] : 0.f;
-                if ((n >> 1) == mr) {
-                    float* d = dg + mr * 272 + (g + 8 * e2) * 17 + 8 * (n & 1) + 2 * t;
-                    d[0] = a0;
-                    d[1] = a1;
-                } else {
-                    uint32_t hi, lo;
-                    split2(a0, a1, hi, lo);
-                    uint8_t* const ap = sm + tri_blk(mr, n >> 1) + pair;
-                    *reinterpret_cast<uint32_t*>(ap + L::AH) = hi;
-                    *reinterpret_cast<uint32_t*>(ap + L::AL) = lo;
+            for (int n = 0; n < 2; ++n) {
+                const int jj = 16 * bj + 8 * n + 2 * t;
+                const float2 ch = *reinterpret_cast<const float2*>(g_hi + jj);
+                const float2 cl = *reinterpret_cast<const float2*>(g_lo + jj);
+#pragma unroll
+                for (int e2 = 0; e2 < 2; ++e2) {  // rows g and g + 8 of the block
+                    const int i = 16 * bi + g + 8 * e2;
+                    const float gi = g_hi[i], gl = g_lo[i], b = beta_s[i];
+                    const int last = i < Lc ? i : -1;  // columns up to this one count
+                    const float d0 = exp2_sfu((gi - ch.x) + (gl - cl.x)), d1 = exp2_sfu((gi - ch.y) + (gl - cl.y));
+                    const uint32_t pair = blk_pair(g, e2, n, t);
+                    const float p0 = jj <= last ? d0 * qk[s][n][2 * e2] : 0.f;
+                    const float p1 = jj + 1 <= last ? d1 * qk[s][n][2 * e2 + 1] : 0.f;
+                    uint32_t ph, pl;
+                    split2(p0, p1, ph, pl);
+                    uint8_t* const pp = img + tri_blk(bi, bj) + pair;
+                    *reinterpret_cast<uint32_t*>(pp + kImgP) = ph;
+                    if (bwd) {
+                        *reinterpret_cast<uint32_t*>(pp + kImgPl) = pl;
+                        *reinterpret_cast<uint32_t*>(pp + kImgPl2) = third2(p0, p1, ph, pl);
+                    }
+                    const float a0 = jj < last ? b * d0 * kk[s][n][2 * e2] : 0.f;
+                    const float a1 = jj + 1 < last ? b * d1 * kk[s][n][2 * e2 + 1] : 0.f;
+                    if (bi == bj) {
+                        float* d = dg + bi * 272 + (g + 8 * e2) * 17 + 8 * n + 2 * t;
+                        d[0] = a0;
+                        d[1] = a1;
+                    } else {
+                        uint32_t hi, lo;
+                        split2(a0, a1, hi, lo);
+                        uint8_t* const ap = sm + tri_blk(bi, bj) + pair;
+                        *reinterpret_cast<uint32_t*>(ap + L::AH) = hi;
+                        *reinterpret_cast<uint32_t*>(ap + L::AL) = lo;
+                    }
                 }
             }
         }
@@ -250,7 +262,6 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
         __syncthreads();
         // Block column w of the inverse by warp w.  T_ww = D_w from shared memory, the others from the products.
         {
-            const int w = mr;
             BTerms T[4][2];  // blocks (k, w) as B operands, two 8-column halves
             {
                 uint32_t bh[4], bl[4];
@@ -407,9 +418,11 @@ cudaError_t launch_gdn_prep(const GdnArgs& a, const GdnWorkspace& w, const CUten
     static int configured[64];
     const cudaError_t err = set_smem(kda_gdn_prep_kernel, PrepSmem::ALLOC, configured);
     if (err != cudaSuccess) return err;
-    // the value heads of a group share a CTA's Gram matrices where that leaves a CTA for every SM
+    // the value heads of a group (four, two or one of them) share a CTA's Gram matrices where that leaves a CTA
+    // for every SM
     const int m = a.Hv / a.Hk;
-    const int hp = w.chunks * a.Hk >= device_sm_count() ? m : 1;
+    int hp = m % 4 == 0 ? 4 : m % 2 == 0 ? 2 : 1;
+    while (hp > 1 && w.chunks * (a.Hv / hp) < device_sm_count()) hp /= 2;
     kda_gdn_prep_kernel<<<static_cast<unsigned>(w.chunks * (a.Hv / hp)), kPrepThreads, PrepSmem::ALLOC, stream>>>(
         tm_q, tm_k, a, w.table, w.images, w.chunks, hp, w.records != nullptr);
     return cudaGetLastError();
