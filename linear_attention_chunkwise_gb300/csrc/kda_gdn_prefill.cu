@@ -51,7 +51,7 @@ constexpr float kDecayFloor = -1e4f;
 // hold before b multiplies them, and b's own part in every sum is below fp32's rounding.
 constexpr float kBetaFloor = 8.271806e-25f;  // 2^-80
 
-__global__ void __launch_bounds__(kPrepThreads, 4)
+__global__ void __launch_bounds__(kPrepThreads, 5)
     kda_gdn_prep_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const GdnArgs p, const int32_t* __restrict__ co, uint8_t* images, int64_t chunk_slots,
                         int32_t hp, bool bwd) {
@@ -99,9 +99,10 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     }
     // A value head's cumulative log decay (base 2, two tokens a lane, in fp64; kept as two fp32 terms), beta, and
     // the image's vectors.
-    if (warp < hp) {
-        const int h = h0 + warp;
-        float* const g_hi = reinterpret_cast<float*>(sm + L::G) + warp * 3 * C;
+    const int dw = (warp + 3) & 3;  // warp 0, whose first thread is held by the copies it issues, comes last
+    if (dw < hp) {
+        const int h = h0 + dw;
+        float* const g_hi = reinterpret_cast<float*>(sm + L::G) + dw * 3 * C;
         float* const g_lo = g_hi + C;
         float* const beta_s = g_lo + C;
         double x[2];
