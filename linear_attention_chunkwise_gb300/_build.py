@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(HERE, "libkda.so")
 SOURCES = ["kda_api.cu", "kda_decode.cu", "kda_prefill.cu", "kda_prefill_split.cu", "kda_noalloc.cu",
-           "kda_backward.cu", "kda_gdn_api.cu", "kda_gdn_recurrent.cu", "kda_gdn_prefill.cu", "kda_gdn_backward.cu",
+           "kda_backward.cu", "kda_gdn_api.cu", "kda_gdn_recurrent.cu", "kda_gdn_prefill.cu", "kda_gdn_wide.cu", "kda_gdn_backward.cu",
            "kda_rms_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

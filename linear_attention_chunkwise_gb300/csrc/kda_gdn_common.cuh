@@ -28,6 +28,10 @@ constexpr size_t kImgStride = kImgPl, kImgStrideBwd = kImgPl2 + kTriBytes;
 static_assert((5 * C + 4) * 4 <= 1536 && kImgStride % kAlign == 0 && kImgStrideBwd % kAlign == 0 &&
                   kImgScanBytes % 16 == 0,
               "image layout");
+// The wide scan's images: T's two terms and P's first as whole 128B-swizzled [64][64] tiles, zero above the
+// diagonal, then the vectors.
+constexpr uint32_t kTileBytes = 8192;
+constexpr size_t kImgStrideTile = 3 * kTileBytes + 1536;
 // Block (i, j), j <= i, and within it the pair of columns 2 t, 2 t + 1 of its half n in row g (+ 8 e).
 __device__ __forceinline__ constexpr uint32_t tri_blk(int i, int j) { return (i * (i + 1) / 2 + j) * kBlkBytes; }
 __device__ __forceinline__ uint32_t blk_pair(int g, int e, int n, int t) { return (2 * n + e) * 128 + 16 * g + 4 * t; }

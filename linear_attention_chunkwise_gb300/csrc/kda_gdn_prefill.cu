@@ -13,6 +13,8 @@
 // pass 0  chunk table (launch_chunk_table)
 // pass 1  one CTA per (chunk, value head): Gram matrices, T, P, decays -> an image in the workspace
 // pass 2  scan: the walk of kda_gdn_walk.cuh over the chunks of every (sequence, value head).
+#include <algorithm>
+
 #include "kda_gdn_walk.cuh"
 
 namespace kda {
@@ -51,12 +53,16 @@ constexpr float kDecayFloor = -1e4f;
 // hold before b multiplies them, and b's own part in every sum is below fp32's rounding.
 constexpr float kBetaFloor = 8.271806e-25f;  // 2^-80
 
+template <bool TILE>
 __global__ void __launch_bounds__(kPrepThreads, 5)
     kda_gdn_prep_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const GdnArgs p, const int32_t* __restrict__ co, uint8_t* images, int64_t chunk_slots,
                         int32_t hp, bool bwd) {
     using L = PrepSmem;
-    const size_t stride = bwd ? kImgStrideBwd : kImgStride;
+    constexpr bool tile = TILE;
+    const size_t stride = tile ? kImgStrideTile : bwd ? kImgStrideBwd : kImgStride;
+    // T's terms and P are three matrices of this many bytes; the vectors follow
+    constexpr uint32_t mat = tile ? kTileBytes : kTriBytes;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -125,7 +131,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5)
             if (lane >= off) s += y;
         }
         const double last = __shfl_sync(0xffffffffu, s, 31);
-        float* gv = reinterpret_cast<float*>(images + (static_cast<size_t>(j) * Hv + h) * stride + kImgG);
+        float* gv = reinterpret_cast<float*>(images + (static_cast<size_t>(j) * Hv + h) * stride + 3 * mat);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int r = 2 * lane + e;
@@ -215,8 +221,8 @@ __global__ void __launch_bounds__(kPrepThreads, 5)
                     const float p1 = jj + 1 <= last ? d1 * qk[s][n][2 * e2 + 1] : 0.f;
                     uint32_t ph, pl;
                     split2(p0, p1, ph, pl);
-                    uint8_t* const pp = img + tri_blk(bi, bj) + pair;
-                    *reinterpret_cast<uint32_t*>(pp + kImgP) = ph;
+                    uint8_t* const pp = img + (tile ? sw128_chunk(i, 2 * bj + n) + 4 * t : tri_blk(bi, bj) + pair);
+                    *reinterpret_cast<uint32_t*>(pp + 2 * mat) = ph;
                     if (bwd) {
                         *reinterpret_cast<uint32_t*>(pp + kImgPl) = pl;
                         *reinterpret_cast<uint32_t*>(pp + kImgPl2) = third2(p0, p1, ph, pl);
@@ -235,6 +241,13 @@ __global__ void __launch_bounds__(kPrepThreads, 5)
                         *reinterpret_cast<uint32_t*>(ap + L::AL) = lo;
                     }
                 }
+            }
+        }
+        if (tile) {  // the blocks above the diagonal: rows of 16 r + .. end with 6 - 2 r chunks of 16 bytes
+            for (int e = tid; e < 3 * 48 * 6; e += kPrepThreads) {
+                const int m = e / 288, row = (e - 288 * m) / 6, ch = 7 - (e - 288 * m - 6 * row);
+                if (ch > 2 * (row >> 4) + 1)
+                    *reinterpret_cast<uint4*>(img + m * kTileBytes + sw128_chunk(row, ch)) = make_uint4(0u, 0u, 0u, 0u);
             }
         }
         __syncthreads();
@@ -281,9 +294,10 @@ __global__ void __launch_bounds__(kPrepThreads, 5)
                     for (int e2 = 0; e2 < 2; ++e2) {
                         uint32_t hi, lo;
                         split2(x[n][2 * e2], x[n][2 * e2 + 1], hi, lo);
-                        uint8_t* const tp = img + tri_blk(i, w) + blk_pair(g, e2, n, t);
-                        *reinterpret_cast<uint32_t*>(tp + kImgTh) = hi;
-                        *reinterpret_cast<uint32_t*>(tp + kImgTl) = lo;
+                        uint8_t* const tp = img + (tile ? sw128_chunk(16 * i + g + 8 * e2, 2 * w + n) + 4 * t
+                                                        : tri_blk(i, w) + blk_pair(g, e2, n, t));
+                        *reinterpret_cast<uint32_t*>(tp) = hi;
+                        *reinterpret_cast<uint32_t*>(tp + mat) = lo;
                     }
             };
             {  // the diagonal block itself, as accumulators hold it
@@ -347,9 +361,9 @@ __global__ void __launch_bounds__(kPrepThreads, 5)
 }
 
 // =============================================================== pass 2 ==
-template <int NT, int ST>
-struct ScanCfg : ForwardCfg<NT, 4, ST, false> {
-    using L = ForwardCfg<NT, 4, ST, false>;
+// Four warps of 8 columns: the narrow scan (kda_gdn_wide.cu has the one for many pairs).
+struct ScanCfg : ForwardCfg<1, 4, 3, false> {
+    using L = ForwardCfg<1, 4, 3, false>;
     static constexpr int kThreads = 160;  // four walking warps and the one that copies
     static constexpr uint32_t BARS = ST * L::STAGE;  // full[ST], empty[ST]
     static constexpr uint32_t ABORT = BARS + 16 * ST;
@@ -357,20 +371,19 @@ struct ScanCfg : ForwardCfg<NT, 4, ST, false> {
     static_assert(ALLOC <= 232448, "shared memory");
 };
 
-template <int NT, int ST>
-__global__ void __launch_bounds__(ScanCfg<NT, ST>::kThreads, 1)
+__global__ void __launch_bounds__(ScanCfg::kThreads, 1)
     kda_gdn_scan_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const GdnArgs p, const int32_t* __restrict__ co,
                         const int32_t* __restrict__ order, const uint8_t* __restrict__ images, int64_t chunk_slots) {
-    using L = ScanCfg<NT, ST>;
+    using L = ScanCfg;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const WalkPipe pipe{sm, reinterpret_cast<uint64_t*>(sm + L::BARS), reinterpret_cast<uint64_t*>(sm + L::BARS) + ST,
+    const WalkPipe pipe{sm, reinterpret_cast<uint64_t*>(sm + L::BARS), reinterpret_cast<uint64_t*>(sm + L::BARS) + L::ST,
                         reinterpret_cast<volatile int*>(sm + L::ABORT)};
     if (tid == 0) {
         *pipe.abort_s = 0;
-        pipe_init(pipe, ST, 4);
+        pipe_init(pipe, L::ST, 4);
         fence_mbar_init();
     }
     grid_wait();  // the images, and the table and order, of the launches before
@@ -380,25 +393,23 @@ __global__ void __launch_bounds__(ScanCfg<NT, ST>::kThreads, 1)
     if (warp == 4) {
         if (lane == 0) forward_copies<typename L::L>(u, pipe, p, &tm_q, &tm_k, &tm_v, images);
     } else {
-        walk_forward<typename L::L, NT>(u, pipe, p, nullptr, warp, lane);
+        walk_forward<typename L::L, 1>(u, pipe, p, nullptr, warp, lane);
     }
     __syncthreads();
     if (tid == 0 && *pipe.abort_s && p.device_status) atomicOr(p.device_status, KDA_DEV_TIMEOUT);
 }
 
-template <int NT, int ST>
 cudaError_t launch_scan(const GdnArgs& a, const GdnWorkspace& w, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                         cudaStream_t stream) {
-    using L = ScanCfg<NT, ST>;
+    using L = ScanCfg;
     static int configured[64];
-    cudaError_t err = set_smem(kda_gdn_scan_kernel<NT, ST>, L::ALLOC, configured);
+    cudaError_t err = set_smem(kda_gdn_scan_kernel, L::ALLOC, configured);
     if (err != cudaSuccess) return err;
     CUtensorMap tm_v;
-    if (!make_tensor_map(&tm_v, a.v, a.Hv, a.total_tokens, L::kCols, C,
-                         L::kVRow == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+    if (!make_tensor_map(&tm_v, a.v, a.Hv, a.total_tokens, L::kCols, C, CU_TENSOR_MAP_SWIZZLE_64B))
         return cudaErrorInvalidValue;
     const int64_t blocks = static_cast<int64_t>(a.num_seqs) * a.Hv * (D / L::kCols);
-    return launch_dependent(kda_gdn_scan_kernel<NT, ST>, blocks, L::kThreads, L::ALLOC, stream, tm_q, tm_k, tm_v, a,
+    return launch_dependent(kda_gdn_scan_kernel, blocks, L::kThreads, L::ALLOC, stream, tm_q, tm_k, tm_v, a,
                             w.table, w.order, w.images, w.chunks);
 }
 
@@ -414,29 +425,38 @@ cudaError_t launch_gdn_tables(const GdnArgs& a, const GdnWorkspace& w, cudaStrea
     return err;
 }
 
-cudaError_t launch_gdn_prep(const GdnArgs& a, const GdnWorkspace& w, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
-                            cudaStream_t stream) {
+// The prefill's scan: tcgen05, a CTA for the 128 columns of a (sequence, value head) pair, or mma.sync, four CTAs
+// of 32 columns.  A chunk takes the wide one 3.5 us, prep's larger images apart, the narrow one 1.54, so the narrow one is
+// ahead up to two of its CTAs an SM (8192 tokens: 64 pairs 270 us against 279, 96 pairs 274 against 214).
+bool scan_wide(const GdnArgs& a) { return static_cast<int64_t>(a.num_seqs) * a.Hv * 2 > device_sm_count(); }
+
+template <bool TILE>
+cudaError_t launch_prep(const GdnArgs& a, const GdnWorkspace& w, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                        cudaStream_t stream) {
     static int configured[64];
-    const cudaError_t err = set_smem(kda_gdn_prep_kernel, PrepSmem::ALLOC, configured);
+    const cudaError_t err = set_smem(kda_gdn_prep_kernel<TILE>, PrepSmem::ALLOC, configured);
     if (err != cudaSuccess) return err;
     // the value heads of a group (four, two or one of them) share a CTA's Gram matrices where that leaves a CTA
     // for every SM
     const int m = a.Hv / a.Hk;
     int hp = m % 4 == 0 ? 4 : m % 2 == 0 ? 2 : 1;
     while (hp > 1 && w.chunks * (a.Hv / hp) < device_sm_count()) hp /= 2;
-    kda_gdn_prep_kernel<<<static_cast<unsigned>(w.chunks * (a.Hv / hp)), kPrepThreads, PrepSmem::ALLOC, stream>>>(
+    kda_gdn_prep_kernel<TILE><<<static_cast<unsigned>(w.chunks * (a.Hv / hp)), kPrepThreads, PrepSmem::ALLOC, stream>>>(
         tm_q, tm_k, a, w.table, w.images, w.chunks, hp, w.records != nullptr);
     return cudaGetLastError();
 }
 
-// 32 columns a CTA while that many CTAs find an SM each (the shortest chain: 1.54 us a chunk), else 64
-// (packed 24.6 k tokens x 32 heads: 663 us against 701 us).
+cudaError_t launch_gdn_prep(const GdnArgs& a, const GdnWorkspace& w, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                            cudaStream_t stream) {
+    return !w.records && scan_wide(a) ? launch_prep<true>(a, w, tm_q, tm_k, stream) : launch_prep<false>(a, w, tm_q, tm_k, stream);
+}
+
+// 32 columns a CTA while that many CTAs find an SM each.
 bool gdn_narrow(int32_t num_seqs, int32_t Hv) { return static_cast<int64_t>(num_seqs) * Hv * 4 <= device_sm_count(); }
 
 cudaError_t launch_gdn_scan(const GdnArgs& a, const GdnWorkspace& w, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                             cudaStream_t stream) {
-    return gdn_narrow(a.num_seqs, a.Hv) ? launch_scan<1, 3>(a, w, tm_q, tm_k, stream)
-                                        : launch_scan<2, 3>(a, w, tm_q, tm_k, stream);
+    return scan_wide(a) ? launch_gdn_wide(a, w, tm_q, tm_k, stream) : launch_scan(a, w, tm_q, tm_k, stream);
 }
 
 size_t gdn_workspace(int32_t num_seqs, int64_t total_tokens, int32_t Hv, bool bwd, uint8_t* base, GdnWorkspace* w) {
@@ -444,7 +464,7 @@ size_t gdn_workspace(int32_t num_seqs, int64_t total_tokens, int32_t Hv, bool bw
     const size_t units = static_cast<size_t>(chunks) * Hv;
     const size_t table = round_up(static_cast<size_t>(num_seqs > 0 ? num_seqs : 1) * 4, kAlign);
     const size_t images = table + round_up((static_cast<size_t>(num_seqs) + 2) * 4, kAlign);
-    const size_t records = images + units * (bwd ? kImgStrideBwd : kImgStride);
+    const size_t records = images + units * (bwd ? kImgStrideBwd : std::max(kImgStride, kImgStrideTile));
     if (w) {
         // one sequence needs no table; and where every CTA has an SM of its own, their order does not matter
         w->order = num_seqs > 1 && !gdn_narrow(num_seqs, Hv) ? reinterpret_cast<int32_t*>(base) : nullptr;

@@ -209,12 +209,14 @@ struct GdnWorkspace {
 // Bytes of the workspace, and (w not NULL) its regions from `base`; bwd: the gradient's.
 size_t gdn_workspace(int32_t num_seqs, int64_t total_tokens, int32_t Hv, bool bwd, uint8_t* base, GdnWorkspace* w);
 cudaError_t launch_gdn_tables(const GdnArgs& a, const GdnWorkspace& w, cudaStream_t stream);
-// Whether the walks take 32 columns a CTA (else 64).
+// Whether CTAs of 32 columns find an SM each (else the gradient's walks take 64, and sequences go by length).
 bool gdn_narrow(int32_t num_seqs, int32_t Hv);
 // tm_q, tm_k: maps of q and k with boxes of 64 tokens x 64 channels, 128B-swizzled.
 cudaError_t launch_gdn_prep(const GdnArgs& a, const GdnWorkspace& w, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                             cudaStream_t stream);
 cudaError_t launch_gdn_scan(const GdnArgs& a, const GdnWorkspace& w, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                            cudaStream_t stream);
+cudaError_t launch_gdn_wide(const GdnArgs& a, const GdnWorkspace& w, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                             cudaStream_t stream);
 struct GdnBackwardArgs {
     const void* grad_o = nullptr;          // [T, Hv, 128]

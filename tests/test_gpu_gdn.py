@@ -215,3 +215,82 @@ def test_decode_replayed_steps_match_the_prefill():
             c.copy_(x[n][t:t + 1])
         graph.replay()
     check_state(S, rs)
+
+
+# ------------------------------------------- one CTA for a pair's 128 columns ----
+# More than half as many (sequence, value head) pairs as a GPU has SMs take the wide scan (80 on 152 SMs).
+WIDE = [([1 + (37 * i) % 131 for i in range(20)], 2, 4), ([64] * 40, 1, 2), ([0, 200, 65, 0, 1, 0, 129, 63, 0, 448], 4, 12),
+        ([700], 40, 80), ([257, 40], 24, 48), ([900, 0, 330], 16, 32)]
+
+
+@pytest.mark.parametrize("lengths,Hk,Hv", WIDE)
+def test_prefill_many_pairs(lengths, Hk, Hv):
+    x = inputs(lengths, Hk, Hv, seed=81 + sum(lengths))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, S = kda.kda_gdn_prefill(**x, device_status=status)
+    assert int(status.item()) == 0
+    check(x, o, S)
+    y = dict(x, S0=x["S0"].clone())
+    o2, S2 = kda.kda_gdn_prefill(**y, S_final=y["S0"])
+    assert torch.equal(S, S2) and torch.equal(o, o2)
+    o3, S3 = kda.kda_gdn_prefill(**dict(x, S0=None))
+    check(dict(x, S0=torch.zeros_like(x["S0"])), o3, S3)
+
+
+def test_prefill_many_pairs_extreme_decays():
+    x = inputs([700, 1, 130], 16, 32, seed=82)
+    ld = x["log_decay"]
+    ld[3, 0], ld[7, 1], ld[8, 0] = -np.inf, torch.finfo(torch.float32).min, -1000.0
+    ld[10:14] = 0.0
+    ld[400:, 1] = -30.0
+    x["beta"][5], x["beta"][6] = 0.0, 1.0
+    check(x, *kda.kda_gdn_prefill(**x))
+
+
+@pytest.mark.parametrize("Hk,Hv", [(1, 2), (16, 32)])
+def test_prefill_keeps_a_bad_sequence_to_itself(Hk, Hv):
+    """A sequence of NaNs leaves its neighbours' outputs and states as they are without it."""
+    x = inputs([70, 100, 61, 33], Hk, Hv, seed=83)
+    o, S = kda.kda_gdn_prefill(**x)
+    for n in ("q", "k", "v", "log_decay", "beta"):
+        x[n][70:170] = float("nan")
+    o2, S2 = kda.kda_gdn_prefill(**x)
+    keep = [0, 2, 3]
+    assert torch.equal(S[keep], S2[keep]) and torch.equal(o[:70], o2[:70]) and torch.equal(o[170:], o2[170:])
+    assert bool(S2[1].isnan().any()) and bool(o2[70:170].isnan().any())
+
+
+@pytest.mark.parametrize("cu", [[0, 50, 40, 100], [0, 30, 60, 99], [1, 30, 60, 100], [0, -5, 60, 100], [0, 30, 200, 100]])
+def test_prefill_many_pairs_bad_cu_seqlens(cu):
+    x = inputs([30, 30, 40], 16, 32, seed=84)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    guard = torch.full((120, 32, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    x["cu_seqlens"] = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    kda.kda_gdn_prefill(**x, o=guard[:100], device_status=status)
+    assert int(status.item()) == kda.KDA_DEV_BAD_CU_SEQLENS
+    assert bool((guard[100:] == 7.0).all())
+
+
+@pytest.mark.parametrize("Hv", [2, 80])
+@pytest.mark.parametrize("cu", [[0, 99], [1, 100], [0, 101], [0, -1], [-1, 100]])
+def test_prefill_one_sequence_bad_cu_seqlens(cu, Hv):
+    x = inputs([100], Hv, Hv, seed=85)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    guard = torch.full((120, Hv, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    x["cu_seqlens"] = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    kda.kda_gdn_prefill(**x, o=guard[:100], device_status=status)
+    assert int(status.item()) == kda.KDA_DEV_BAD_CU_SEQLENS
+    assert bool((guard[100:] == 7.0).all())
+
+
+def test_prefill_many_pairs_on_two_streams():
+    a, b = inputs([300, 100], 24, 48, seed=86), inputs([130, 64, 77], 16, 32, seed=87)
+    ra, rb = kda.kda_gdn_prefill(**a), kda.kda_gdn_prefill(**b)
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        got.append((kda.kda_gdn_prefill(**a, stream=one), kda.kda_gdn_prefill(**b, stream=two)))
+    torch.cuda.synchronize()
+    for ga, gb in got:
+        assert torch.equal(ga[0], ra[0]) and torch.equal(ga[1], ra[1]) and torch.equal(gb[0], rb[0]) and torch.equal(gb[1], rb[1])
