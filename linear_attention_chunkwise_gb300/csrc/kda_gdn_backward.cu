@@ -16,10 +16,12 @@
 // decay of 0 gives exactly 0.)
 //
 // Kernels: the prefill's prep; a walk over the chunks (leaving S and U) and beside it one back (leaving X and
-// W, writing dv and the start state's gradient); and one CTA per (chunk, q/k head) for the rest, which adds
-// up the value heads of a group in its registers.  Operands that are not raw bf16 inputs are two bf16 terms
+// W, writing dv and the start state's gradient); and the rest by (chunk, q/k head), the value heads of a group
+// added up in registers.  Operands that are not raw bf16 inputs are two bf16 terms
 // wherever the result is kept in fp32 (states, decays, b); M and E, which only reach the bf16 dq and dk,
 // are one.
+#include <algorithm>
+
 #include "kda_gdn_walk.cuh"
 
 namespace kda {
@@ -367,20 +369,27 @@ __global__ void __launch_bounds__(WalksCfg<NT>::kThreads, 1)
 }
 
 // ============================================================== the rest ==
-// One CTA of 8 warps per (chunk, q/k head).  Warp (mr, nh): tokens 16 mr, channels 64 nh of dq and dk.
+// A CTA of 8 warps for every SM, each going over its share of the (chunk, q/k head) units and over the value
+// heads of each.  What the next value head needs is copied as soon as its place is free: S and dO once S and X
+// have been read (S goes where X was), U and W behind the 64 x 64 products, X once dO is in registers.
+// 8192 tokens x 16/32 heads: 377 us, 420 with a CTA for every unit, whose first copies nothing hides.  What bounds it
+// is mma.sync at two warps an SM quarter (255 registers a thread): the tensor pipe is busy 47% of the time.
+// Warp (mr, nh): tokens 16 mr, channels 64 nh of dq and dk.
 // Of the 64 x 64 products the warps nh = 0 form dP and Q K^T, the others dA and K K^T; the two warps of an
 // SM quarter have row blocks mr and 3 - mr, so that the quarters' triangles are even.
 constexpr int kRestThreads = 256;
 struct RestSmem {
-    static constexpr uint32_t S = 0, X = 65536, U = 131072, W = 163840;  // as in the record
+    static constexpr uint32_t SX = 0, kSX = 65536;   // S and X of a record, in turn in either place
+    static constexpr uint32_t U = 131072, W = 163840;
     static constexpr uint32_t K = 196608, Q = 212992;
     static constexpr uint32_t G = 229376;            // the image's vectors
-    static constexpr uint32_t BARS = G + 1328;       // u64: K and Q, S and W, X and U, dO
+    static constexpr uint32_t BARS = G + 1328;       // u64: K and Q, S and dO, X, U and W
     static constexpr uint32_t TOTAL = BARS + 32;
     static constexpr uint32_t ALLOC = TOTAL + 1024;
-    // over S once it and X have been read
+    // over S once it and X have been read; behind them the next dO
     static constexpr uint32_t M = 0, E = 8192;       // bf16 [64][64], 128B-swizzled
     static constexpr uint32_t P = 16384;             // f32: parts of the sums, below
+    static constexpr uint32_t DO = 32768;            // [2][64][128 B], 128B-swizzled
 };
 static_assert(RestSmem::ALLOC <= 232448 && RestSmem::BARS % 8 == 0, "shared memory");
 // parts (floats): a per nh [2][64], w per nh [2][64], the pairs' sums per warp [8][64], db [64],
@@ -396,67 +405,69 @@ __global__ void __launch_bounds__(kRestThreads, 1)
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int N = p.num_seqs, Hv = p.Hv, group = Hv / p.Hk;
-    const int j = blockIdx.x / p.Hk, hk = blockIdx.x - j * p.Hk;
     grid_wait();  // the walks' records
-    if (!table_ok(p, co) || j >= table_at(p, co, N)) return;
-    int seq = 0;
-    if (co) {  // the largest n with co[n] <= j
-        int lo = 0, hi = N - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (co[mid] <= j) lo = mid;
-            else hi = mid - 1;
-        }
-        seq = lo;
-    }
-    const int64_t t0 = static_cast<int64_t>(p.cu_seqlens[seq]) + static_cast<int64_t>(j - table_at(p, co, seq)) * C;
-    const int64_t rem = p.cu_seqlens[seq + 1] - t0;
-    const int Lc = static_cast<int>(rem < C ? rem : C);
-    if (!KDA_BOUNDS(seq >= 0 && seq < N && j < chunk_slots && t0 >= 0 && Lc >= 1 && t0 + Lc <= p.total_tokens,
-                    p.device_status))
-        return;
+    if (!table_ok(p, co)) return;
+    const int units = table_at(p, co, N) * p.Hk;
+    // The first token and the number of tokens of a unit's chunk; units come in rising order.
+    int seq = 0, tok0, Lc, next_tok0 = 0, next_Lc = 0;
+    auto locate = [&](int unit, int& tok, int& len) {
+        if (unit >= units) return false;
+        const int j = unit / p.Hk;
+        while (seq + 1 < N && table_at(p, co, seq + 1) <= j) ++seq;
+        const int64_t t0 = static_cast<int64_t>(p.cu_seqlens[seq]) + static_cast<int64_t>(j - table_at(p, co, seq)) * C;
+        const int64_t rem = p.cu_seqlens[seq + 1] - t0;
+        tok = static_cast<int>(t0);
+        len = static_cast<int>(rem < C ? rem : C);
+        return KDA_BOUNDS(seq >= 0 && seq < N && j < chunk_slots && t0 >= 0 && len >= 1 && t0 + len <= p.total_tokens,
+                          p.device_status);
+    };
+    int unit = blockIdx.x;
+    if (!locate(unit, tok0, Lc)) return;
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BARS);
     float* const gs = reinterpret_cast<float*>(sm + L::G);
-    float* const parts = reinterpret_cast<float*>(sm + L::P);
-    const size_t unit0 = static_cast<size_t>(j) * Hv + static_cast<size_t>(hk) * group;
-    auto issue = [&](int hh) {  // a value head's record
-        const uint8_t* rec = records + (unit0 + hh) * kRecStride;
-        mbar_arrive_expect_tx(&bars[1], 65536 + 32768);
-        bulk_g2s(sm + L::S, rec + kRecS, 65536, &bars[1]);
-        bulk_g2s(sm + L::W, rec + kRecW, 32768, &bars[1]);
-        // dO's tile through X's place: X and U follow once its fragments are in registers
-        mbar_arrive_expect_tx(&bars[3], 16384);
-#pragma unroll
-        for (int kh = 0; kh < 2; ++kh)
-            tma_load_3d(sm + L::X + kh * 8192, &tm_do, &bars[3], 64 * kh, hk * group + hh, static_cast<int32_t>(t0));
+    // the copies of value head hh of a unit, whose chunk starts at token tok: record and image (j Hv + h)
+    auto record = [&](int u, int hh) {
+        return records + (static_cast<size_t>(u / p.Hk) * Hv + static_cast<size_t>(u % p.Hk) * group + hh) * kRecStride;
     };
-    auto issue_x = [&](int hh) {
-        const uint8_t* rec = records + (unit0 + hh) * kRecStride;
-        mbar_arrive_expect_tx(&bars[2], 65536 + 32768);
-        bulk_g2s(sm + L::X, rec + kRecX, 65536, &bars[2]);
-        bulk_g2s(sm + L::U, rec + kRecU, 32768, &bars[2]);
-    };
-    if (tid == 0) {
-        for (int i = 0; i < 4; ++i) mbar_init(&bars[i], 1);
-        fence_mbar_init();
+    auto issue_kq = [&](int u, int tok) {
         mbar_arrive_expect_tx(&bars[0], 32768);
 #pragma unroll
         for (int kh = 0; kh < 2; ++kh) {
-            tma_load_3d(sm + L::K + kh * 8192, &tm_k, &bars[0], 64 * kh, hk, static_cast<int32_t>(t0));
-            tma_load_3d(sm + L::Q + kh * 8192, &tm_q, &bars[0], 64 * kh, hk, static_cast<int32_t>(t0));
+            tma_load_3d(sm + L::K + kh * 8192, &tm_k, &bars[0], 64 * kh, u % p.Hk, tok);
+            tma_load_3d(sm + L::Q + kh * 8192, &tm_q, &bars[0], 64 * kh, u % p.Hk, tok);
         }
-        issue(0);
+    };
+    auto issue_s = [&](int u, int hh, int tok, uint32_t s_at, uint32_t x_at) {  // dO through X's place
+        mbar_arrive_expect_tx(&bars[1], 65536 + 16384);
+        bulk_g2s(sm + s_at, record(u, hh) + kRecS, 65536, &bars[1]);
+#pragma unroll
+        for (int kh = 0; kh < 2; ++kh)
+            tma_load_3d(sm + x_at + L::DO + kh * 8192, &tm_do, &bars[1], 64 * kh, u % p.Hk * group + hh, tok);
+    };
+    auto issue_x = [&](int u, int hh, uint32_t x_at) {
+        mbar_arrive_expect_tx(&bars[2], 65536);
+        bulk_g2s(sm + x_at, record(u, hh) + kRecX, 65536, &bars[2]);
+    };
+    auto issue_uw = [&](int u, int hh) {
+        mbar_arrive_expect_tx(&bars[3], 65536);
+        bulk_g2s(sm + L::U, record(u, hh) + kRecU, 65536, &bars[3]);  // W follows U
+    };
+    auto image_vec = [&](int u, int hh) {
+        return reinterpret_cast<const float*>(
+            images + (static_cast<size_t>(u / p.Hk) * Hv + static_cast<size_t>(u % p.Hk) * group + hh) * kImgStrideBwd + kImgG);
+    };
+    constexpr int kVec = 5 * C + 4;
+    static_assert(kRecW == kRecU + 32768 && L::W == L::U + 32768 && kVec <= 2 * kRestThreads, "layouts");
+    if (tid == 0) {
+        for (int i = 0; i < 4; ++i) mbar_init(&bars[i], 1);
+        fence_mbar_init();
+        issue_s(unit, 0, tok0, L::SX, L::SX + L::kSX);
+        issue_uw(unit, 0);
+        issue_kq(unit, tok0);
     }
+    for (int e = tid; e < kVec; e += kRestThreads) gs[e] = image_vec(unit, 0)[e];
     __syncthreads();
-    bool ok = mbar_wait_pipe(&bars[0], 0);
-    if (Lc < C) {  // rows behind the sequence's end
-        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-        for (int e = tid; e < (C - Lc) * 16; e += kRestThreads) {
-            const uint32_t off = (e & 1) * 8192 + sw128_chunk(Lc + (e >> 4), (e >> 1) & 7);
-            *reinterpret_cast<uint4*>(sm + L::K + off) = z;
-            *reinterpret_cast<uint4*>(sm + L::Q + off) = z;
-        }
-    }
+    bool ok = true;
     const int g = lane >> 2, t = lane & 3;
     const int nh = warp >> 2, mr = nh ? 7 - warp : warp;
     const int lr = lane & 15, lc = lane >> 4;                                      // row-major A operand
@@ -471,23 +482,30 @@ __global__ void __launch_bounds__(kRestThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) dq[n][e] = dk[n][e] = 0.f;
 
-    for (int hh = 0; hh < group; ++hh) {
-        const int h = hk * group + hh;
-        const uint32_t par = hh & 1;
-        const float* vec = reinterpret_cast<const float*>(images + (unit0 + hh) * kImgStrideBwd + kImgG);
-        for (int e = tid; e < 5 * C + 4; e += kRestThreads) gs[e] = vec[e];
+    uint32_t kq_par = 0;
+    for (int it = 0, hh = 0;; ++it) {  // value head hh of a unit
+        const uint32_t par = it & 1, s_at = L::SX + L::kSX * par, x_at = L::SX + L::kSX * (par ^ 1);
+        float* const parts = reinterpret_cast<float*>(sm + s_at + L::P);
+        if (hh == 0 && Lc < C) {  // rows behind the sequence's end
+            ok = mbar_wait_pipe(&bars[0], kq_par) && ok;
+            const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+            for (int e = tid; e < (C - Lc) * 16; e += kRestThreads) {
+                const uint32_t off = (e & 1) * 8192 + sw128_chunk(Lc + (e >> 4), (e >> 1) & 7);
+                *reinterpret_cast<uint4*>(sm + L::K + off) = z;
+                *reinterpret_cast<uint4*>(sm + L::Q + off) = z;
+            }
+        }
         uint32_t dof[8][4];  // dO rows 16 mr as A operand
-        ok = mbar_wait_pipe(&bars[3], par) && ok;
+        ok = mbar_wait_pipe(&bars[1], par) && ok;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            ldsm4(dof[k], base + L::X + (k >> 2) * 8192 + sw128_chunk(16 * mr + lr, 2 * (k & 3) + lc));
+            ldsm4(dof[k], base + x_at + L::DO + (k >> 2) * 8192 + sw128_chunk(16 * mr + lr, 2 * (k & 3) + lc));
             const bool r0 = 16 * mr + g < Lc, r1 = 16 * mr + g + 8 < Lc;
             if (!r0) dof[k][0] = dof[k][2] = 0u;
             if (!r1) dof[k][1] = dof[k][3] = 0u;
         }
-        ok = mbar_wait_pipe(&bars[1], par) && ok;
         __syncthreads();  // the vectors (and the cleared rows) are there, dO's tile has been read
-        if (tid == 0) issue_x(hh);
+        if (tid == 0) issue_x(unit, hh, x_at);
         float eg[2], eo[2], be[2], gh[2], gl[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -515,6 +533,7 @@ __global__ void __launch_bounds__(kRestThreads, 1)
             }
         };
         float row_a[2], row_w[2];
+        ok = mbar_wait_pipe(&bars[3], par) && ok;
         {  // dO S^T and W S^T
             float a1[8][4], a2[8][4];
 #pragma unroll
@@ -530,7 +549,7 @@ __global__ void __launch_bounds__(kRestThreads, 1)
 #pragma unroll
                 for (int np = 0; np < 4; ++np) {
                     uint32_t sh[4], sl[4];
-                    const uint32_t sa = base + L::S + lb + (4 * nh + np) * 4096 + k * 256;
+                    const uint32_t sa = base + s_at + lb + (4 * nh + np) * 4096 + k * 256;
                     ldsm4(sh, sa);
                     ldsm4(sl, sa + 32768);
 #pragma unroll
@@ -544,6 +563,7 @@ __global__ void __launch_bounds__(kRestThreads, 1)
                 }
             }
             float d1[2], d2[2];
+            if (hh == 0) ok = mbar_wait_pipe(&bars[0], kq_par) && ok;
             row_dots(a1, L::Q, d1);
             row_dots(a2, L::K, d2);
 #pragma unroll
@@ -572,7 +592,7 @@ __global__ void __launch_bounds__(kRestThreads, 1)
 #pragma unroll
                 for (int np = 0; np < 4; ++np) {
                     uint32_t xh[4], xl[4];
-                    const uint32_t xa = base + L::X + lb + (4 * nh + np) * 4096 + k * 256;
+                    const uint32_t xa = base + x_at + lb + (4 * nh + np) * 4096 + k * 256;
                     ldsm4(xh, xa);
                     ldsm4(xl, xa + 32768);
 #pragma unroll
@@ -593,8 +613,8 @@ __global__ void __launch_bounds__(kRestThreads, 1)
         }
         float inner = 0.f;  // <X, S>
         for (int e = tid; e < 2048; e += kRestThreads) {
-            const uint4 sh = *reinterpret_cast<const uint4*>(sm + L::S + 16 * e), sl = *reinterpret_cast<const uint4*>(sm + L::S + 32768 + 16 * e);
-            const uint4 xh = *reinterpret_cast<const uint4*>(sm + L::X + 16 * e), xl = *reinterpret_cast<const uint4*>(sm + L::X + 32768 + 16 * e);
+            const uint4 sh = *reinterpret_cast<const uint4*>(sm + s_at + 16 * e), sl = *reinterpret_cast<const uint4*>(sm + s_at + 32768 + 16 * e);
+            const uint4 xh = *reinterpret_cast<const uint4*>(sm + x_at + 16 * e), xl = *reinterpret_cast<const uint4*>(sm + x_at + 32768 + 16 * e);
             const uint32_t* a = &sh.x;
             const uint32_t* b = &sl.x;
             const uint32_t* c = &xh.x;
@@ -608,7 +628,11 @@ __global__ void __launch_bounds__(kRestThreads, 1)
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, off);
-        __syncthreads();  // S and X have been read: M, E and the parts take S's place
+        const bool last = hh + 1 == group;  // of the unit; the next item is another's first head then
+        const int next_unit = last ? unit + static_cast<int>(gridDim.x) : unit, next_hh = last ? 0 : hh + 1;
+        const bool more = !last || locate(next_unit, next_tok0, next_Lc);
+        __syncthreads();  // S and X have been read: M, E and the parts take S's place, the next S X's
+        if (tid == 0 && more) issue_s(next_unit, next_hh, last ? next_tok0 : tok0, x_at, s_at);
         if (t == 0) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -713,7 +737,7 @@ __global__ void __launch_bounds__(kRestThreads, 1)
                     left[e2] += __shfl_sync(0xffffffffu, sum, 3, 4);
                     if (jj <= i) cs[0] += before;
                     if (jj + 1 <= i) cs[1] += before + d[0];
-                    *reinterpret_cast<uint32_t*>(sm + (nh ? L::E : L::M) + sw128_chunk(i, 4 * ph + n) + 4 * t) =
+                    *reinterpret_cast<uint32_t*>(sm + s_at + (nh ? L::E : L::M) + sw128_chunk(i, 4 * ph + n) + 4 * t) =
                         pack_bf16(m[0], m[1]);
                 }
 #pragma unroll
@@ -725,12 +749,19 @@ __global__ void __launch_bounds__(kRestThreads, 1)
             }
         }
         __syncthreads();
+        float vec[2] = {0.f, 0.f};  // of the next item
+        if (more) {
+            if (tid == 0) issue_uw(next_unit, next_hh);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (tid + kRestThreads * e < kVec) vec[e] = image_vec(next_unit, next_hh)[tid + kRestThreads * e];
+        }
         // dq += M K, dk += E K (columns up to the own rows), dk += E^T K + M^T Q (rows from the own columns on)
 #pragma unroll 1
         for (int k = 0; k <= mr; ++k) {
             uint32_t am[4], ae[4];
-            ldsm4(am, base + L::M + sw128_chunk(16 * mr + lr, 2 * k + lc));
-            ldsm4(ae, base + L::E + sw128_chunk(16 * mr + lr, 2 * k + lc));
+            ldsm4(am, base + s_at + L::M + sw128_chunk(16 * mr + lr, 2 * k + lc));
+            ldsm4(ae, base + s_at + L::E + sw128_chunk(16 * mr + lr, 2 * k + lc));
 #pragma unroll
             for (int np = 0; np < 4; ++np) {
                 uint32_t kf[4];
@@ -745,8 +776,8 @@ __global__ void __launch_bounds__(kRestThreads, 1)
 #pragma unroll 1
         for (int k = mr; k < 4; ++k) {
             uint32_t tm[4], te[4];
-            ldsm4t(tm, base + L::M + sw128_chunk(16 * k + br, 2 * mr + bc));
-            ldsm4t(te, base + L::E + sw128_chunk(16 * k + br, 2 * mr + bc));
+            ldsm4t(tm, base + s_at + L::M + sw128_chunk(16 * k + br, 2 * mr + bc));
+            ldsm4t(te, base + s_at + L::E + sw128_chunk(16 * k + br, 2 * mr + bc));
 #pragma unroll
             for (int np = 0; np < 4; ++np) {
                 uint32_t kf[4], qf[4];
@@ -760,6 +791,7 @@ __global__ void __launch_bounds__(kRestThreads, 1)
                 }
             }
         }
+        const int hk = unit % p.Hk, h = hk * group + hh;
         if (warp == 0) {  // the decays' and b's gradients, two tokens a lane
             float ra[2], rw[2], pairs[2], in = 0.f;
 #pragma unroll
@@ -790,29 +822,44 @@ __global__ void __launch_bounds__(kRestThreads, 1)
                 const int r = 2 * lane + e;
                 const float a_on = after + (e ? ra[1] : ra[0] + ra[1]), w_before = e ? before + rw[0] : before;
                 if (r < Lc) {
-                    gr.grad_log_decay[(t0 + r) * Hv + h] = (pairs[e] + a_on) + (w_before + in);
-                    gr.grad_beta[(t0 + r) * Hv + h] = parts[kPtB + r];
+                    gr.grad_log_decay[static_cast<int64_t>(tok0 + r) * Hv + h] = (pairs[e] + a_on) + (w_before + in);
+                    gr.grad_beta[static_cast<int64_t>(tok0 + r) * Hv + h] = parts[kPtB + r];
                 }
             }
         }
-        fence_async_smem();  // M, E, the parts and the vectors, before the next record's copies
+        fence_async_smem();  // M, E, the parts and the cleared rows, before the next copies
         __syncthreads();
-        if (tid == 0 && hh + 1 < group) issue(hh + 1);
+        if (last) {
+            if (tid == 0 && more) issue_kq(next_unit, next_tok0);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = 16 * mr + g + 8 * e;
+                if (row >= Lc) continue;
+                const int64_t off = (static_cast<int64_t>(tok0 + row) * p.Hk + hk) * D + 64 * nh + 2 * t;
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(gr.grad_q) + off + 8 * n) =
+                        pack_bf16(dq[n][2 * e], dq[n][2 * e + 1]);
+                    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(gr.grad_k) + off + 8 * n) =
+                        pack_bf16(dk[n][2 * e], dk[n][2 * e + 1]);
+                }
+            }
+            if (!more) break;
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dq[n][e] = dk[n][e] = 0.f;
+            unit = next_unit;
+            tok0 = next_tok0;
+            Lc = next_Lc;
+            kq_par ^= 1;
+        }
+        hh = next_hh;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (tid + kRestThreads * e < kVec) gs[tid + kRestThreads * e] = vec[e];
     }
     if (!ok && p.device_status) atomicOr(p.device_status, KDA_DEV_TIMEOUT);
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int row = 16 * mr + g + 8 * e;
-        if (row >= Lc) continue;
-        const int64_t off = ((t0 + row) * p.Hk + hk) * D + 64 * nh + 2 * t;
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(gr.grad_q) + off + 8 * n) =
-                pack_bf16(dq[n][2 * e], dq[n][2 * e + 1]);
-            *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(gr.grad_k) + off + 8 * n) =
-                pack_bf16(dk[n][2 * e], dk[n][2 * e + 1]);
-        }
-    }
 }
 
 template <int NT>
@@ -846,7 +893,8 @@ cudaError_t launch_gdn_backward(const GdnArgs& a, const GdnBackwardArgs& b, cons
     static int configured[64];
     if (err == cudaSuccess) err = set_smem(kda_gdn_grad_kernel, RestSmem::ALLOC, configured);
     if (err != cudaSuccess) return err;
-    return launch_dependent(kda_gdn_grad_kernel, w.chunks * a.Hk, kRestThreads, RestSmem::ALLOC, stream, tm_q, tm_k, tm_do, a,
+    const int64_t blocks = std::min<int64_t>(w.chunks * a.Hk, device_sm_count());
+    return launch_dependent(kda_gdn_grad_kernel, blocks, kRestThreads, RestSmem::ALLOC, stream, tm_q, tm_k, tm_do, a,
                             b, w.table, w.images, w.chunks, w.records);
 }
 

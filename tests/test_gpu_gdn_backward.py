@@ -180,3 +180,13 @@ def test_backward_is_the_forwards_slope():
     noise = 2.0 ** -12 * float(dS.double().norm()) * float(kda.kda_gdn_prefill(**x)[1].double().norm())
     assert abs((loss(step) - loss(-step)) / (2 * step) - slope) <= 1e-3 * size + noise
     assert abs(slope) > 10 * (1e-3 * size + noise)
+
+
+@pytest.mark.parametrize("lengths,Hk,Hv", [([1 + (37 * i) % 131 for i in range(40)], 4, 8), ([0, 65, 1, 200, 0, 64, 640, 90], 12, 36)])
+def test_backward_more_chunks_than_sms(lengths, Hk, Hv):
+    """A thread block goes over several chunks of several sequences, full ones and others, with two or three heads each."""
+    x = with_grads(inputs(lengths, Hk, Hv, seed=91 + Hk))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    grads = kda.kda_gdn_prefill_backward(**x, device_status=status)
+    assert int(status.item()) == 0
+    check(x, grads)
