@@ -89,6 +89,8 @@ def library_path() -> str:
 def load_library(path: str | None = None):
     """Open libkda.so and declare the C signatures.  Raises if it is not built."""
     global _lib
+    if path is None and _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -96,6 +98,9 @@ def load_library(path: str | None = None):
         if not os.path.exists(p):
             raise RuntimeError(f"libkda.so is not built ({p}); run __graft_entry__.build() first")
         lib = ctypes.CDLL(p)
+        # The same library called with the interpreter lock held: a call only checks and launches, 3 us, and giving
+        # the lock up and taking it back costs a call that also makes tensors 1.8 us of 8.4.
+        lib.held = held = ctypes.PyDLL(p)
         P, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         lib.kda_abi_version.argtypes = []
         lib.kda_abi_version.restype = i32
@@ -149,7 +154,8 @@ def load_library(path: str | None = None):
                 ("kda_rms_norm", E, [P, P, E, P, F, i64, i32, E, i32, P, P, P, P]),
                 ("kda_rms_norm_backward_workspace_bytes", sz, [i64, i32]),
                 ("kda_rms_norm_backward", E, [P, P, P, E, P, F, i64, i32, P, P, P, sz, P])):
-            getattr(lib, name).restype, getattr(lib, name).argtypes = res, args
+            for functions in (lib, held):
+                getattr(functions, name).restype, getattr(functions, name).argtypes = res, args
         if path is None:
             _lib = lib
         return lib

@@ -5,18 +5,17 @@ handed to libkda.so, on the current stream of the tensors' own device or on ``st
 """
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from . import _binding as _b
 
 _NORM_OUT = {None: (_b.KDA_NORM_OUT_SAME, None), "e4m3": (_b.KDA_NORM_OUT_E4M3, torch.float8_e4m3fn),
              "int8": (_b.KDA_NORM_OUT_INT8, torch.int8)}
-_same_device = contextlib.nullcontext()
 # the current stream's handle without the Stream object that torch.cuda.current_stream makes of it (2 us)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+# the current device without torch.cuda.current_device's look whether CUDA is up: a call's tensors are there
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _check(t, name, dtype, shape, dev):
@@ -51,13 +50,24 @@ def _first(t, name, dims):
     return t.device, _b._dtype_code(t.dtype)
 
 
+def _contiguous(t, name):
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
 def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _on(dev):
-    """The call's device made current: launches go to it whatever device the caller has current."""
-    return _same_device if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+def _call(function, dev, *args):
+    """The call with its tensors' device current: launches go to it whatever device the caller has current."""
+    if _current_device() == dev.index:
+        st = function(*args)
+    else:
+        with torch.cuda.device(dev):
+            st = function(*args)
+    if st != _b.KDA_OK:
+        raise _b.KdaError(function.__name__, st, _b.kda_status_string(st))
 
 
 def _stream(stream, dev, *mine):
@@ -72,11 +82,6 @@ def _stream(stream, dev, *mine):
     return stream.cuda_stream
 
 
-def _done(name, st):
-    if st != _b.KDA_OK:
-        raise _b.KdaError(name, st, _b.kda_status_string(st))
-
-
 def _heads(q, v, name):
     """Hk, Hv, dk, dv of q [.., Hk, dk] and v [.., Hv, dv]."""
     if not isinstance(v, torch.Tensor) or v.dim() != q.dim():
@@ -87,8 +92,8 @@ def _heads(q, v, name):
 def kda_gdn_prefill_workspace_bytes(qkv_dtype, num_seqs: int, total_tokens: int, Hk: int, Hv: int, dk: int = 128,
                                     dv: int = 128) -> int:
     code = qkv_dtype if isinstance(qkv_dtype, int) else _b._dtype_code(qkv_dtype)
-    return int(_b.load_library().kda_gdn_prefill_workspace_bytes(code, int(num_seqs), int(total_tokens), int(Hk),
-                                                                 int(Hv), int(dk), int(dv)))
+    return int(_b.load_library().held.kda_gdn_prefill_workspace_bytes(
+        code, int(num_seqs), int(total_tokens), int(Hk), int(Hv), int(dk), int(dv)))
 
 
 def kda_gdn_prefill(q, k, v, log_decay, beta, cu_seqlens, S0=None, *, o=None, S_final=None, return_final=True,
@@ -99,11 +104,11 @@ def kda_gdn_prefill(q, k, v, log_decay, beta, cu_seqlens, S0=None, *, o=None, S_
     cu_seqlens: int32 [N+1] on the device; S0: fp32 [N, Hv, 128, 128] or None.  Returns (o, S_final) --
     S_final is None when return_final is False and none was given.
     """
-    lib = _b.load_library()
+    lib = _b.load_library().held
     dev, code = _first(q, "q", 3)
     T = q.shape[0]
     Hk, Hv, dk, dv = _heads(q, v, "[T, Hv, 128]")
-    _check(q, "q", q.dtype, (T, Hk, dk), dev)
+    _contiguous(q, "q")
     _check(k, "k", q.dtype, (T, Hk, dk), dev)
     _check(v, "v", q.dtype, (T, Hv, dv), dev)
     _check(log_decay, "log_decay", torch.float32, (T, Hv), dev)
@@ -116,7 +121,7 @@ def kda_gdn_prefill(q, k, v, log_decay, beta, cu_seqlens, S0=None, *, o=None, S_
         _check(S0, "S0", torch.float32, (N, Hv, dk, dv), dev)
     mine = []
     if o is None:
-        mine.append(o := torch.empty((T, Hv, dv), dtype=q.dtype, device=dev))
+        mine.append(o := torch.empty_like(v))
     else:
         _check(o, "o", q.dtype, (T, Hv, dv), dev)
     if S_final is not None:
@@ -129,19 +134,18 @@ def kda_gdn_prefill(q, k, v, log_decay, beta, cu_seqlens, S0=None, *, o=None, S_
     else:
         _b._check(workspace, "workspace", torch.uint8, dev)
     _b._check(device_status, "device_status", torch.int32, dev)
-    with _on(dev):
-        _done("kda_gdn_prefill", lib.kda_gdn_prefill(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), code, log_decay.data_ptr(), beta.data_ptr(), _p(S0),
-            cu_seqlens.data_ptr(), N, T, Hk, Hv, dk, dv, o.data_ptr(), _p(S_final), workspace.data_ptr(),
-            workspace.numel(), _p(device_status), _stream(stream, dev, *mine)))
+    _call(lib.kda_gdn_prefill, dev,
+          q.data_ptr(), k.data_ptr(), v.data_ptr(), code, log_decay.data_ptr(), beta.data_ptr(), _p(S0),
+          cu_seqlens.data_ptr(), N, T, Hk, Hv, dk, dv, o.data_ptr(), _p(S_final), workspace.data_ptr(),
+          workspace.numel(), _p(device_status), _stream(stream, dev, *mine))
     return o, S_final
 
 
 def kda_gdn_prefill_backward_workspace_bytes(qkv_dtype, num_seqs: int, total_tokens: int, Hk: int, Hv: int,
                                              dk: int = 128, dv: int = 128) -> int:
     code = qkv_dtype if isinstance(qkv_dtype, int) else _b._dtype_code(qkv_dtype)
-    return int(_b.load_library().kda_gdn_prefill_backward_workspace_bytes(code, int(num_seqs), int(total_tokens),
-                                                                          int(Hk), int(Hv), int(dk), int(dv)))
+    return int(_b.load_library().held.kda_gdn_prefill_backward_workspace_bytes(
+        code, int(num_seqs), int(total_tokens), int(Hk), int(Hv), int(dk), int(dv)))
 
 
 def kda_gdn_prefill_backward(q, k, v, log_decay, beta, cu_seqlens, grad_o, S0=None, grad_S_final=None, *,
@@ -152,12 +156,12 @@ def kda_gdn_prefill_backward(q, k, v, log_decay, beta, cu_seqlens, grad_o, S0=No
     Returns (grad_q, grad_k, grad_v, grad_log_decay, grad_beta, grad_S0): the first three in the dtype of q,
     the others fp32; grad_S0 is None when need_grad_S0 is False.  `grads` may pass those six tensors in.
     """
-    lib = _b.load_library()
+    lib = _b.load_library().held
     dev, code = _first(q, "q", 3)
     T = q.shape[0]
     Hk, Hv, dk, dv = _heads(q, v, "[T, Hv, 128]")
     f32 = torch.float32
-    _check(q, "q", q.dtype, (T, Hk, dk), dev)
+    _contiguous(q, "q")
     _check(k, "k", q.dtype, (T, Hk, dk), dev)
     _check(v, "v", q.dtype, (T, Hv, dv), dev)
     _check(grad_o, "grad_o", q.dtype, (T, Hv, dv), dev)
@@ -175,8 +179,8 @@ def kda_gdn_prefill_backward(q, k, v, log_decay, beta, cu_seqlens, grad_o, S0=No
              ("grad_log_decay", f32, (T, Hv)), ("grad_beta", f32, (T, Hv)), ("grad_S0", f32, state))
     mine = []
     if grads is None:
-        grads = tuple(torch.empty(shape, dtype=dt, device=dev) if n != "grad_S0" or need_grad_S0 else None
-                      for n, dt, shape in specs)
+        grads = tuple(torch.empty_like(t) for t in (q, k, v, log_decay, beta)) + (
+            torch.empty(state, dtype=f32, device=dev) if need_grad_S0 else None,)
         mine.extend(grads)
     elif len(grads) != 6:
         raise ValueError("grads must hold 6 tensors")
@@ -190,12 +194,11 @@ def kda_gdn_prefill_backward(q, k, v, log_decay, beta, cu_seqlens, grad_o, S0=No
     else:
         _b._check(workspace, "workspace", torch.uint8, dev)
     _b._check(device_status, "device_status", torch.int32, dev)
-    with _on(dev):
-        _done("kda_gdn_prefill_backward", lib.kda_gdn_prefill_backward(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), code, log_decay.data_ptr(), beta.data_ptr(), _p(S0),
-            cu_seqlens.data_ptr(), N, T, Hk, Hv, dk, dv, grad_o.data_ptr(), _p(grad_S_final),
-            *(_p(x) for x in grads), workspace.data_ptr(), workspace.numel(), _p(device_status),
-            _stream(stream, dev, *mine)))
+    _call(lib.kda_gdn_prefill_backward, dev,
+          q.data_ptr(), k.data_ptr(), v.data_ptr(), code, log_decay.data_ptr(), beta.data_ptr(), _p(S0),
+          cu_seqlens.data_ptr(), N, T, Hk, Hv, dk, dv, grad_o.data_ptr(), _p(grad_S_final),
+          *(_p(x) for x in grads), workspace.data_ptr(), workspace.numel(), _p(device_status),
+          _stream(stream, dev, *mine))
     return tuple(grads)
 
 
@@ -206,11 +209,11 @@ def kda_gdn_decode_step(q, k, v, log_decay, beta, S, state_indices=None, *, o=No
     q, k: [N, Hk, 128]; v: [N, Hv, 128] (bf16 or fp32); log_decay, beta: [N, Hv] fp32; state_indices:
     int32 [N] or None (slot n for sequence n).  Returns o [N, Hv, 128].
     """
-    lib = _b.load_library()
+    lib = _b.load_library().held
     dev, code = _first(q, "q", 3)
     N = q.shape[0]
     Hk, Hv, dk, dv = _heads(q, v, "[N, Hv, 128]")
-    _check(q, "q", q.dtype, (N, Hk, dk), dev)
+    _contiguous(q, "q")
     _check(k, "k", q.dtype, (N, Hk, dk), dev)
     _check(v, "v", q.dtype, (N, Hv, dv), dev)
     _check(log_decay, "log_decay", torch.float32, (N, Hv), dev)
@@ -221,15 +224,14 @@ def kda_gdn_decode_step(q, k, v, log_decay, beta, S, state_indices=None, *, o=No
         _check(state_indices, "state_indices", torch.int32, (N,), dev)
     mine = []
     if o is None:
-        mine.append(o := torch.empty((N, Hv, dv), dtype=q.dtype, device=dev))
+        mine.append(o := torch.empty_like(v))
     else:
         _check(o, "o", q.dtype, (N, Hv, dv), dev)
     _b._check(device_status, "device_status", torch.int32, dev)
-    with _on(dev):
-        _done("kda_gdn_decode_step", lib.kda_gdn_decode_step(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), code, log_decay.data_ptr(), beta.data_ptr(), S.data_ptr(),
-            slots, _p(state_indices), N, Hk, Hv, dk, dv, o.data_ptr(), _p(device_status),
-            _stream(stream, dev, *mine)))
+    _call(lib.kda_gdn_decode_step, dev,
+          q.data_ptr(), k.data_ptr(), v.data_ptr(), code, log_decay.data_ptr(), beta.data_ptr(), S.data_ptr(),
+          slots, _p(state_indices), N, Hk, Hv, dk, dv, o.data_ptr(), _p(device_status),
+          _stream(stream, dev, *mine))
     return o
 
 
@@ -242,10 +244,10 @@ def kda_rms_norm(x, weight=None, residual=None, *, eps=1e-6, quant=None, group=0
     (group=128).  Returns (y, scales, residual_out): scales [rows, scales in a row] is None without quant,
     residual_out (h in the type of x) None without a residual.
     """
-    lib = _b.load_library()
+    lib = _b.load_library().held
     dev, code = _first(x, "x", 2)
     rows, dim = x.shape
-    _check(x, "x", x.dtype, (rows, dim), dev)
+    _contiguous(x, "x")
     if weight is not None:
         _check(weight, "weight", torch.float32, (dim,), dev)
     if quant not in _NORM_OUT:
@@ -261,7 +263,7 @@ def kda_rms_norm(x, weight=None, residual=None, *, eps=1e-6, quant=None, group=0
     if residual_out is not None:
         _check(residual_out, "residual_out", x.dtype, (rows, dim), dev)
     if y is None:
-        mine.append(y := torch.empty((rows, dim), dtype=out_dtype or x.dtype, device=dev))
+        mine.append(y := torch.empty_like(x, dtype=out_dtype))
     else:
         _check(y, "y", out_dtype or x.dtype, (rows, dim), dev)
     if quant:
@@ -272,15 +274,14 @@ def kda_rms_norm(x, weight=None, residual=None, *, eps=1e-6, quant=None, group=0
             _check(scales, "scales", torch.float32, shape, dev)
     elif scales is not None:
         raise ValueError("scales are written with an 8-bit output only")
-    with _on(dev):
-        _done("kda_rms_norm", lib.kda_rms_norm(
-            x.data_ptr(), _p(residual), code, _p(weight), eps, rows, dim, out_type, group, y.data_ptr(), _p(scales),
-            _p(residual_out), _stream(stream, dev, *mine)))
+    _call(lib.kda_rms_norm, dev,
+          x.data_ptr(), _p(residual), code, _p(weight), eps, rows, dim, out_type, group, y.data_ptr(), _p(scales),
+          _p(residual_out), _stream(stream, dev, *mine))
     return y, scales, residual_out
 
 
 def kda_rms_norm_backward_workspace_bytes(rows: int, dim: int) -> int:
-    return int(_b.load_library().kda_rms_norm_backward_workspace_bytes(int(rows), int(dim)))
+    return int(_b.load_library().held.kda_rms_norm_backward_workspace_bytes(int(rows), int(dim)))
 
 
 def kda_rms_norm_backward(grad_y, h, weight=None, *, grad_h=None, eps=1e-6, need_grad_weight=True, grad_x=None,
@@ -291,10 +292,10 @@ def kda_rms_norm_backward(grad_y, h, weight=None, *, grad_h=None, eps=1e-6, need
     weight: fp32 [dim] or None (ones).  Returns (grad_x, grad_weight): grad_x, in that type, is the
     gradient of x and of residual alike; grad_weight fp32 [dim], or None when not asked for.
     """
-    lib = _b.load_library()
+    lib = _b.load_library().held
     dev, code = _first(h, "h", 2)
     rows, dim = h.shape
-    _check(h, "h", h.dtype, (rows, dim), dev)
+    _contiguous(h, "h")
     _check(grad_y, "grad_y", h.dtype, (rows, dim), dev)
     if grad_h is not None:
         _check(grad_h, "grad_h", h.dtype, (rows, dim), dev)
@@ -314,9 +315,8 @@ def kda_rms_norm_backward(grad_y, h, weight=None, *, grad_h=None, eps=1e-6, need
     elif grad_weight is not None:
         need = lib.kda_rms_norm_backward_workspace_bytes(rows, dim)
         mine.append(workspace := torch.empty(max(need, 256), dtype=torch.uint8, device=dev))
-    with _on(dev):
-        _done("kda_rms_norm_backward", lib.kda_rms_norm_backward(
-            grad_y.data_ptr(), h.data_ptr(), _p(grad_h), code, _p(weight), eps, rows, dim, grad_x.data_ptr(),
-            _p(grad_weight), _p(workspace), 0 if workspace is None else workspace.numel(),
-            _stream(stream, dev, *mine)))
+    _call(lib.kda_rms_norm_backward, dev,
+          grad_y.data_ptr(), h.data_ptr(), _p(grad_h), code, _p(weight), eps, rows, dim, grad_x.data_ptr(),
+          _p(grad_weight), _p(workspace), 0 if workspace is None else workspace.numel(),
+          _stream(stream, dev, *mine))
     return grad_x, grad_weight
