@@ -17,6 +17,12 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 # the current device without torch.cuda.current_device's look whether CUDA is up: a call's tensors are there
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
+# PyTorch's allocator on the current device, (bytes, stream handle) -> address; torch.cuda.caching_allocator_alloc less
+# its device switch
+_allocate = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None) or (
+    lambda size, stream: torch.cuda.caching_allocator_alloc(size, stream=stream))
+_free = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None) or torch.cuda.caching_allocator_delete
+
 
 def _check(t, name, dtype, shape, dev):
     """t: a contiguous CUDA tensor of this type, shape and device."""
@@ -68,6 +74,25 @@ def _call(function, dev, *args):
             st = function(*args)
     if st != _b.KDA_OK:
         raise _b.KdaError(function.__name__, st, _b.kda_status_string(st))
+
+
+def _call_with_workspace(function, dev, workspace, need, args, rest):
+    """_call(args, workspace and its bytes, rest), with the caller's workspace, or one of `need` bytes for this call.
+
+    That one comes from PyTorch's allocator without a tensor around it (4 us), for the stream that the call
+    goes to, rest[-1], and is back with the allocator once the launches are queued on it.
+    """
+    if workspace is not None:
+        return _call(function, dev, *args, workspace.data_ptr(), workspace.numel(), *rest)
+    if _current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return _call_with_workspace(function, dev, None, need, args, rest)
+    need = max(need, 256)
+    memory = _allocate(need, rest[-1])
+    try:
+        _call(function, dev, *args, memory, need, *rest)
+    finally:
+        _free(memory)
 
 
 def _stream(stream, dev, *mine):
@@ -128,16 +153,17 @@ def kda_gdn_prefill(q, k, v, log_decay, beta, cu_seqlens, S0=None, *, o=None, S_
         _check(S_final, "S_final", torch.float32, (N, Hv, dk, dv), dev)
     elif return_final:
         mine.append(S_final := torch.empty((N, Hv, dk, dv), dtype=torch.float32, device=dev))
+    need = 0
     if workspace is None:
         need = lib.kda_gdn_prefill_workspace_bytes(code, N, T, Hk, Hv, dk, dv)
-        mine.append(workspace := torch.empty(max(need, 256), dtype=torch.uint8, device=dev))
     else:
         _b._check(workspace, "workspace", torch.uint8, dev)
     _b._check(device_status, "device_status", torch.int32, dev)
-    _call(lib.kda_gdn_prefill, dev,
-          q.data_ptr(), k.data_ptr(), v.data_ptr(), code, log_decay.data_ptr(), beta.data_ptr(), _p(S0),
-          cu_seqlens.data_ptr(), N, T, Hk, Hv, dk, dv, o.data_ptr(), _p(S_final), workspace.data_ptr(),
-          workspace.numel(), _p(device_status), _stream(stream, dev, *mine))
+    _call_with_workspace(
+        lib.kda_gdn_prefill, dev, workspace, need,
+        (q.data_ptr(), k.data_ptr(), v.data_ptr(), code, log_decay.data_ptr(), beta.data_ptr(), _p(S0),
+         cu_seqlens.data_ptr(), N, T, Hk, Hv, dk, dv, o.data_ptr(), _p(S_final)),
+        (_p(device_status), _stream(stream, dev, *mine)))
     return o, S_final
 
 
@@ -188,17 +214,17 @@ def kda_gdn_prefill_backward(q, k, v, log_decay, beta, cu_seqlens, grad_o, S0=No
         for x, (n, dt, shape) in zip(grads, specs):
             if x is not None or n != "grad_S0":
                 _check(x, n, dt, shape, dev)
+    need = 0
     if workspace is None:
         need = lib.kda_gdn_prefill_backward_workspace_bytes(code, N, T, Hk, Hv, dk, dv)
-        mine.append(workspace := torch.empty(max(need, 256), dtype=torch.uint8, device=dev))
     else:
         _b._check(workspace, "workspace", torch.uint8, dev)
     _b._check(device_status, "device_status", torch.int32, dev)
-    _call(lib.kda_gdn_prefill_backward, dev,
-          q.data_ptr(), k.data_ptr(), v.data_ptr(), code, log_decay.data_ptr(), beta.data_ptr(), _p(S0),
-          cu_seqlens.data_ptr(), N, T, Hk, Hv, dk, dv, grad_o.data_ptr(), _p(grad_S_final),
-          *(_p(x) for x in grads), workspace.data_ptr(), workspace.numel(), _p(device_status),
-          _stream(stream, dev, *mine))
+    _call_with_workspace(
+        lib.kda_gdn_prefill_backward, dev, workspace, need,
+        (q.data_ptr(), k.data_ptr(), v.data_ptr(), code, log_decay.data_ptr(), beta.data_ptr(), _p(S0),
+         cu_seqlens.data_ptr(), N, T, Hk, Hv, dk, dv, grad_o.data_ptr(), _p(grad_S_final), *(_p(x) for x in grads)),
+        (_p(device_status), _stream(stream, dev, *mine)))
     return tuple(grads)
 
 
@@ -310,13 +336,16 @@ def kda_rms_norm_backward(grad_y, h, weight=None, *, grad_h=None, eps=1e-6, need
         _check(grad_weight, "grad_weight", torch.float32, (dim,), dev)
     elif need_grad_weight:
         mine.append(grad_weight := torch.empty((dim,), dtype=torch.float32, device=dev))
+    need = 0
     if workspace is not None:
         _b._check(workspace, "workspace", torch.uint8, dev)
     elif grad_weight is not None:
         need = lib.kda_rms_norm_backward_workspace_bytes(rows, dim)
-        mine.append(workspace := torch.empty(max(need, 256), dtype=torch.uint8, device=dev))
-    _call(lib.kda_rms_norm_backward, dev,
-          grad_y.data_ptr(), h.data_ptr(), _p(grad_h), code, _p(weight), eps, rows, dim, grad_x.data_ptr(),
-          _p(grad_weight), _p(workspace), 0 if workspace is None else workspace.numel(),
-          _stream(stream, dev, *mine))
+    args = (grad_y.data_ptr(), h.data_ptr(), _p(grad_h), code, _p(weight), eps, rows, dim, grad_x.data_ptr(),
+            _p(grad_weight))
+    handle = _stream(stream, dev, *mine)
+    if grad_weight is None and workspace is None:
+        _call(lib.kda_rms_norm_backward, dev, *args, None, 0, handle)
+    else:
+        _call_with_workspace(lib.kda_rms_norm_backward, dev, workspace, need, args, (handle,))
     return grad_x, grad_weight
