@@ -828,7 +828,13 @@ __global__ void __launch_bounds__(kRestThreads, 1)
             }
         }
         fence_async_smem();  // M, E, the parts and the cleared rows, before the next copies
-        __syncthreads();
+        if (__syncthreads_or(!ok)) {  // a bounded wait expired: no copy is left in flight
+            if (more) {
+                (void)mbar_wait(&bars[1], par ^ 1, kDrainLimit);
+                (void)mbar_wait(&bars[3], par ^ 1, kDrainLimit);
+            }
+            break;
+        }
         if (last) {
             if (tid == 0 && more) issue_kq(next_unit, next_tok0);
 #pragma unroll

@@ -69,7 +69,7 @@ __device__ __forceinline__ void pipe_copies(const WalkPipe& p, int steps, F issu
     int i = 0;
     for (; i < steps && !*p.abort_s; ++i) {
         const int s = i % ST;
-        if (i >= ST && !mbar_wait_pipe(&p.empty[s], ((i / ST) - 1) & 1)) {
+        if (i >= ST && !mbar_wait_or_stop(&p.empty[s], ((i / ST) - 1) & 1)) {
             *p.abort_s = 1;
             break;
         }

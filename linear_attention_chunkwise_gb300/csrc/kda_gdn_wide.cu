@@ -18,7 +18,8 @@
 // the longest of 6825, x 32 heads (prep included): 515 us, and 632 with two CTAs of 64 columns on mma.sync.  With the left
 // operands in shared memory it was 610 (its bandwidth is what bounds then), with sixteen epilogue warps 533, with V read
 // after the first product instead of during it 529.
-// Every on-chip wait is bounded; when one expires KDA_DEV_TIMEOUT is set and the CTA winds down.
+// Every on-chip wait is bounded; when one expires KDA_DEV_TIMEOUT is set and the CTA winds down: the copying thread
+// waits for its copies, the issuing one for its products, and then the CTA gives TMEM back.
 #include "kda_gdn_walk.cuh"
 
 namespace kda {
@@ -102,7 +103,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
             // Chunk c's state products come after the outputs of chunk c - 1, the last that read its stage.  Two
             // barriers in turn: neither can pass this thread by.
             for (int c = 0; n < nch; ++c) {
-                if (*abort_s || !mbar_wait_pipe(&bars[L::B_FREE + (c & 1)], (c >> 1) & 1)) {
+                if (*abort_s || !mbar_wait_or_stop(&bars[L::B_FREE + (c & 1)], (c >> 1) & 1)) {
                     *abort_s = 1;
                     break;
                 }
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
         if (lane == 0) {
             constexpr uint32_t id = idesc_bf16_f32(128, 64, false, false), id_k = idesc_bf16_f32(128, 64, false, true);
             auto past = [&](int bar, uint32_t parity) {
-                if (mbar_wait_pipe(&bars[bar], parity)) {
+                if (mbar_wait_or_stop(&bars[bar], parity)) {
                     tc_fence_after();
                     return true;
                 }
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < NC; ++i) S[i] = p.S0 ? p.S0[state + static_cast<size_t>(i) * D] : 0.f;
         auto past = [&](int bar, uint32_t parity) {  // the whole warp
-            const bool ok = mbar_wait_pipe(&bars[bar], parity);
+            const bool ok = mbar_wait_or_stop(&bars[bar], parity);
             if (__all_sync(0xffffffffu, ok)) return true;
             *abort_s = 1;
             return false;

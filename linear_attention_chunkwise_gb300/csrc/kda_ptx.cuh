@@ -93,6 +93,12 @@ __device__ __forceinline__ bool mbar_wait_pipe(uint64_t* bar, uint32_t parity) {
     (void)mbar_wait(bar, parity, kDrainLimit);
     return false;
 }
+// The same without the second wait, for a caller whose end of its own work is all that follows an expired wait while
+// another thread waits for the operation.
+__device__ __forceinline__ bool mbar_wait_or_stop(uint64_t* bar, uint32_t parity) {
+    if constexpr (kWaitLimit == 0) return mbar_test(bar, parity);
+    return mbar_wait(bar, parity, kWaitLimit);
+}
 // ------------------------------------------------------------------ TMA ----
 // 3-D tiled load global -> shared, completion counted on `bar` in bytes.
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t c0,
