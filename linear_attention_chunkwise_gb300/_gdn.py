@@ -114,6 +114,15 @@ def _heads(q, v, name):
     return q.shape[-2], v.shape[-2], q.shape[-1], v.shape[-1]
 
 
+def _sequences(cu_seqlens, dev):
+    """Their number."""
+    N = cu_seqlens.numel() - 1 if isinstance(cu_seqlens, torch.Tensor) else 0
+    if N < 0:
+        raise ValueError("cu_seqlens must have at least one entry")
+    _check(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev)
+    return N
+
+
 def kda_gdn_prefill_workspace_bytes(qkv_dtype, num_seqs: int, total_tokens: int, Hk: int, Hv: int, dk: int = 128,
                                     dv: int = 128) -> int:
     code = qkv_dtype if isinstance(qkv_dtype, int) else _b._dtype_code(qkv_dtype)
@@ -138,10 +147,7 @@ def kda_gdn_prefill(q, k, v, log_decay, beta, cu_seqlens, S0=None, *, o=None, S_
     _check(v, "v", q.dtype, (T, Hv, dv), dev)
     _check(log_decay, "log_decay", torch.float32, (T, Hv), dev)
     _check(beta, "beta", torch.float32, (T, Hv), dev)
-    N = cu_seqlens.numel() - 1
-    if N < 0:
-        raise ValueError("cu_seqlens must have at least one entry")
-    _check(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev)
+    N = _sequences(cu_seqlens, dev)
     if S0 is not None:
         _check(S0, "S0", torch.float32, (N, Hv, dk, dv), dev)
     mine = []
@@ -193,10 +199,7 @@ def kda_gdn_prefill_backward(q, k, v, log_decay, beta, cu_seqlens, grad_o, S0=No
     _check(grad_o, "grad_o", q.dtype, (T, Hv, dv), dev)
     _check(log_decay, "log_decay", f32, (T, Hv), dev)
     _check(beta, "beta", f32, (T, Hv), dev)
-    N = cu_seqlens.numel() - 1
-    if N < 0:
-        raise ValueError("cu_seqlens must have at least one entry")
-    _check(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev)
+    N = _sequences(cu_seqlens, dev)
     state = (N, Hv, dk, dv)
     for x, name in ((S0, "S0"), (grad_S_final, "grad_S_final")):
         if x is not None:
@@ -244,7 +247,7 @@ def kda_gdn_decode_step(q, k, v, log_decay, beta, S, state_indices=None, *, o=No
     _check(v, "v", q.dtype, (N, Hv, dv), dev)
     _check(log_decay, "log_decay", torch.float32, (N, Hv), dev)
     _check(beta, "beta", torch.float32, (N, Hv), dev)
-    slots = S.shape[0]
+    slots = S.shape[0] if isinstance(S, torch.Tensor) and S.dim() else 0
     _check(S, "S", torch.float32, (slots, Hv, dk, dv), dev)
     if state_indices is not None:
         _check(state_indices, "state_indices", torch.int32, (N,), dev)

@@ -145,3 +145,41 @@ def test_binding_refuses_tensors_off_the_gpu():
         kda.kda_rms_norm_backward(x[0], x[0])
     with pytest.raises(TypeError):
         kda.kda_rms_norm(None)
+
+
+def _backward(lib, **over):  # T = 128 tokens of 2 q/k and 4 value heads, every buffer a megabyte apart
+    names = ("q", "k", "v", "ld", "beta", "cu", "do", "dq", "dk", "dv", "dld", "db", "ws")
+    a = dict({n: BASE + i * MB for i, n in enumerate(names)}, dtype=0, S0=None, N=1, T=128, Hk=2, Hv=4, kd=128, vd=128,
+             dS=None, dS0=None, wsb=1 << 30, status=None)
+    a.update(over)
+    return lib.kda_gdn_prefill_backward(
+        P(a["q"]), P(a["k"]), P(a["v"]), a["dtype"], P(a["ld"]), P(a["beta"]), P(a["S0"]), P(a["cu"]), a["N"], a["T"], a["Hk"],
+        a["Hv"], a["kd"], a["vd"], P(a["do"]), P(a["dS"]), P(a["dq"]), P(a["dk"]), P(a["dv"]), P(a["dld"]), P(a["db"]),
+        P(a["dS0"]), P(a["ws"]), a["wsb"], P(a["status"]), None)
+
+
+FAR = BASE + 40 * MB
+
+
+@pytest.mark.parametrize("over,expect", [
+    (dict(dtype=1), UNS), (dict(dtype=2), UNS), (dict(kd=64), UNS), (dict(vd=64), UNS), (dict(Hv=3), INV), (dict(Hk=0), INV),
+    (dict(Hv=0), INV), (dict(N=-1), INV), (dict(T=-1), INV), (dict(T=2 ** 31), INV), (dict(N=0), INV), (dict(N=2 ** 30), INV),
+    *[({n: None}, INV) for n in ("q", "k", "v", "ld", "beta", "cu", "do", "dq", "dk", "dv", "dld", "db", "ws")],
+    *[({n: FAR + 8}, INV) for n in ("q", "k", "v", "do", "dq", "dk", "dv", "S0", "dS", "dS0", "ws")],
+    *[({n: FAR + 2}, INV) for n in ("ld", "beta", "dld", "db", "cu", "status")],
+    (dict(wsb=0), WS), (dict(wsb=2 * 4 * 200000), WS),
+    (dict(dq=BASE), INV), (dict(dk=BASE + MB + 16), INV), (dict(dv=BASE + 2 * MB), INV), (dict(dld=BASE + 3 * MB), INV),
+    (dict(db=BASE + 10 * MB), INV), (dict(dS=FAR, dS0=FAR), INV), (dict(S0=FAR, dS0=FAR + 4096), INV),
+    (dict(dv=BASE + 6 * MB), INV), (dict(ws=BASE + 9 * MB + 256), INV), (dict(status=BASE + 7 * MB), INV),
+    (dict(status=BASE + 5 * MB + 4), INV),
+])
+def test_backward_refuses(lib, over, expect):
+    assert _backward(lib, **over) == expect
+
+
+def test_backward_workspace_queries(lib):
+    need = kda.kda_gdn_prefill_backward_workspace_bytes
+    assert need(torch.bfloat16, 1, 8192, 16, 32) > need(torch.bfloat16, 1, 4096, 16, 32) > 0
+    for bad in ((torch.float32, 1, 64, 2, 2), (torch.bfloat16, -1, 64, 2, 2), (torch.bfloat16, 1, 64, 2, 3),
+                (torch.bfloat16, 1, -1, 2, 2), (torch.bfloat16, 1, 64, 2, 2, 64, 128)):
+        assert need(*bad) == 0

@@ -294,3 +294,45 @@ def test_prefill_many_pairs_on_two_streams():
     torch.cuda.synchronize()
     for ga, gb in got:
         assert torch.equal(ga[0], ra[0]) and torch.equal(ga[1], ra[1]) and torch.equal(gb[0], rb[0]) and torch.equal(gb[1], rb[1])
+
+
+# ---------------------------------------------------------------- refusals ----
+def wrong(t):
+    """What a tensor argument must not be: another type, shape, place or layout, or no tensor."""
+    spread = torch.empty(tuple(t.shape) + (2,), dtype=t.dtype, device="cuda")[..., 0]
+    return [(t.to(torch.float64), TypeError), (t[..., :-1].contiguous(), ValueError), (t.cpu(), ValueError),
+            (spread, ValueError), (t.tolist(), TypeError)]
+
+
+def test_prefill_refuses_tensors():
+    x = inputs([40, 24], 2, 4, seed=71)
+    for name in x:
+        for bad, error in wrong(x[name]):
+            if name == "q" and error is ValueError and bad.is_cuda and bad.is_contiguous():
+                continue  # a q of another shape: the others are the wrong ones then
+            if name == "cu_seqlens" and error is ValueError and bad.is_cuda and bad.is_contiguous():
+                continue  # one sequence fewer: S0 is the wrong one
+            with pytest.raises((error, ValueError) if name in ("v", "q") else error):
+                kda.kda_gdn_prefill(**dict(x, **{name: bad}))
+    for name, like in (("o", x["v"]), ("S_final", x["S0"])):
+        for bad, error in wrong(like):
+            with pytest.raises(error):
+                kda.kda_gdn_prefill(**x, **{name: bad})
+    with pytest.raises(kda.KdaError):
+        kda.kda_gdn_prefill(**x, workspace=torch.empty(100, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(kda.KdaError):
+        kda.kda_gdn_prefill(**x, o=x["v"])
+
+
+def test_decode_refuses_tensors():
+    x = inputs([1] * 3, 2, 4, seed=72)
+    args = dict({n: x[n] for n in ("q", "k", "v", "log_decay", "beta")}, S=x["S0"],
+                state_indices=torch.tensor([2, 0, 1], dtype=torch.int32, device="cuda"), o=torch.empty_like(x["v"]))
+    for name in args:
+        for bad, error in wrong(args[name]):
+            if name == "q" and error is ValueError and bad.is_cuda and bad.is_contiguous():
+                continue
+            with pytest.raises((error, ValueError) if name in ("v", "q") else error):
+                kda.kda_gdn_decode_step(**dict(args, **{name: bad}))
+    with pytest.raises(kda.KdaError):  # more sequences than slots
+        kda.kda_gdn_decode_step(**dict(args, S=x["S0"][:2], state_indices=None))

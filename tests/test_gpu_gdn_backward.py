@@ -18,7 +18,7 @@ import linear_attention_chunkwise_gb300 as kda
 import oracle
 from tests.conftest import cuda_ok
 from tests.gpu_util import host
-from tests.test_gpu_gdn import inputs
+from tests.test_gpu_gdn import inputs, wrong
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not cuda_ok(), reason="needs a CUDA GPU")]
 
@@ -190,3 +190,23 @@ def test_backward_more_chunks_than_sms(lengths, Hk, Hv):
     grads = kda.kda_gdn_prefill_backward(**x, device_status=status)
     assert int(status.item()) == 0
     check(x, grads)
+
+
+def test_backward_refuses_tensors():
+    x = with_grads(inputs([40, 24], 2, 4, seed=73))
+    for name in ("k", "v", "log_decay", "beta", "grad_o", "S0", "grad_S_final"):
+        for bad, error in wrong(x[name]):
+            with pytest.raises((error, ValueError) if name == "v" else error):
+                kda.kda_gdn_prefill_backward(**dict(x, **{name: bad}))
+    y = with_grads(inputs([40, 24], 2, 4, dtype=torch.float32, seed=73))
+    with pytest.raises(kda.KdaError):
+        kda.kda_gdn_prefill_backward(**y)
+    with pytest.raises(ValueError):
+        kda.kda_gdn_prefill_backward(**x, grads=(None,) * 5)
+    with pytest.raises(TypeError):
+        kda.kda_gdn_prefill_backward(**x, grads=(None,) * 6)
+    with pytest.raises(kda.KdaError):
+        kda.kda_gdn_prefill_backward(**x, workspace=torch.empty(4096, dtype=torch.uint8, device="cuda"))
+    like = [torch.empty_like(x[n]) for n in ("q", "k", "v", "log_decay", "beta", "S0")]
+    with pytest.raises(kda.KdaError):  # a gradient over an input
+        kda.kda_gdn_prefill_backward(**x, grads=(x["q"], *like[1:]))
