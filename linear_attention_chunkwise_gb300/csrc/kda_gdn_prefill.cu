@@ -425,6 +425,8 @@ cudaError_t launch_gdn_tables(const GdnArgs& a, const GdnWorkspace& w, cudaStrea
     return err;
 }
 
+namespace {
+
 // The prefill's scan: tcgen05, a CTA for the 128 columns of a (sequence, value head) pair, or mma.sync, four CTAs
 // of 32 columns.  A chunk takes the wide one 3.5 us, prep's larger images apart, the narrow one 1.54, so the narrow one is
 // ahead up to two of its CTAs an SM (8192 tokens: 64 pairs 270 us against 279, 96 pairs 274 against 214).
@@ -445,6 +447,8 @@ cudaError_t launch_prep(const GdnArgs& a, const GdnWorkspace& w, const CUtensorM
         tm_q, tm_k, a, w.table, w.images, w.chunks, hp, w.records != nullptr);
     return cudaGetLastError();
 }
+
+}  // namespace
 
 cudaError_t launch_gdn_prep(const GdnArgs& a, const GdnWorkspace& w, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                             cudaStream_t stream) {
