@@ -518,7 +518,7 @@ KDA_API kda_status kda_gdn_prefill(const void *q, const void *k, const void *v, 
  * repeatable.  The gradient of a log_decay at which the decay is 0 in fp32 is 0.
  *
  * Workspace: >= kda_gdn_prefill_backward_workspace_bytes(...) device bytes
- * (about 3.6 KB per token and value head), 256-byte aligned.  q, k, v, grad_o,
+ * (about 3.5 KB per token and value head), 256-byte aligned.  q, k, v, grad_o,
  * states and their gradients are 16-byte aligned, the others 4.  The outputs
  * overlap nothing (KDA_ERR_INVALID_ARG).  A malformed cu_seqlens sets
  * KDA_DEV_BAD_CU_SEQLENS and leaves the gradients unspecified.

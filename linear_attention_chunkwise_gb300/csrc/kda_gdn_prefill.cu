@@ -31,7 +31,8 @@ using namespace gdn;
 // inverse, T_ij = -D_i sum_{j <= k < i} A_ik T_kj, by mma.sync on two-term operands, its blocks staying in
 // its registers.  (The block products in fp32 on the CUDA cores and one value head a CTA, 256 threads:
 // 109 us for 8192 tokens x 32 heads, 16.1 K warp instructions a (chunk, head); a warp for every row of blocks
-// and the decays of one value head after the other: 70 us.)
+// and the decays of one value head after the other: 70 us; now 63.  The issue slots are 38% busy, HBM 34%: the
+// rest is the latency of a CTA's steps, five CTAs an SM.)
 constexpr int kPrepThreads = 128;
 constexpr int kPrepHeads = 4;  // most value heads of a CTA: a warp for each one's decays
 
@@ -361,7 +362,10 @@ __global__ void __launch_bounds__(kPrepThreads, 5)
 }
 
 // =============================================================== pass 2 ==
-// Four warps of 8 columns: the narrow scan (kda_gdn_wide.cu has the one for many pairs).
+// Four warps of 8 columns: the narrow scan (kda_gdn_wide.cu has the one for many pairs).  8192 tokens x 32 heads: 205 us,
+// 1.54 us a chunk, the chain of a warp's products; the tensor pipe is 52% busy.  One long sequence in pieces, prep of the
+// next one beside a piece's scan, gains nothing: 270 us with 64 chunks a piece, 277 with 42, 290 with 32, against 272
+// (the prep beside it slows the chain by what it saves).
 struct ScanCfg : ForwardCfg<1, 4, 3, false> {
     using L = ForwardCfg<1, 4, 3, false>;
     static constexpr int kThreads = 160;  // four walking warps and the one that copies
@@ -428,7 +432,7 @@ cudaError_t launch_gdn_tables(const GdnArgs& a, const GdnWorkspace& w, cudaStrea
 namespace {
 
 // The prefill's scan: tcgen05, a CTA for the 128 columns of a (sequence, value head) pair, or mma.sync, four CTAs
-// of 32 columns.  A chunk takes the wide one 3.5 us, prep's larger images apart, the narrow one 1.54, so the narrow one is
+// of 32 columns.  A chunk takes the wide one 3.2 us, prep's larger images apart, the narrow one 1.54, so the narrow one is
 // ahead up to two of its CTAs an SM (8192 tokens: 64 pairs 270 us against 279, 96 pairs 274 against 214).
 bool scan_wide(const GdnArgs& a) { return static_cast<int64_t>(a.num_seqs) * a.Hv * 2 > device_sm_count(); }
 
@@ -455,7 +459,8 @@ cudaError_t launch_gdn_prep(const GdnArgs& a, const GdnWorkspace& w, const CUten
     return !w.records && scan_wide(a) ? launch_prep<true>(a, w, tm_q, tm_k, stream) : launch_prep<false>(a, w, tm_q, tm_k, stream);
 }
 
-// 32 columns a CTA while that many CTAs find an SM each.
+// 32 columns a CTA while that many CTAs find an SM each.  (The gradient's walks of 32 columns, 32 pairs: 447 us for
+// 8192 tokens.)
 bool gdn_narrow(int32_t num_seqs, int32_t Hv) { return static_cast<int64_t>(num_seqs) * Hv * 4 <= device_sm_count(); }
 
 cudaError_t launch_gdn_scan(const GdnArgs& a, const GdnWorkspace& w, const CUtensorMap& tm_q, const CUtensorMap& tm_k,

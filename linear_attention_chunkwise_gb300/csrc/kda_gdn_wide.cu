@@ -13,11 +13,11 @@
 // halves of the channels are handed over by themselves, so that one half's products run beside the other
 // half's epilogue.  O of a chunk is formed while the next chunk's second product runs.  One thread issues the
 // products and another the copies.
-// A chunk is three products and three epilogues one after the other: 3.5 us, of which the products are 1.2; the
-// epilogues wait for one another's latencies more than for any unit.  Measured at 24571 tokens in eight sequences,
-// the longest of 6825, x 32 heads (prep included): 515 us, and 632 with two CTAs of 64 columns on mma.sync.  With the left
-// operands in shared memory it was 610 (its bandwidth is what bounds then), with sixteen epilogue warps 533, with V read
-// after the first product instead of during it 529.
+// A chunk is three products and three epilogues one after the other: 3.2 us, of which the tensor pipe is busy 28%
+// and the issue slots 40%; what bounds it is the chain of their latencies.  24571 tokens in eight sequences, the
+// longest of 6825, x 32 heads: 344 us, 505 with prep and the tables; with two CTAs of 64 columns on mma.sync 489 and
+// 632.  With the left operands in shared memory the call took 610 us (its bandwidth is what bounds then), with
+// sixteen epilogue warps 533, with V read after the first product instead of during it 529.
 // Every on-chip wait is bounded; when one expires KDA_DEV_TIMEOUT is set and the CTA winds down: the copying thread
 // waits for its copies, the issuing one for its products, and then the CTA gives TMEM back.
 #include "kda_gdn_walk.cuh"
