@@ -336,3 +336,31 @@ def test_decode_refuses_tensors():
                 kda.kda_gdn_decode_step(**dict(args, **{name: bad}))
     with pytest.raises(kda.KdaError):  # more sequences than slots
         kda.kda_gdn_decode_step(**dict(args, S=x["S0"][:2], state_indices=None))
+
+
+# ------------------------------------------------- the choice of the path ----
+@pytest.mark.parametrize("lengths", [[16], [17], [8] * 5, [8] * 4 + [9], [1] * 40 + [300], [1] * 63 + [441], [0] * 9 + [64, 3]])
+def test_prefill_around_the_choice_of_the_path(lengths):
+    x = inputs(lengths, 2, 4, seed=74 + len(lengths))
+    check(x, *kda.kda_gdn_prefill(**x))
+
+
+def test_prefill_many_pairs_under_a_graph():
+    x = with_same(inputs([300, 0, 65], 16, 32, seed=88))
+    o, S = kda.kda_gdn_prefill(**x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o2, S2 = kda.kda_gdn_prefill(**x)
+        o3, S3 = kda.kda_gdn_prefill(**dict(x, S0=S2))  # one after the other, in the workspace that the first gave back
+    o2.zero_()
+    S2.zero_()
+    for _ in range(3):
+        graph.replay()
+    assert torch.equal(o, o2) and torch.equal(S, S2)
+    o4, S4 = kda.kda_gdn_prefill(**dict(x, S0=S))
+    assert torch.equal(o4, o3) and torch.equal(S4, S3)
+
+
+def with_same(x):
+    return {n: t.clone() for n, t in x.items()}
