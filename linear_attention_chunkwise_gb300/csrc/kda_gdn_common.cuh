@@ -44,26 +44,6 @@ __device__ __forceinline__ uint32_t blk_pair(int g, int e, int n, int t) { retur
 constexpr uint32_t kRecS = 0, kRecX = 65536, kRecU = 131072, kRecW = 163840;
 constexpr size_t kRecStride = 196608;
 
-// Programmatic dependent launches: a kernel lets the next one's blocks start (on what the SMs have left) once
-// all its own have begun, and the next one waits for its end and its writes before it reads them.
-__device__ __forceinline__ void grid_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-template <typename K, typename... A>
-inline cudaError_t launch_dependent(K kernel, int64_t blocks, int threads, uint32_t smem, cudaStream_t stream,
-                                    const A&... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])

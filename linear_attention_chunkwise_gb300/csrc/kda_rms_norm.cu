@@ -462,6 +462,7 @@ template <typename T, int V, int NV, bool BLOCK>
 __global__ void __launch_bounds__(BLOCK ? kRowThreads : 32 * kWarpRows, BLOCK && NV > 1 ? 1 : 2)
     kda_rms_norm_backward_kernel(const NormBackwardArgs a) {
     constexpr int S = ahead(NV + 1, BLOCK);
+    grid_dependents();  // the weight's kernel
     __shared__ float2 s_sum[2][32];
     extern __shared__ __align__(16) uint8_t s_ring[];  // and, after the last row, the warps' shares of grad_w [dim]
     float* const s_w = reinterpret_cast<float*>(s_ring);
@@ -646,6 +647,7 @@ __global__ void __launch_bounds__(1024) kda_rms_norm_weight_kernel(const float* 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     float s = 0.f;
+    grid_wait();  // the shares
     if (c < dim) {
 #pragma unroll 8
         for (int64_t p = warp; p < parts; p += 32) s += partial[p * dim + c];
@@ -770,8 +772,8 @@ cudaError_t launch_rms_norm_backward(bool f32_io, const NormBackwardArgs& a, cud
         err = f32_io ? norm_backward_t<float>(a, blocks, stream) : norm_backward_t<__nv_bfloat16>(a, blocks, stream);
     }
     if (err != cudaSuccess || !a.grad_weight) return err;
-    kda_rms_norm_weight_kernel<<<(a.dim + 31) / 32, 1024, 0, stream>>>(a.partial, parts, a.dim, a.grad_weight);
-    return cudaGetLastError();
+    return launch_dependent(kda_rms_norm_weight_kernel, (a.dim + 31) / 32, 1024, 0, stream, a.partial, parts, a.dim,
+                            a.grad_weight);
 }
 
 }  // namespace kda
