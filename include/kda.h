@@ -569,7 +569,8 @@ KDA_API kda_status kda_gdn_decode_step(const void *q, const void *k, const void 
  *              columns (dim a multiple of 128)
  *   scales     [rows, group ? dim / group : 1] fp32 (out), 8-bit outputs only:
  *              max(max |y| / qmax, 2^-126), qmax = 448 (e4m3) or 127 (int8).
- *              The code is y / scale rounded to nearest even; it stands for
+ *              The code is y / scale rounded to nearest even (both quotients
+ *              as products with the reciprocal, in fp32); it stands for
  *              code * scale.  Values that are not finite make the scale they
  *              share NaN.
  *
