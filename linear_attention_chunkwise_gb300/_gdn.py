@@ -287,10 +287,10 @@ def kda_rms_norm(x, weight=None, residual=None, *, eps=1e-6, quant=None, group=0
     mine = []
     if residual is not None:
         _check(residual, "residual", x.dtype, (rows, dim), dev)
-        if residual_out is None:
-            mine.append(residual_out := torch.empty_like(x))
     if residual_out is not None:
         _check(residual_out, "residual_out", x.dtype, (rows, dim), dev)
+    elif residual is not None:
+        mine.append(residual_out := torch.empty_like(x))
     if y is None:
         mine.append(y := torch.empty_like(x, dtype=out_dtype))
     else:

@@ -17,7 +17,8 @@
 // and the issue slots 40%; what bounds it is the chain of their latencies.  24571 tokens in eight sequences, the
 // longest of 6825, x 32 heads: 344 us, 505 with prep and the tables; with two CTAs of 64 columns on mma.sync 489 and
 // 632.  With the left operands in shared memory the call took 610 us (its bandwidth is what bounds then), with
-// sixteen epilogue warps 533, with V read after the first product instead of during it 529.
+// sixteen epilogue warps 533, with V read after the first product instead of during it 529; with the outputs on four
+// warps of their own 552 (they are in the way all the time then, not while the second product runs).
 // Every on-chip wait is bounded; when one expires KDA_DEV_TIMEOUT is set and the CTA winds down: the copying thread
 // waits for its copies, the issuing one for its products, and then the CTA gives TMEM back.
 #include "kda_gdn_walk.cuh"
