@@ -33,7 +33,8 @@ using namespace gdn;
 // Four warps walk forward and four back, each group with tiles and a copying thread of its own: a warp of
 // either is a chain that leaves the SM's issue slots and tensor cores half idle, and the two do not wait for
 // each other.  8192 tokens x 16/32 heads: 447 us, 3.5 us a chunk, 0.8 GB of records written; the tensor pipe is 51%
-// busy, the back walk's chain is the longer one.  The copying warps' registers go to the walks': launched with 168 a thread, 3 x 168 = 216 + 248 + 40.
+// busy, the back walk's chain is the longer one.  The copying warps' registers go to the walks': launched with 168 a
+// thread, 3 x 168 = 216 + 248 + 40.
 template <int NT>
 struct BackCfg {
     static constexpr int ST = 2;
@@ -375,6 +376,7 @@ __global__ void __launch_bounds__(WalksCfg<NT>::kThreads, 1)
 // have been read (S goes where X was), U and W behind the 64 x 64 products, X once dO is in registers.
 // 8192 tokens x 16/32 heads: 377 us, 420 with a CTA for every unit, whose first copies nothing hides.  What bounds it
 // is mma.sync at two warps an SM quarter (255 registers a thread): the tensor pipe is busy 47% of the time.
+// SPLIT: the CTAs of a cluster take a value head each of one unit and add up dq and dk in one another's shared memory.
 // Warp (mr, nh): tokens 16 mr, channels 64 nh of dq and dk.
 // Of the 64 x 64 products the warps nh = 0 form dP and Q K^T, the others dA and K K^T; the two warps of an
 // SM quarter have row blocks mr and 3 - mr, so that the quarters' triangles are even.
@@ -397,10 +399,12 @@ static_assert(RestSmem::ALLOC <= 232448 && RestSmem::BARS % 8 == 0, "shared memo
 // <X, S> per warp [8]
 constexpr int kPtA = 0, kPtW = 128, kPtC = 256, kPtB = 768, kPtI = 832;
 
+template <bool SPLIT>
 __global__ void __launch_bounds__(kRestThreads, 1)
     kda_gdn_grad_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                        const __grid_constant__ CUtensorMap tm_do, const GdnArgs p, const GdnBackwardArgs gr, const int32_t* __restrict__ co, const uint8_t* __restrict__ images,
-                        int64_t chunk_slots, const uint8_t* __restrict__ records) {
+                        const __grid_constant__ CUtensorMap tm_do, const GdnArgs p, const GdnBackwardArgs gr,
+                        const int32_t* __restrict__ co, const uint8_t* __restrict__ images, int64_t chunk_slots,
+                        const uint8_t* __restrict__ records) {
     using L = RestSmem;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -422,7 +426,8 @@ __global__ void __launch_bounds__(kRestThreads, 1)
         return KDA_BOUNDS(seq >= 0 && seq < N && j < chunk_slots && t0 >= 0 && len >= 1 && t0 + len <= p.total_tokens,
                           p.device_status);
     };
-    int unit = blockIdx.x;
+    const int rank = SPLIT ? static_cast<int>(blockIdx.x) % group : 0;  // in the cluster: the value head it takes
+    int unit = SPLIT ? static_cast<int>(blockIdx.x) / group : static_cast<int>(blockIdx.x);
     if (!locate(unit, tok0, Lc)) return;
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BARS);
     float* const gs = reinterpret_cast<float*>(sm + L::G);
@@ -462,11 +467,11 @@ __global__ void __launch_bounds__(kRestThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < 4; ++i) mbar_init(&bars[i], 1);
         fence_mbar_init();
-        issue_s(unit, 0, tok0, L::SX, L::SX + L::kSX);
-        issue_uw(unit, 0);
+        issue_s(unit, rank, tok0, L::SX, L::SX + L::kSX);
+        issue_uw(unit, rank);
         issue_kq(unit, tok0);
     }
-    for (int e = tid; e < kVec; e += kRestThreads) gs[e] = image_vec(unit, 0)[e];
+    for (int e = tid; e < kVec; e += kRestThreads) gs[e] = image_vec(unit, rank)[e];
     __syncthreads();
     bool ok = true;
     const int g = lane >> 2, t = lane & 3;
@@ -484,10 +489,11 @@ __global__ void __launch_bounds__(kRestThreads, 1)
         for (int e = 0; e < 4; ++e) dq[n][e] = dk[n][e] = 0.f;
 
     uint32_t kq_par = 0;
-    for (int it = 0, hh = 0;; ++it) {  // value head hh of a unit
+    for (int it = 0, hh = rank;; ++it) {  // value head hh of a unit
         const uint32_t par = it & 1, s_at = L::SX + L::kSX * par, x_at = L::SX + L::kSX * (par ^ 1);
         float* const parts = reinterpret_cast<float*>(sm + s_at + L::P);
-        if (hh == 0 && Lc < C) {  // rows behind the sequence's end
+        const bool first = SPLIT || hh == 0;  // of the unit
+        if (first && Lc < C) {  // rows behind the sequence's end
             ok = mbar_wait_pipe(&bars[0], kq_par) && ok;
             const uint4 z = make_uint4(0u, 0u, 0u, 0u);
             for (int e = tid; e < (C - Lc) * 16; e += kRestThreads) {
@@ -564,7 +570,7 @@ __global__ void __launch_bounds__(kRestThreads, 1)
                 }
             }
             float d1[2], d2[2];
-            if (hh == 0) ok = mbar_wait_pipe(&bars[0], kq_par) && ok;
+            if (first) ok = mbar_wait_pipe(&bars[0], kq_par) && ok;
             row_dots(a1, L::Q, d1);
             row_dots(a2, L::K, d2);
 #pragma unroll
@@ -614,8 +620,10 @@ __global__ void __launch_bounds__(kRestThreads, 1)
         }
         float inner = 0.f;  // <X, S>
         for (int e = tid; e < 2048; e += kRestThreads) {
-            const uint4 sh = *reinterpret_cast<const uint4*>(sm + s_at + 16 * e), sl = *reinterpret_cast<const uint4*>(sm + s_at + 32768 + 16 * e);
-            const uint4 xh = *reinterpret_cast<const uint4*>(sm + x_at + 16 * e), xl = *reinterpret_cast<const uint4*>(sm + x_at + 32768 + 16 * e);
+            const uint4 sh = *reinterpret_cast<const uint4*>(sm + s_at + 16 * e);
+            const uint4 sl = *reinterpret_cast<const uint4*>(sm + s_at + 32768 + 16 * e);
+            const uint4 xh = *reinterpret_cast<const uint4*>(sm + x_at + 16 * e);
+            const uint4 xl = *reinterpret_cast<const uint4*>(sm + x_at + 32768 + 16 * e);
             const uint32_t* a = &sh.x;
             const uint32_t* b = &sl.x;
             const uint32_t* c = &xh.x;
@@ -629,9 +637,9 @@ __global__ void __launch_bounds__(kRestThreads, 1)
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, off);
-        const bool last = hh + 1 == group;  // of the unit; the next item is another's first head then
+        const bool last = SPLIT || hh + 1 == group;  // of the unit; the next item is another's first head then
         const int next_unit = last ? unit + static_cast<int>(gridDim.x) : unit, next_hh = last ? 0 : hh + 1;
-        const bool more = !last || locate(next_unit, next_tok0, next_Lc);
+        const bool more = !SPLIT && (!last || locate(next_unit, next_tok0, next_Lc));
         __syncthreads();  // S and X have been read: M, E and the parts take S's place, the next S X's
         if (tid == 0 && more) issue_s(next_unit, next_hh, last ? next_tok0 : tok0, x_at, s_at);
         if (t == 0) {
@@ -829,42 +837,72 @@ __global__ void __launch_bounds__(kRestThreads, 1)
             }
         }
         fence_async_smem();  // M, E, the parts and the cleared rows, before the next copies
-        if (__syncthreads_or(!ok)) {  // a bounded wait expired: no copy is left in flight
+        if (__syncthreads_or(!ok) && !SPLIT) {  // a bounded wait expired: no copy is left in flight
             if (more) {
                 (void)mbar_wait(&bars[1], par ^ 1, kDrainLimit);
                 (void)mbar_wait(&bars[3], par ^ 1, kDrainLimit);
             }
             break;
         }
-        if (last) {
-            if (tid == 0 && more) issue_kq(next_unit, next_tok0);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int row = 16 * mr + g + 8 * e;
-                if (row >= Lc) continue;
-                const int64_t off = (static_cast<int64_t>(tok0 + row) * p.Hk + hk) * D + 64 * nh + 2 * t;
-#pragma unroll
-                for (int n = 0; n < 8; ++n) {
-                    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(gr.grad_q) + off + 8 * n) =
-                        pack_bf16(dq[n][2 * e], dq[n][2 * e + 1]);
-                    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(gr.grad_k) + off + 8 * n) =
-                        pack_bf16(dk[n][2 * e], dk[n][2 * e + 1]);
-                }
-            }
-            if (!more) break;
+        if constexpr (SPLIT) {  // the heads' sums, in order; each CTA of the cluster takes 64 / group of a thread's values
+            float* const mine = reinterpret_cast<float*>(sm + L::SX);  // [64][threads]
 #pragma unroll
             for (int n = 0; n < 8; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) dq[n][e] = dk[n][e] = 0.f;
-            unit = next_unit;
-            tok0 = next_tok0;
-            Lc = next_Lc;
-            kq_par ^= 1;
-        }
-        hh = next_hh;
+                for (int e = 0; e < 4; ++e) {
+                    mine[(4 * n + e) * kRestThreads + tid] = dq[n][e];
+                    mine[(32 + 4 * n + e) * kRestThreads + tid] = dk[n][e];
+                }
+            cluster_sync();
+            const uint32_t at = smem_u32(mine + tid);
+            for (int i = rank * (64 / group); i < (rank + 1) * (64 / group); i += 2) {
+                float x = 0.f, y = 0.f;
+                for (int k = 0; k < group; ++k) {
+                    const uint32_t there = cluster_address(at + i * kRestThreads * 4, k);
+                    x += cluster_load(there);
+                    y += cluster_load(there + kRestThreads * 4);
+                }
+                const int row = 16 * mr + g + 8 * ((i >> 1) & 1);
+                if (row < Lc) {
+                    const int64_t off =
+                        (static_cast<int64_t>(tok0 + row) * p.Hk + hk) * D + 64 * nh + 2 * t + 8 * ((i & 31) >> 2);
+                    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(i < 32 ? gr.grad_q : gr.grad_k) + off) =
+                        pack_bf16(x, y);
+                }
+            }
+            cluster_sync();  // the others have read this CTA's
+            break;
+        } else {
+            if (last) {
+                if (tid == 0 && more) issue_kq(next_unit, next_tok0);
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-            if (tid + kRestThreads * e < kVec) gs[tid + kRestThreads * e] = vec[e];
+                for (int e = 0; e < 2; ++e) {
+                    const int row = 16 * mr + g + 8 * e;
+                    if (row >= Lc) continue;
+                    const int64_t off = (static_cast<int64_t>(tok0 + row) * p.Hk + hk) * D + 64 * nh + 2 * t;
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) {
+                        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(gr.grad_q) + off + 8 * n) =
+                            pack_bf16(dq[n][2 * e], dq[n][2 * e + 1]);
+                        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(gr.grad_k) + off + 8 * n) =
+                            pack_bf16(dk[n][2 * e], dk[n][2 * e + 1]);
+                    }
+                }
+                if (!more) break;
+#pragma unroll
+                for (int n = 0; n < 8; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dq[n][e] = dk[n][e] = 0.f;
+                unit = next_unit;
+                tok0 = next_tok0;
+                Lc = next_Lc;
+                kq_par ^= 1;
+            }
+            hh = next_hh;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (tid + kRestThreads * e < kVec) gs[tid + kRestThreads * e] = vec[e];
+        }
     }
     if (!ok && p.device_status) atomicOr(p.device_status, KDA_DEV_TIMEOUT);
 }
@@ -898,10 +936,20 @@ cudaError_t launch_gdn_backward(const GdnArgs& a, const GdnBackwardArgs& b, cons
     if (!make_tensor_map(&tm_do, b.grad_o, a.Hv, a.total_tokens, 64, C, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
     static int configured[64];
-    if (err == cudaSuccess) err = set_smem(kda_gdn_grad_kernel, RestSmem::ALLOC, configured);
+    if (err == cudaSuccess) err = set_smem(kda_gdn_grad_kernel<false>, RestSmem::ALLOC, configured);
     if (err != cudaSuccess) return err;
+    // Where the value heads of all units find an SM each, a group's share a unit as a cluster (333 tokens in three
+    // sequences x 4/8 heads, the whole call: 58 us, one head after the other 64).
+    const int group = a.Hv / a.Hk;
+    if ((group == 2 || group == 4 || group == 8) && w.chunks * a.Hv <= device_sm_count()) {
+        static int configured_split[64];
+        err = set_smem(kda_gdn_grad_kernel<true>, RestSmem::ALLOC, configured_split);
+        if (err != cudaSuccess) return err;
+        return launch_dependent_clusters(group, kda_gdn_grad_kernel<true>, w.chunks * a.Hv, kRestThreads, RestSmem::ALLOC,
+                                         stream, tm_q, tm_k, tm_do, a, b, w.table, w.images, w.chunks, w.records);
+    }
     const int64_t blocks = std::min<int64_t>(w.chunks * a.Hk, device_sm_count());
-    return launch_dependent(kda_gdn_grad_kernel, blocks, kRestThreads, RestSmem::ALLOC, stream, tm_q, tm_k, tm_do, a,
+    return launch_dependent(kda_gdn_grad_kernel<false>, blocks, kRestThreads, RestSmem::ALLOC, stream, tm_q, tm_k, tm_do, a,
                             b, w.table, w.images, w.chunks, w.records);
 }
 

@@ -292,20 +292,46 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
 // all its own have begun, and the next one waits for its end and its writes before it reads them.
 __device__ __forceinline__ void grid_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Blocks in clusters of `cluster` (1: none).
 template <typename K, typename... A>
-inline cudaError_t launch_dependent(K kernel, int64_t blocks, int threads, uint32_t smem, cudaStream_t stream,
-                                    const A&... args) {
+inline cudaError_t launch_dependent_clusters(int cluster, K kernel, int64_t blocks, int threads, uint32_t smem,
+                                             cudaStream_t stream, const A&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks));
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+template <typename K, typename... A>
+inline cudaError_t launch_dependent(K kernel, int64_t blocks, int threads, uint32_t smem, cudaStream_t stream,
+                                    const A&... args) {
+    return launch_dependent_clusters(1, kernel, blocks, threads, smem, stream, args...);
+}
+
+// -------------------------------------------------------------- clusters ----
+// Every thread of every block of the cluster; writes before it are seen behind it.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The same shared-memory address in block `rank` of the cluster, and a load from one.
+__device__ __forceinline__ uint32_t cluster_address(uint32_t addr, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float cluster_load(uint32_t addr) {
+    float x;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+    return x;
 }
 
 }  // namespace kda

@@ -210,3 +210,15 @@ def test_backward_refuses_tensors():
     like = [torch.empty_like(x[n]) for n in ("q", "k", "v", "log_decay", "beta", "S0")]
     with pytest.raises(kda.KdaError):  # a gradient over an input
         kda.kda_gdn_prefill_backward(**x, grads=(x["q"], *like[1:]))
+
+
+@pytest.mark.parametrize("lengths,Hk,Hv", [([130, 0, 64], 1, 8), ([200], 2, 16), ([65, 3], 4, 16), ([90], 9, 18), ([64] * 9, 4, 8)])
+def test_backward_groups_on_few_sms(lengths, Hk, Hv):
+    """Groups of two, four and eight value heads with an SM for each, and (the last) without."""
+    x = with_grads(inputs(lengths, Hk, Hv, seed=92 + Hv))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    grads = kda.kda_gdn_prefill_backward(**x, device_status=status)
+    assert int(status.item()) == 0
+    check(x, grads)
+    again = kda.kda_gdn_prefill_backward(**x)
+    assert all(torch.equal(a, b) for a, b in zip(grads, again))

@@ -21,8 +21,8 @@ from tests.test_gpu_wait_limit import WAIT_DIR
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not cuda_ok(), reason="needs a CUDA GPU")]
 
-# few and many (sequence, value head) pairs; the second has more chunks than a pipeline has stages
-LAYOUTS = [([300, 77, 130], 1, 3), ([700, 0, 65], 16, 32), ([64] * 45, 2, 4)]
+# few and many (sequence, value head) pairs, more chunks than a pipeline has stages; the last in clusters
+LAYOUTS = [([300, 77, 130], 1, 3), ([700, 0, 65], 16, 32), ([64] * 45, 2, 4), ([130, 64], 2, 4)]
 
 
 @pytest.fixture(scope="module")
