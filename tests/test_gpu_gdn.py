@@ -364,3 +364,15 @@ def test_prefill_many_pairs_under_a_graph():
 
 def with_same(x):
     return {n: t.clone() for n, t in x.items()}
+
+
+def test_prefill_many_pairs_slow_decay_over_many_chunks():
+    x = inputs([2048], 40, 80, lo=-1e-4, seed=89)
+    check(x, *kda.kda_gdn_prefill(**x))
+
+
+def test_prefill_many_pairs_similar_keys():
+    x = inputs([320, 130], 20, 40, seed=90, lo=-0.02)
+    k = x["k"].float() + 0.5 / 128 ** 0.5 * 4
+    x["k"] = (k / k.norm(dim=-1, keepdim=True)).to(torch.bfloat16)
+    check(x, *kda.kda_gdn_prefill(**x))
