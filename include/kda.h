@@ -517,11 +517,13 @@ KDA_API kda_status kda_gdn_prefill(const void *q, const void *k, const void *v, 
  * qkv_dtype is KDA_DTYPE_BF16 (else KDA_ERR_UNSUPPORTED).  The call reruns the
  * chunkwise forward, keeping the state before every 64-token chunk, walks the
  * state's adjoint back over the chunks, and forms everything else per chunk.
+ * Up to two tokens a sequence and six more go token by token, in fp32.
  * The fp32 gradients are accurate as S_final is; results are bitwise
  * repeatable.  The gradient of a log_decay at which the decay is 0 in fp32 is 0.
  *
  * Workspace: >= kda_gdn_prefill_backward_workspace_bytes(...) device bytes
- * (about 3.5 KB per token and value head), 256-byte aligned.  q, k, v, grad_o,
+ * (about 3.5 KB per token and value head, 64 KB where it goes token by token),
+ * 256-byte aligned.  q, k, v, grad_o,
  * states and their gradients are 16-byte aligned, the others 4.  The outputs
  * overlap nothing (KDA_ERR_INVALID_ARG).  A malformed cu_seqlens sets
  * KDA_DEV_BAD_CU_SEQLENS and leaves the gradients unspecified.

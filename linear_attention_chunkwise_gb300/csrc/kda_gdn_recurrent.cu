@@ -1,5 +1,6 @@
 // kda_gdn_recurrent.cu -- the gated delta rule token by token, in fp32: the decode
-// step, and the prefill of short sequences and of fp32 inputs.
+// step, the prefill of short sequences and of fp32 inputs, and the gradient of a
+// few tokens.
 //
 // The gated delta rule is the recurrence of "Understanding Kimi Delta Attention"
 // (pyshine), "The KDA Recurrence: Scalar Gate vs Channel-wise Gate", with its
@@ -10,6 +11,7 @@
 // Value head h reads q/k head h / (Hv / Hk).
 #include <cuda_bf16.h>
 
+#include "kda_args.h"
 #include "kda_internal.h"
 #include "kda_ptx.cuh"
 
@@ -272,6 +274,201 @@ __global__ void __launch_bounds__(kRecThreads) kda_gdn_recurrent_kernel(const Gd
     }
 }
 
+// ============================================================== gradient ==
+// The gradient of short sequences, token by token in fp32: a CTA per (sequence, value head), and where groups share a
+// q/k head a kernel that adds them up.  A walk forward leaves the state before every token in the workspace, the
+// walk back takes them: with G the adjoint of the state after a token, S' = a S its decayed state, y = S'^T k, u = b (v - y), z = -b G^T k,
+//   G += q dO^T;  dq = S' dO + k (u . dO);  dv = b G^T k;  db = (G^T k) . (v - y);  dk = G u + S' z;
+//   G' = G + k z^T;  gradient of log_decay = <G', S'>;  the adjoint of the state before = a G'.
+// A few tokens leave few numbers to average an error over, and a sum that cancels among them shows every
+// rounding: with operands of two bf16 terms single gradients of log_decay and b were off by 1e-5 to 1e-4 of themselves.
+// Thread (warp w, lane l) holds rows 16 w .. and columns 4 l .. + 3 of S' and of G.  Bound by the chain of a token's
+// reductions, 3.5 us both ways.
+constexpr int kGradThreads = 256;
+constexpr int kGradRows = D / (kGradThreads / 32);  // rows of a warp: 16
+
+// x[0 .. 15] of 32 lanes: lane l gets the sum over the lanes of x[l / 2].
+__device__ __forceinline__ float sum_rows(float (&x)[kGradRows], int lane) {
+#pragma unroll
+    for (int n = 8, off = 16; n > 0; n >>= 1, off >>= 1) {
+        const bool up = lane & off;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float keep = up ? x[i + n] : x[i], give = up ? x[i] : x[i + n];
+            x[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+        }
+    }
+    return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 1);
+}
+// The sum over the block of x (every thread's), for every thread; `part` is one of a kind until the block's next barrier.
+__device__ __forceinline__ float block_sum(float x, float* part) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = 0.f;
+#pragma unroll
+    for (int w = 0; w < kGradThreads / 32; ++w) x += part[w];
+    return x;
+}
+
+__global__ void __launch_bounds__(kGradThreads, 1)
+    kda_gdn_recurrent_grad_kernel(const GdnArgs a, const GdnBackwardArgs gr, float* __restrict__ states,
+                                  float* __restrict__ sums) {
+    __shared__ __align__(16) float k_s[D], q_s[D], v_s[D], do_s[D], u_s[D], z_s[D];
+    __shared__ __align__(16) float red[2][kGradThreads / 32][D];
+    __shared__ float part[3][kGradThreads / 32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int n = blockIdx.x / a.Hv, h = blockIdx.x - n * a.Hv, group = a.Hv / a.Hk, hk = h / group;
+    grid_dependents();  // the groups' sums
+    const int64_t t_begin = a.cu_seqlens[n], t_end = a.cu_seqlens[n + 1];
+    const bool ends_ok = a.cu_seqlens[0] == 0 && a.cu_seqlens[a.num_seqs] == a.total_tokens;
+    const bool ok = t_begin >= 0 && t_end >= t_begin && t_end <= a.total_tokens;
+    if ((!ok || !ends_ok) && tid == 0 && a.device_status) atomicOr(a.device_status, KDA_DEV_BAD_CU_SEQLENS);
+    if (!ok) return;
+    const auto bf16 = [](const void* p) { return static_cast<const __nv_bfloat16*>(p); };
+    const int r0 = kGradRows * warp;
+    const size_t state = (static_cast<size_t>(n) * a.Hv + h) * D * D + static_cast<size_t>(r0) * D;
+    // this thread's places in the state before token t
+    auto saved = [&](int64_t t) {
+        return reinterpret_cast<float4*>(states + ((static_cast<size_t>(t) * a.Hv + h) * D + r0) * D) + lane;
+    };
+    float4 S[kGradRows], G[kGradRows];
+#pragma unroll
+    for (int i = 0; i < kGradRows; ++i)
+        S[i] = a.S0 ? reinterpret_cast<const float4*>(a.S0 + state + i * D)[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+    // a token's rows into shared memory; the barrier also ends the reads of the one before
+    auto stage = [&](int64_t t) {
+        __syncthreads();
+        const size_t qk = (static_cast<size_t>(t) * a.Hk + hk) * D, v = (static_cast<size_t>(t) * a.Hv + h) * D;
+        if (tid < D) {
+            k_s[tid] = to_f32(bf16(a.k)[qk + tid]);
+            q_s[tid] = to_f32(bf16(a.q)[qk + tid]);
+        } else {
+            v_s[tid - D] = to_f32(bf16(a.v)[v + tid - D]);
+            do_s[tid - D] = to_f32(bf16(gr.grad_o)[v + tid - D]);
+        }
+        __syncthreads();
+    };
+    auto column = [&](float (*r)[D], int c) {  // over the warps
+        float x = 0.f;
+#pragma unroll
+        for (int w = 0; w < kGradThreads / 32; ++w) x += r[w][c];
+        return x;
+    };
+    for (int64_t t = t_begin; t < t_end; ++t) {
+        stage(t);
+        const float al = expf(a.log_decay[t * a.Hv + h]), b = a.beta[t * a.Hv + h];
+        float4* const to = saved(t);
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kGradRows; ++i) {
+            to[i * (D / 4)] = S[i];
+            const float kr = k_s[r0 + i];
+            S[i].x *= al; S[i].y *= al; S[i].z *= al; S[i].w *= al;
+            y.x = fmaf(kr, S[i].x, y.x); y.y = fmaf(kr, S[i].y, y.y);
+            y.z = fmaf(kr, S[i].z, y.z); y.w = fmaf(kr, S[i].w, y.w);
+        }
+        reinterpret_cast<float4*>(red[0][warp])[lane] = y;
+        __syncthreads();
+        if (tid < D) u_s[tid] = b * (v_s[tid] - column(red[0], tid));
+        __syncthreads();
+        const float4 u = reinterpret_cast<const float4*>(u_s)[lane];
+#pragma unroll
+        for (int i = 0; i < kGradRows; ++i) {
+            const float kr = k_s[r0 + i];
+            S[i].x = fmaf(kr, u.x, S[i].x); S[i].y = fmaf(kr, u.y, S[i].y);
+            S[i].z = fmaf(kr, u.z, S[i].z); S[i].w = fmaf(kr, u.w, S[i].w);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kGradRows; ++i)
+        G[i] = gr.grad_S_final ? reinterpret_cast<const float4*>(gr.grad_S_final + state + i * D)[lane]
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int64_t t = t_end - 1; t >= t_begin; --t) {
+        const float4* const from = saved(t);
+#pragma unroll
+        for (int i = 0; i < kGradRows; ++i) S[i] = from[i * (D / 4)];
+        stage(t);
+        const float al = expf(a.log_decay[t * a.Hv + h]), b = a.beta[t * a.Hv + h];
+        const float4 dO = reinterpret_cast<const float4*>(do_s)[lane];
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f), gk = y;
+#pragma unroll
+        for (int i = 0; i < kGradRows; ++i) {
+            const float kr = k_s[r0 + i], qr = q_s[r0 + i];
+            S[i].x *= al; S[i].y *= al; S[i].z *= al; S[i].w *= al;
+            G[i].x = fmaf(qr, dO.x, G[i].x); G[i].y = fmaf(qr, dO.y, G[i].y);
+            G[i].z = fmaf(qr, dO.z, G[i].z); G[i].w = fmaf(qr, dO.w, G[i].w);
+            y.x = fmaf(kr, S[i].x, y.x); y.y = fmaf(kr, S[i].y, y.y);
+            y.z = fmaf(kr, S[i].z, y.z); y.w = fmaf(kr, S[i].w, y.w);
+            gk.x = fmaf(kr, G[i].x, gk.x); gk.y = fmaf(kr, G[i].y, gk.y);
+            gk.z = fmaf(kr, G[i].z, gk.z); gk.w = fmaf(kr, G[i].w, gk.w);
+        }
+        reinterpret_cast<float4*>(red[0][warp])[lane] = y;
+        reinterpret_cast<float4*>(red[1][warp])[lane] = gk;
+        __syncthreads();
+        float db = 0.f, ud = 0.f;
+        if (tid < D) {
+            const float e = v_s[tid] - column(red[0], tid), g = column(red[1], tid), u = b * e;
+            u_s[tid] = u;
+            z_s[tid] = -b * g;
+            db = g * e;
+            ud = u * do_s[tid];
+            static_cast<__nv_bfloat16*>(gr.grad_v)[(static_cast<size_t>(t) * a.Hv + h) * D + tid] =
+                __float2bfloat16_rn(b * g);
+        }
+        db = block_sum(db, part[0]);
+        ud = block_sum(ud, part[1]);
+        const float4 u = reinterpret_cast<const float4*>(u_s)[lane], z = reinterpret_cast<const float4*>(z_s)[lane];
+        float rq[kGradRows], rk[kGradRows], ld = 0.f;
+#pragma unroll
+        for (int i = 0; i < kGradRows; ++i) {
+            rq[i] = fmaf(S[i].x, dO.x, fmaf(S[i].y, dO.y, fmaf(S[i].z, dO.z, S[i].w * dO.w)));
+            rk[i] = fmaf(S[i].x, z.x, fmaf(S[i].y, z.y, fmaf(S[i].z, z.z, S[i].w * z.w)));
+            rk[i] = fmaf(G[i].x, u.x, fmaf(G[i].y, u.y, fmaf(G[i].z, u.z, fmaf(G[i].w, u.w, rk[i]))));
+            const float kr = k_s[r0 + i];
+            G[i].x = fmaf(kr, z.x, G[i].x); G[i].y = fmaf(kr, z.y, G[i].y);
+            G[i].z = fmaf(kr, z.z, G[i].z); G[i].w = fmaf(kr, z.w, G[i].w);
+            ld = fmaf(G[i].x, S[i].x, fmaf(G[i].y, S[i].y, fmaf(G[i].z, S[i].z, fmaf(G[i].w, S[i].w, ld))));
+            G[i].x *= al; G[i].y *= al; G[i].z *= al; G[i].w *= al;
+        }
+        const int row = r0 + (lane >> 1);
+        const float dq = fmaf(k_s[row], ud, sum_rows(rq, lane)), dk = sum_rows(rk, lane);
+        if (!(lane & 1)) {
+            if (group == 1) {
+                const size_t at = (static_cast<size_t>(t) * a.Hk + hk) * D + row;
+                static_cast<__nv_bfloat16*>(gr.grad_q)[at] = __float2bfloat16_rn(dq);
+                static_cast<__nv_bfloat16*>(gr.grad_k)[at] = __float2bfloat16_rn(dk);
+            } else {
+                float* const at = sums + (static_cast<size_t>(t) * a.Hv + h) * 2 * D + row;
+                at[0] = dq;
+                at[D] = dk;
+            }
+        }
+        ld = block_sum(ld, part[2]);
+        if (tid == 0) {
+            gr.grad_log_decay[t * a.Hv + h] = ld;
+            gr.grad_beta[t * a.Hv + h] = db;
+        }
+    }
+    if (gr.grad_S0) {
+#pragma unroll
+        for (int i = 0; i < kGradRows; ++i) reinterpret_cast<float4*>(gr.grad_S0 + state + i * D)[lane] = G[i];
+    }
+}
+
+// dq and dk of a token's q/k head: its value heads' added up in order, rounded once.
+__global__ void __launch_bounds__(2 * D)
+    kda_gdn_group_sum_kernel(const float* __restrict__ sums, int32_t Hk, int32_t group, __nv_bfloat16* __restrict__ grad_q,
+                             __nv_bfloat16* __restrict__ grad_k) {
+    grid_wait();
+    const float* from = sums + static_cast<size_t>(blockIdx.x) * group * 2 * D + threadIdx.x;
+    float x = 0.f;
+    for (int i = 0; i < group; ++i) x += from[static_cast<size_t>(i) * 2 * D];
+    __nv_bfloat16* const to = threadIdx.x < D ? grad_q : grad_k;
+    to[static_cast<size_t>(blockIdx.x) * D + threadIdx.x % D] = __float2bfloat16_rn(x);
+}
+
 }  // namespace
 
 cudaError_t launch_gdn_decode(bool f32_io, const void* q, const void* k, const void* v, const float* log_decay,
@@ -299,6 +496,23 @@ cudaError_t launch_gdn_recurrent(bool f32_io, const GdnArgs& a, cudaStream_t str
     if (f32_io) kda_gdn_recurrent_kernel<float><<<blocks, kRecThreads, 0, stream>>>(a);
     else kda_gdn_recurrent_kernel<__nv_bfloat16><<<blocks, kRecThreads, 0, stream>>>(a);
     return cudaGetLastError();
+}
+
+size_t gdn_recurrent_backward_workspace(int64_t total_tokens, int32_t Hk, int32_t Hv) {
+    const size_t T = static_cast<size_t>(total_tokens);
+    return round_up(T * Hv * D * D * 4, kAlign) + round_up(Hv > Hk ? 2 * T * Hv * D * 4 : 0, kAlign) + kAlign;
+}
+
+cudaError_t launch_gdn_recurrent_backward(const GdnArgs& a, const GdnBackwardArgs& b, void* workspace, cudaStream_t stream) {
+    const int64_t blocks = static_cast<int64_t>(a.num_seqs) * a.Hv;
+    if (blocks == 0) return cudaSuccess;
+    float* const states = static_cast<float*>(workspace);
+    float* const sums = states + round_up(static_cast<size_t>(a.total_tokens) * a.Hv * D * D * 4, kAlign) / 4;
+    kda_gdn_recurrent_grad_kernel<<<static_cast<unsigned>(blocks), kGradThreads, 0, stream>>>(a, b, states, sums);
+    const cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess || a.Hv == a.Hk || a.total_tokens == 0) return err;
+    return launch_dependent(kda_gdn_group_sum_kernel, a.total_tokens * a.Hk, 2 * D, 0, stream, sums, a.Hk, a.Hv / a.Hk,
+                            static_cast<__nv_bfloat16*>(b.grad_q), static_cast<__nv_bfloat16*>(b.grad_k));
 }
 
 }  // namespace kda

@@ -228,6 +228,9 @@ struct GdnBackwardArgs {
     float* grad_beta = nullptr;
     float* grad_S0 = nullptr;              // NULL: not stored
 };
+// Token by token in fp32 (kda_gdn_recurrent.cu).
+size_t gdn_recurrent_backward_workspace(int64_t total_tokens, int32_t Hk, int32_t Hv);
+cudaError_t launch_gdn_recurrent_backward(const GdnArgs& a, const GdnBackwardArgs& b, void* workspace, cudaStream_t stream);
 cudaError_t launch_gdn_backward(const GdnArgs& a, const GdnBackwardArgs& b, const GdnWorkspace& w, const CUtensorMap& tm_q,
                                 const CUtensorMap& tm_k, cudaStream_t stream);
 cudaError_t launch_gdn_decode(bool f32_io, const void* q, const void* k, const void* v, const float* log_decay,

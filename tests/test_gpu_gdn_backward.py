@@ -222,3 +222,52 @@ def test_backward_groups_on_few_sms(lengths, Hk, Hv):
     check(x, grads)
     again = kda.kda_gdn_prefill_backward(**x)
     assert all(torch.equal(a, b) for a, b in zip(grads, again))
+
+
+# Up to two tokens a sequence and six more go token by token in fp32.  An error of a value here is some roundings, 2^-24 of what it adds up, of
+# which `sizes` bounds the largest part; bf16 gradients are rounded once.
+SHORT = 64 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("lengths,Hk,Hv", [([1], 1, 1), ([1], 2, 8), ([0, 1, 0], 1, 1), ([16], 1, 3), ([3, 0, 4, 5], 2, 4), ([1] * 40, 2, 2),
+                                           ([2, 5], 4, 16)])
+def test_backward_of_few_tokens(lengths, Hk, Hv):
+    x = with_grads(inputs(lengths, Hk, Hv, seed=93 + len(lengths)))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    grads = kda.kda_gdn_prefill_backward(**x, device_status=status)
+    assert int(status.item()) == 0
+    size, ref = sizes(x), reference(x)
+    few = sum(lengths) <= 2 * len(lengths) + 6  # more go in chunks, with their tolerances
+    for name, got, want in zip(NAMES, grads, ref) if few else ():
+        far = np.abs(host(got).astype(np.float64) - want)
+        top = np.abs(want).max(initial=0.0)
+        if name in size:
+            assert np.all(far <= SHORT * (128 * size[name] + np.abs(want)) + 1e-30), (name, far.max())
+        elif got.dtype == torch.float32:
+            assert np.all(far <= SHORT * top + 1e-30), name
+        else:
+            assert np.all(far <= 2.0 ** -8 * np.abs(want) * (1 + SHORT) + 16 * SHORT * top + 1e-30), name
+    check(x, grads, ref)
+    again = kda.kda_gdn_prefill_backward(**x)
+    assert all(torch.equal(a, b) for a, b in zip(grads, again))
+
+
+def test_backward_of_few_tokens_extreme_decays():
+    x = with_grads(inputs([10], 2, 4, seed=94))
+    x["log_decay"][3, 0], x["log_decay"][7, 1], x["log_decay"][5, 2] = -np.inf, torch.finfo(torch.float32).min, 0.0
+    x["beta"][5], x["beta"][6] = 0.0, 1.0
+    grads = kda.kda_gdn_prefill_backward(**x)
+    check(x, grads)
+    assert float(grads[3][3, 0]) == 0.0 and float(grads[3][7, 1]) == 0.0
+
+
+@pytest.mark.parametrize("cu", [[0, 2, 1, 5], [0, 1, 2, 4], [1, 2, 3, 5], [0, -5, 3, 5], [0, 3, 20, 5]])
+def test_backward_of_few_tokens_bad_cu_seqlens(cu):
+    x = with_grads(inputs([2, 1, 2], 1, 2, seed=95))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x["cu_seqlens"] = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    guard = torch.full((40, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    like = [torch.empty_like(x[n]) for n in ("q", "k", "v", "log_decay", "beta", "S0")]
+    kda.kda_gdn_prefill_backward(**x, grads=(*like[:2], guard[:5], *like[3:]), device_status=status)
+    assert int(status.item()) == kda.KDA_DEV_BAD_CU_SEQLENS
+    assert bool((guard[5:] == 7.0).all())
