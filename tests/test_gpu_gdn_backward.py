@@ -271,3 +271,24 @@ def test_backward_of_few_tokens_bad_cu_seqlens(cu):
     kda.kda_gdn_prefill_backward(**x, grads=(*like[:2], guard[:5], *like[3:]), device_status=status)
     assert int(status.item()) == kda.KDA_DEV_BAD_CU_SEQLENS
     assert bool((guard[5:] == 7.0).all())
+
+
+@pytest.mark.parametrize("lengths,Hk,Hv", [([3, 2], 2, 4), ([70, 40], 2, 4)])
+def test_backward_replayed_and_on_streams(lengths, Hk, Hv):
+    x, y = (with_grads(inputs(lengths, Hk, Hv, seed=s)) for s in (96, 97))
+    want, other = kda.kda_gdn_prefill_backward(**x), kda.kda_gdn_prefill_backward(**y)
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = [(kda.kda_gdn_prefill_backward(**x, stream=one), kda.kda_gdn_prefill_backward(**y, stream=two)) for _ in range(5)]
+    torch.cuda.synchronize()
+    for a, b in got:
+        assert all(torch.equal(g, w) for g, w in zip(a, want)) and all(torch.equal(g, w) for g, w in zip(b, other))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        first = kda.kda_gdn_prefill_backward(**x)
+        second = kda.kda_gdn_prefill_backward(**y)
+    for t in (*first, *second):
+        t.zero_()
+    for _ in range(3):
+        graph.replay()
+    assert all(torch.equal(g, w) for g, w in zip(first, want)) and all(torch.equal(g, w) for g, w in zip(second, other))
