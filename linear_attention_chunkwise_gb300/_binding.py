@@ -99,7 +99,8 @@ def load_library(path: str | None = None):
             raise RuntimeError(f"libkda.so is not built ({p}); run __graft_entry__.build() first")
         lib = ctypes.CDLL(p)
         # The same library called with the interpreter lock held: a call only checks and launches, 3 us, and giving
-        # the lock up and taking it back costs a call that also makes tensors 1.8 us of 8.4.
+        # the lock up and taking it back costs a call that also makes tensors 1.8 us of 8.4.  (A launch that finds the
+        # device's queue full waits with the lock; nothing on the device waits for Python.)
         lib.held = held = ctypes.PyDLL(p)
         P, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         lib.kda_abi_version.argtypes = []
