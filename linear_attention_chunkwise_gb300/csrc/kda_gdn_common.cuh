@@ -28,8 +28,8 @@ constexpr size_t kImgStride = kImgPl, kImgStrideBwd = kImgPl2 + kTriBytes;
 static_assert((5 * C + 4) * 4 <= 1536 && kImgStride % kAlign == 0 && kImgStrideBwd % kAlign == 0 &&
                   kImgScanBytes % 16 == 0,
               "image layout");
-// The wide scan's images: T's two terms and P's first as whole 128B-swizzled [64][64] tiles, zero above the
-// diagonal, then the vectors.
+// The wide scan's images: T's two terms and P's first as whole 128B-swizzled [64][64] tiles, whose blocks above
+// the diagonal are never written nor used, then the vectors.
 constexpr uint32_t kTileBytes = 8192;
 constexpr size_t kImgStrideTile = 3 * kTileBytes + 1536;
 // Block (i, j), j <= i, and within it the pair of columns 2 t, 2 t + 1 of its half n in row g (+ 8 e).

@@ -244,13 +244,6 @@ __global__ void __launch_bounds__(kPrepThreads, 5)
                 }
             }
         }
-        if (tile) {  // the blocks above the diagonal: rows of 16 r + .. end with 6 - 2 r chunks of 16 bytes
-            for (int e = tid; e < 3 * 48 * 6; e += kPrepThreads) {
-                const int m = e / 288, row = (e - 288 * m) / 6, ch = 7 - (e - 288 * m - 6 * row);
-                if (ch > 2 * (row >> 4) + 1)
-                    *reinterpret_cast<uint4*>(img + m * kTileBytes + sw128_chunk(row, ch)) = make_uint4(0u, 0u, 0u, 0u);
-            }
-        }
         __syncthreads();
         if (tid < 64) {  // D_b = (I + A_bb)^-1, column c of block b
             const int b = tid >> 4, c = tid & 15;

@@ -15,7 +15,7 @@
 // products and another the copies.
 // A chunk is three products and three epilogues one after the other: 3.2 us, of which the tensor pipe is busy 28%
 // and the issue slots 40%; what bounds it is the chain of their latencies.  24571 tokens in eight sequences, the
-// longest of 6825, x 32 heads: 344 us, 505 with prep and the tables; with two CTAs of 64 columns on mma.sync 489 and
+// longest of 6825, x 32 heads: 344 us, 500 with prep and the tables; with two CTAs of 64 columns on mma.sync 489 and
 // 632.  With the left operands in shared memory the call took 610 us (its bandwidth is what bounds then), with
 // sixteen epilogue warps 533, with V read after the first product instead of during it 529; with the outputs on four
 // warps of their own 552 (they are in the way all the time then, not while the second product runs).
@@ -128,6 +128,14 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
 #pragma unroll
                 for (int s = 0; s < 4; ++s) mma_bf16_ta(tmem + d, tmem + a + 8 * s, b + 2 * s, id, s > 0 || !fresh);
             };
+            // The same with T or P: tokens 16 s .. of K reach the columns from there on only, and the blocks above the
+            // diagonal are not read.
+            auto lower_steps = [&](uint32_t d, uint32_t a, uint64_t b, bool fresh) {
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    mma_bf16_ta(tmem + d + 16 * s, tmem + a + 8 * s, b + 128 * s + 2 * s,
+                                idesc_bf16_f32(128, 64 - 16 * s, false, false), s > 0 || !fresh);
+            };
             for (int c = 0; c < nch; ++c) {
                 const uint32_t par = c & 1, st = smem_u32(sm + c % L::ST * L::STAGE), dq = L::DQ + 64 * par;
                 const uint64_t d_k = sdesc_sw128(st + L::KQ, 16, 1024), d_q = d_k + 512;
@@ -142,9 +150,9 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
                 steps(dq, L::SH, d_q, true);
                 steps(dq, L::SH + 32, d_q + 1024, false);
                 if (!past(L::B_R, par)) break;
-                steps(L::D2, L::RH, d_t, true);
-                steps(L::D2, L::RL, d_t, false);
-                steps(L::D2, L::RH, d_t + 512, false);
+                lower_steps(L::D2, L::RH, d_t, true);
+                lower_steps(L::D2, L::RL, d_t, false);
+                lower_steps(L::D2, L::RH, d_t + 512, false);
                 mma_commit(&bars[L::B_D2]);
                 if (!past(L::B_U, par)) break;
 #pragma unroll
@@ -155,7 +163,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
                                     d_k + 1024 * kh + 128 * (s & 3), id_k, s > 0);
                     if (kh == 0) {
                         mma_commit(&bars[L::B_D3]);
-                        steps(L::D4, L::UH, d_p, true);
+                        lower_steps(L::D4, L::UH, d_p, true);
                         mma_commit(&bars[L::B_D4]);
                     }
                 }

@@ -376,3 +376,14 @@ def test_prefill_many_pairs_similar_keys():
     k = x["k"].float() + 0.5 / 128 ** 0.5 * 4
     x["k"] = (k / k.norm(dim=-1, keepdim=True)).to(torch.bfloat16)
     check(x, *kda.kda_gdn_prefill(**x))
+
+
+@pytest.mark.parametrize("lengths,Hk,Hv", [([70, 100, 200], 1, 2), ([70, 100, 200], 16, 32), ([70], 1, 2), ([5, 6], 1, 2)])
+def test_prefill_with_a_workspace_of_nans(lengths, Hk, Hv):
+    """Nothing that the call has not written itself reaches a result."""
+    x = inputs(lengths, Hk, Hv, seed=98)
+    need = kda.kda_gdn_prefill_workspace_bytes(torch.bfloat16, len(lengths), sum(lengths), Hk, Hv)
+    o, S = kda.kda_gdn_prefill(**x, workspace=torch.full((need,), 255, dtype=torch.uint8, device="cuda"))
+    o2, S2 = kda.kda_gdn_prefill(**x, workspace=torch.zeros(need, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(o, o2) and torch.equal(S, S2)
+    check(x, o, S)

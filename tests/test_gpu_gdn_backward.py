@@ -292,3 +292,13 @@ def test_backward_replayed_and_on_streams(lengths, Hk, Hv):
     for _ in range(3):
         graph.replay()
     assert all(torch.equal(g, w) for g, w in zip(first, want)) and all(torch.equal(g, w) for g, w in zip(second, other))
+
+
+@pytest.mark.parametrize("lengths,Hk,Hv", [([3, 2], 2, 4), ([70, 100], 2, 4), ([70, 100, 65], 16, 32)])
+def test_backward_with_a_workspace_of_nans(lengths, Hk, Hv):
+    x = with_grads(inputs(lengths, Hk, Hv, seed=99))
+    need = kda.kda_gdn_prefill_backward_workspace_bytes(torch.bfloat16, len(lengths), sum(lengths), Hk, Hv)
+    got = kda.kda_gdn_prefill_backward(**x, workspace=torch.full((need,), 255, dtype=torch.uint8, device="cuda"))
+    check(x, got)
+    again = kda.kda_gdn_prefill_backward(**x, workspace=torch.zeros(need, dtype=torch.uint8, device="cuda"))
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
