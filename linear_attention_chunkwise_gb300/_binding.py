@@ -98,9 +98,10 @@ def load_library(path: str | None = None):
         if not os.path.exists(p):
             raise RuntimeError(f"libkda.so is not built ({p}); run __graft_entry__.build() first")
         lib = ctypes.CDLL(p)
-        # The same library called with the interpreter lock held: a call only checks and launches, 3 us, and giving
-        # the lock up and taking it back costs a call that also makes tensors 1.8 us of 8.4.  (A launch that finds the
-        # device's queue full waits with the lock; nothing on the device waits for Python.)
+        # The same library called with the interpreter lock held, for the workspace queries of _gdn.py, which are
+        # arithmetic.  A call that launches goes through `lib`, which gives the lock up: a launch waits while the
+        # device's queue is full, and what it waits behind may need another Python thread (a host callback, a
+        # collective whose other half a thread has yet to launch).
         lib.held = held = ctypes.PyDLL(p)
         P, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         lib.kda_abi_version.argtypes = []
@@ -155,7 +156,7 @@ def load_library(path: str | None = None):
                 ("kda_rms_norm", E, [P, P, E, P, F, i64, i32, E, i32, P, P, P, P]),
                 ("kda_rms_norm_backward_workspace_bytes", sz, [i64, i32]),
                 ("kda_rms_norm_backward", E, [P, P, P, E, P, F, i64, i32, P, P, P, sz, P])):
-            for functions in (lib, held):
+            for functions in (lib, held) if name.endswith("_workspace_bytes") else (lib,):
                 getattr(functions, name).restype, getattr(functions, name).argtypes = res, args
         if path is None:
             _lib = lib

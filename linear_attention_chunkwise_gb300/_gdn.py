@@ -138,7 +138,7 @@ def kda_gdn_prefill(q, k, v, log_decay, beta, cu_seqlens, S0=None, *, o=None, S_
     cu_seqlens: int32 [N+1] on the device; S0: fp32 [N, Hv, 128, 128] or None.  Returns (o, S_final) --
     S_final is None when return_final is False and none was given.
     """
-    lib = _b.load_library().held
+    lib = _b.load_library()
     dev, code = _first(q, "q", 3)
     T = q.shape[0]
     Hk, Hv, dk, dv = _heads(q, v, "[T, Hv, 128]")
@@ -161,7 +161,7 @@ def kda_gdn_prefill(q, k, v, log_decay, beta, cu_seqlens, S0=None, *, o=None, S_
         mine.append(S_final := torch.empty((N, Hv, dk, dv), dtype=torch.float32, device=dev))
     need = 0
     if workspace is None:
-        need = lib.kda_gdn_prefill_workspace_bytes(code, N, T, Hk, Hv, dk, dv)
+        need = lib.held.kda_gdn_prefill_workspace_bytes(code, N, T, Hk, Hv, dk, dv)
     else:
         _b._check(workspace, "workspace", torch.uint8, dev)
     _b._check(device_status, "device_status", torch.int32, dev)
@@ -188,7 +188,7 @@ def kda_gdn_prefill_backward(q, k, v, log_decay, beta, cu_seqlens, grad_o, S0=No
     Returns (grad_q, grad_k, grad_v, grad_log_decay, grad_beta, grad_S0): the first three in the dtype of q,
     the others fp32; grad_S0 is None when need_grad_S0 is False.  `grads` may pass those six tensors in.
     """
-    lib = _b.load_library().held
+    lib = _b.load_library()
     dev, code = _first(q, "q", 3)
     T = q.shape[0]
     Hk, Hv, dk, dv = _heads(q, v, "[T, Hv, 128]")
@@ -219,7 +219,7 @@ def kda_gdn_prefill_backward(q, k, v, log_decay, beta, cu_seqlens, grad_o, S0=No
                 _check(x, n, dt, shape, dev)
     need = 0
     if workspace is None:
-        need = lib.kda_gdn_prefill_backward_workspace_bytes(code, N, T, Hk, Hv, dk, dv)
+        need = lib.held.kda_gdn_prefill_backward_workspace_bytes(code, N, T, Hk, Hv, dk, dv)
     else:
         _b._check(workspace, "workspace", torch.uint8, dev)
     _b._check(device_status, "device_status", torch.int32, dev)
@@ -238,7 +238,7 @@ def kda_gdn_decode_step(q, k, v, log_decay, beta, S, state_indices=None, *, o=No
     q, k: [N, Hk, 128]; v: [N, Hv, 128] (bf16 or fp32); log_decay, beta: [N, Hv] fp32; state_indices:
     int32 [N] or None (slot n for sequence n).  Returns o [N, Hv, 128].
     """
-    lib = _b.load_library().held
+    lib = _b.load_library()
     dev, code = _first(q, "q", 3)
     N = q.shape[0]
     Hk, Hv, dk, dv = _heads(q, v, "[N, Hv, 128]")
@@ -273,7 +273,7 @@ def kda_rms_norm(x, weight=None, residual=None, *, eps=1e-6, quant=None, group=0
     (group=128).  Returns (y, scales, residual_out): scales [rows, scales in a row] is None without quant,
     residual_out (h in the type of x) None without a residual.
     """
-    lib = _b.load_library().held
+    lib = _b.load_library()
     dev, code = _first(x, "x", 2)
     rows, dim = x.shape
     _contiguous(x, "x")
@@ -321,7 +321,7 @@ def kda_rms_norm_backward(grad_y, h, weight=None, *, grad_h=None, eps=1e-6, need
     weight: fp32 [dim] or None (ones).  Returns (grad_x, grad_weight): grad_x, in that type, is the
     gradient of x and of residual alike; grad_weight fp32 [dim], or None when not asked for.
     """
-    lib = _b.load_library().held
+    lib = _b.load_library()
     dev, code = _first(h, "h", 2)
     rows, dim = h.shape
     _contiguous(h, "h")
@@ -343,7 +343,7 @@ def kda_rms_norm_backward(grad_y, h, weight=None, *, grad_h=None, eps=1e-6, need
     if workspace is not None:
         _b._check(workspace, "workspace", torch.uint8, dev)
     elif grad_weight is not None:
-        need = lib.kda_rms_norm_backward_workspace_bytes(rows, dim)
+        need = lib.held.kda_rms_norm_backward_workspace_bytes(rows, dim)
     args = (grad_y.data_ptr(), h.data_ptr(), _p(grad_h), code, _p(weight), eps, rows, dim, grad_x.data_ptr(),
             _p(grad_weight))
     handle = _stream(stream, dev, *mine)
