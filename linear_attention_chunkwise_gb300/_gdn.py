@@ -95,16 +95,28 @@ def _call_with_workspace(function, dev, workspace, need, args, rest):
         _free(memory)
 
 
-def _stream(stream, dev, *mine):
-    """The stream's handle; tensors that this call allocated are kept alive on a stream of the caller's."""
+def _stream(stream, dev):
+    """The handle of the stream that the call goes to."""
     if stream is None:
         return _current_stream(dev.index)
     if stream.device != dev:
         raise ValueError(f"stream is on {stream.device}, expected {dev}")
-    for t in mine:
-        if t is not None:
-            t.record_stream(stream)
     return stream.cuda_stream
+
+
+def _new(stream, dev, make, *args, **kwargs):
+    """An output of this call, make(...), in memory of the stream that writes it.
+
+    A block of the current stream's may still be in use there, by work queued before the block was freed, which the
+    caller's `stream` does not wait for.  Where the caller drops the output, it is free once the current stream is done with it too.
+    """
+    if stream is None:
+        return make(*args, **kwargs)
+    current = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        t = make(*args, **kwargs)
+    t.record_stream(current)
+    return t
 
 
 def _heads(q, v, name):
@@ -150,15 +162,15 @@ def kda_gdn_prefill(q, k, v, log_decay, beta, cu_seqlens, S0=None, *, o=None, S_
     N = _sequences(cu_seqlens, dev)
     if S0 is not None:
         _check(S0, "S0", torch.float32, (N, Hv, dk, dv), dev)
-    mine = []
+    handle = _stream(stream, dev)
     if o is None:
-        mine.append(o := torch.empty_like(v))
+        o = _new(stream, dev, torch.empty_like, v)
     else:
         _check(o, "o", q.dtype, (T, Hv, dv), dev)
     if S_final is not None:
         _check(S_final, "S_final", torch.float32, (N, Hv, dk, dv), dev)
     elif return_final:
-        mine.append(S_final := torch.empty((N, Hv, dk, dv), dtype=torch.float32, device=dev))
+        S_final = _new(stream, dev, torch.empty, (N, Hv, dk, dv), dtype=torch.float32, device=dev)
     need = 0
     if workspace is None:
         need = lib.held.kda_gdn_prefill_workspace_bytes(code, N, T, Hk, Hv, dk, dv)
@@ -169,7 +181,7 @@ def kda_gdn_prefill(q, k, v, log_decay, beta, cu_seqlens, S0=None, *, o=None, S_
         lib.kda_gdn_prefill, dev, workspace, need,
         (q.data_ptr(), k.data_ptr(), v.data_ptr(), code, log_decay.data_ptr(), beta.data_ptr(), _p(S0),
          cu_seqlens.data_ptr(), N, T, Hk, Hv, dk, dv, o.data_ptr(), _p(S_final)),
-        (_p(device_status), _stream(stream, dev, *mine)))
+        (_p(device_status), handle))
     return o, S_final
 
 
@@ -206,11 +218,10 @@ def kda_gdn_prefill_backward(q, k, v, log_decay, beta, cu_seqlens, grad_o, S0=No
             _check(x, name, f32, state, dev)
     specs = (("grad_q", q.dtype, (T, Hk, dk)), ("grad_k", q.dtype, (T, Hk, dk)), ("grad_v", q.dtype, (T, Hv, dv)),
              ("grad_log_decay", f32, (T, Hv)), ("grad_beta", f32, (T, Hv)), ("grad_S0", f32, state))
-    mine = []
+    handle = _stream(stream, dev)
     if grads is None:
-        grads = tuple(torch.empty_like(t) for t in (q, k, v, log_decay, beta)) + (
-            torch.empty(state, dtype=f32, device=dev) if need_grad_S0 else None,)
-        mine.extend(grads)
+        grads = tuple(_new(stream, dev, torch.empty_like, t) for t in (q, k, v, log_decay, beta)) + (
+            _new(stream, dev, torch.empty, state, dtype=f32, device=dev) if need_grad_S0 else None,)
     elif len(grads) != 6:
         raise ValueError("grads must hold 6 tensors")
     else:
@@ -227,7 +238,7 @@ def kda_gdn_prefill_backward(q, k, v, log_decay, beta, cu_seqlens, grad_o, S0=No
         lib.kda_gdn_prefill_backward, dev, workspace, need,
         (q.data_ptr(), k.data_ptr(), v.data_ptr(), code, log_decay.data_ptr(), beta.data_ptr(), _p(S0),
          cu_seqlens.data_ptr(), N, T, Hk, Hv, dk, dv, grad_o.data_ptr(), _p(grad_S_final), *(_p(x) for x in grads)),
-        (_p(device_status), _stream(stream, dev, *mine)))
+        (_p(device_status), handle))
     return tuple(grads)
 
 
@@ -251,16 +262,16 @@ def kda_gdn_decode_step(q, k, v, log_decay, beta, S, state_indices=None, *, o=No
     _check(S, "S", torch.float32, (slots, Hv, dk, dv), dev)
     if state_indices is not None:
         _check(state_indices, "state_indices", torch.int32, (N,), dev)
-    mine = []
+    handle = _stream(stream, dev)
     if o is None:
-        mine.append(o := torch.empty_like(v))
+        o = _new(stream, dev, torch.empty_like, v)
     else:
         _check(o, "o", q.dtype, (N, Hv, dv), dev)
     _b._check(device_status, "device_status", torch.int32, dev)
     _call(lib.kda_gdn_decode_step, dev,
           q.data_ptr(), k.data_ptr(), v.data_ptr(), code, log_decay.data_ptr(), beta.data_ptr(), S.data_ptr(),
           slots, _p(state_indices), N, Hk, Hv, dk, dv, o.data_ptr(), _p(device_status),
-          _stream(stream, dev, *mine))
+          handle)
     return o
 
 
@@ -284,28 +295,28 @@ def kda_rms_norm(x, weight=None, residual=None, *, eps=1e-6, quant=None, group=0
     out_type, out_dtype = _NORM_OUT[quant]
     if group not in ((0, 128) if quant else (0,)) or (group and dim % group):
         raise ValueError(f"group must be 0, or 128 with an 8-bit output and dim a multiple of it, got {group}")
-    mine = []
+    handle = _stream(stream, dev)
     if residual is not None:
         _check(residual, "residual", x.dtype, (rows, dim), dev)
     if residual_out is not None:
         _check(residual_out, "residual_out", x.dtype, (rows, dim), dev)
     elif residual is not None:
-        mine.append(residual_out := torch.empty_like(x))
+        residual_out = _new(stream, dev, torch.empty_like, x)
     if y is None:
-        mine.append(y := torch.empty_like(x, dtype=out_dtype))
+        y = _new(stream, dev, torch.empty_like, x, dtype=out_dtype)
     else:
         _check(y, "y", out_dtype or x.dtype, (rows, dim), dev)
     if quant:
         shape = (rows, dim // group if group else 1)
         if scales is None:
-            mine.append(scales := torch.empty(shape, dtype=torch.float32, device=dev))
+            scales = _new(stream, dev, torch.empty, shape, dtype=torch.float32, device=dev)
         else:
             _check(scales, "scales", torch.float32, shape, dev)
     elif scales is not None:
         raise ValueError("scales are written with an 8-bit output only")
     _call(lib.kda_rms_norm, dev,
           x.data_ptr(), _p(residual), code, _p(weight), eps, rows, dim, out_type, group, y.data_ptr(), _p(scales),
-          _p(residual_out), _stream(stream, dev, *mine))
+          _p(residual_out), handle)
     return y, scales, residual_out
 
 
@@ -330,15 +341,15 @@ def kda_rms_norm_backward(grad_y, h, weight=None, *, grad_h=None, eps=1e-6, need
         _check(grad_h, "grad_h", h.dtype, (rows, dim), dev)
     if weight is not None:
         _check(weight, "weight", torch.float32, (dim,), dev)
-    mine = []
+    handle = _stream(stream, dev)
     if grad_x is None:
-        mine.append(grad_x := torch.empty_like(h))
+        grad_x = _new(stream, dev, torch.empty_like, h)
     else:
         _check(grad_x, "grad_x", h.dtype, (rows, dim), dev)
     if grad_weight is not None:
         _check(grad_weight, "grad_weight", torch.float32, (dim,), dev)
     elif need_grad_weight:
-        mine.append(grad_weight := torch.empty((dim,), dtype=torch.float32, device=dev))
+        grad_weight = _new(stream, dev, torch.empty, (dim,), dtype=torch.float32, device=dev)
     need = 0
     if workspace is not None:
         _b._check(workspace, "workspace", torch.uint8, dev)
@@ -346,7 +357,6 @@ def kda_rms_norm_backward(grad_y, h, weight=None, *, grad_h=None, eps=1e-6, need
         need = lib.held.kda_rms_norm_backward_workspace_bytes(rows, dim)
     args = (grad_y.data_ptr(), h.data_ptr(), _p(grad_h), code, _p(weight), eps, rows, dim, grad_x.data_ptr(),
             _p(grad_weight))
-    handle = _stream(stream, dev, *mine)
     if grad_weight is None and workspace is None:
         _call(lib.kda_rms_norm_backward, dev, *args, None, 0, handle)
     else:
