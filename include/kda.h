@@ -517,7 +517,8 @@ KDA_API kda_status kda_gdn_prefill(const void *q, const void *k, const void *v, 
  * qkv_dtype is KDA_DTYPE_BF16 (else KDA_ERR_UNSUPPORTED).  The call reruns the
  * chunkwise forward, keeping the state before every 64-token chunk, walks the
  * state's adjoint back over the chunks, and forms everything else per chunk.
- * Up to two tokens a sequence and six more go token by token, in fp32.
+ * Up to two tokens a sequence and six more go token by token, in fp32, but no
+ * more than 40 + num_seqs * Hv / 20 in all.
  * The fp32 gradients are accurate as S_final is; results are bitwise
  * repeatable.  The gradient of a log_decay at which the decay is 0 in fp32 is 0.
  *

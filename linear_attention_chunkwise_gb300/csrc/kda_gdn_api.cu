@@ -47,11 +47,15 @@ bool chunked(kda_dtype t, int32_t num_seqs, int64_t total_tokens) {
     return t == KDA_DTYPE_BF16 && total_tokens > (num_seqs == 1 ? 16 : 8) * static_cast<int64_t>(num_seqs);
 }
 
-// The gradient goes token by token up to two tokens a sequence and six more: in fp32, and sooner (16/32 heads: one sequence
-// of 8 tokens 36 us against 41 in chunks, 8 of 2 25 against 103, 64 of 2 164 against 548; 64 of one token and one of 65
-// among them 373 against 549, with 2/4 heads 234 against 106).
-bool chunked_backward(int32_t num_seqs, int64_t total_tokens) {
-    return total_tokens > 2 * static_cast<int64_t>(num_seqs) + 6;
+// The gradient goes token by token up to two tokens a sequence and six more, and up to so many in all that even a sequence
+// that has them all to itself, 3.5 us each one after the other, is not far behind: the host does not know the longest, and
+// empty sequences count in num_seqs.  Chunks take 0.26 us for every (sequence, head) that has a token, 0.07 where it has none.
+// (One token in each of N sequences: 64 x 32 heads 119 us against 568 in chunks, 256 x 8 heads 120 against 582, 64 x 4 heads 25 against
+// 114.  As many tokens in one of them: 322 against 178, 1081 against 187, 221 against 64; so 256 x 8 and 64 x 4 go in chunks.
+// 64 of one and one of 65: 32 heads 383 against 567, 4 heads 253 against 109.)
+bool chunked_backward(int32_t num_seqs, int64_t total_tokens, int32_t Hv) {
+    const int64_t N = num_seqs;
+    return total_tokens > std::min(2 * N + 6, 40 + N * Hv / 20);
 }
 
 }  // namespace
@@ -136,7 +140,7 @@ kda_status kda_gdn_prefill(const void* q, const void* k, const void* v, kda_dtyp
 size_t kda_gdn_prefill_backward_workspace_bytes(kda_dtype qkv_dtype, int32_t num_seqs, int64_t total_tokens, int32_t Hk,
                                                 int32_t Hv, int32_t dk, int32_t dv) {
     if (qkv_dtype != KDA_DTYPE_BF16 || gdn_shape(qkv_dtype, total_tokens, num_seqs, Hk, Hv, dk, dv) != KDA_OK) return 0;
-    if (!chunked_backward(num_seqs, total_tokens)) return kda::gdn_recurrent_backward_workspace(total_tokens, Hk, Hv);
+    if (!chunked_backward(num_seqs, total_tokens, Hv)) return kda::gdn_recurrent_backward_workspace(total_tokens, Hk, Hv);
     return kda::gdn_workspace(num_seqs, total_tokens, Hv, true, nullptr, nullptr);
 }
 
@@ -217,7 +221,7 @@ kda_status kda_gdn_prefill_backward(const void* q, const void* k, const void* v,
     b.grad_beta = grad_beta;
     b.grad_S0 = grad_S0;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (!chunked_backward(num_seqs, total_tokens))
+    if (!chunked_backward(num_seqs, total_tokens, Hv))
         return kda::launch_gdn_recurrent_backward(a, b, workspace, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
     kda::GdnWorkspace w;
     kda::gdn_workspace(num_seqs, total_tokens, Hv, true, static_cast<uint8_t*>(workspace), &w);

@@ -183,3 +183,13 @@ def test_backward_workspace_queries(lib):
     for bad in ((torch.float32, 1, 64, 2, 2), (torch.bfloat16, -1, 64, 2, 2), (torch.bfloat16, 1, 64, 2, 3),
                 (torch.bfloat16, 1, -1, 2, 2), (torch.bfloat16, 1, 64, 2, 2, 64, 128)):
         assert need(*bad) == 0
+
+
+def _in_chunks(num_seqs, tokens, heads, per_chunk):  # workspace of the chunkwise path, its tables (under 16 KB) apart
+    return (-(-tokens // 64) + num_seqs) * heads * per_chunk
+
+
+@pytest.mark.parametrize("num_seqs,tokens,Hk,Hv", [(65, 129, 2, 4), (1000, 2000, 16, 32), (64, 64, 2, 4), (2000, 2000, 1, 1)])
+def test_backward_of_one_long_sequence_among_short_ones_goes_in_chunks(num_seqs, tokens, Hk, Hv):
+    need = kda.kda_gdn_prefill_backward_workspace_bytes(torch.bfloat16, num_seqs, tokens, Hk, Hv)
+    assert 0 <= need - _in_chunks(num_seqs, tokens, Hv, 27136 + 196608) < 1 << 16
