@@ -490,9 +490,11 @@ KDA_API size_t kda_gdn_prefill_workspace_bytes(kda_dtype qkv_dtype, int32_t num_
  * other overlap) and errors are those of kda_prefill.  A malformed cu_seqlens
  * sets KDA_DEV_BAD_CU_SEQLENS; sequences with invalid bounds are not written,
  * and others may not be.  Results are bitwise repeatable.
- * fp32 inputs and short sequences (up to 8 tokens on average) go token by
- * token, and o is rounded once; in chunks of 64 it is rounded to bf16 from
- * products whose operands are.
+ * fp32 inputs and short sequences go token by token, and o is rounded once; in
+ * chunks of 64 it is rounded to bf16 from products whose operands are.  Short
+ * is one sequence of up to 16 tokens, and several of up to 8 tokens on average
+ * and 192 + num_seqs * Hv / 16 in all: the same sequence may get either o,
+ * depending on what it is packed with.
  */
 KDA_API kda_status kda_gdn_prefill(const void *q, const void *k, const void *v, kda_dtype qkv_dtype,
                                    const float *log_decay, const float *beta, const float *S0,

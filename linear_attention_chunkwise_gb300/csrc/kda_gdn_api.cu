@@ -40,11 +40,14 @@ bool qk_maps(const kda::GdnArgs& a, CUtensorMap* tm_q, CUtensorMap* tm_k) {
 }
 
 // fp32 inputs and short sequences go token by token: one of up to 16 tokens (12 us against 15), several of up to 8 on
-// average (16/32 heads: 64 of 4 tokens 132 us against 175, 64 of 8 174 against 176, 64 of 16 261 against 177, 256 of 8 671
-// against 619).  A long sequence among many short ones is what the average must not hide: 3000 tokens beside 255 of one
-// take 650 us in chunks and 1493 token by token.
-bool chunked(kda_dtype t, int32_t num_seqs, int64_t total_tokens) {
-    return t == KDA_DTYPE_BF16 && total_tokens > (num_seqs == 1 ? 16 : 8) * static_cast<int64_t>(num_seqs);
+// average, and up to so many in all that a sequence that has them all to itself, 0.3 us each one after the other, takes no
+// more than about twice what chunks take: the host does not know the longest, and empty sequences count in num_seqs.
+// (64 sequences, 16/32 heads: of 4 tokens each 134 us against 176 in chunks, 256 in one of them 155 against 96; of 8 tokens 176
+// against 177, 512 in one 247 against 101.  256 of 4: 510 against 614, 1024 in one 592 against 306; with 2/4 heads 71 against
+// 102 and 331 against 84, so that goes in chunks.  3000 tokens beside 255 of one take 650 us in chunks and 1493 token by token.)
+bool chunked(kda_dtype t, int32_t num_seqs, int64_t total_tokens, int32_t Hv) {
+    const int64_t N = num_seqs;
+    return t == KDA_DTYPE_BF16 && total_tokens > (N == 1 ? 16 : std::min(8 * N, 192 + N * Hv / 16));
 }
 
 // The gradient goes token by token up to two tokens a sequence and six more, and up to so many in all that even a sequence
@@ -65,7 +68,7 @@ extern "C" {
 size_t kda_gdn_prefill_workspace_bytes(kda_dtype qkv_dtype, int32_t num_seqs, int64_t total_tokens, int32_t Hk,
                                        int32_t Hv, int32_t dk, int32_t dv) {
     if (gdn_shape(qkv_dtype, total_tokens, num_seqs, Hk, Hv, dk, dv) != KDA_OK) return 0;
-    if (!chunked(qkv_dtype, num_seqs, total_tokens)) return kAlign;
+    if (!chunked(qkv_dtype, num_seqs, total_tokens, Hv)) return kAlign;
     return kda::gdn_workspace(num_seqs, total_tokens, Hv, false, nullptr, nullptr);
 }
 
@@ -123,7 +126,7 @@ kda_status kda_gdn_prefill(const void* q, const void* k, const void* v, kda_dtyp
     a.Hv = Hv;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t err = cudaSuccess;
-    if (chunked(qkv_dtype, num_seqs, total_tokens)) {
+    if (chunked(qkv_dtype, num_seqs, total_tokens, Hv)) {
         kda::GdnWorkspace w;
         kda::gdn_workspace(num_seqs, total_tokens, Hv, false, static_cast<uint8_t*>(workspace), &w);
         CUtensorMap tm_q, tm_k;

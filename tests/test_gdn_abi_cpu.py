@@ -193,3 +193,9 @@ def _in_chunks(num_seqs, tokens, heads, per_chunk):  # workspace of the chunkwis
 def test_backward_of_one_long_sequence_among_short_ones_goes_in_chunks(num_seqs, tokens, Hk, Hv):
     need = kda.kda_gdn_prefill_backward_workspace_bytes(torch.bfloat16, num_seqs, tokens, Hk, Hv)
     assert 0 <= need - _in_chunks(num_seqs, tokens, Hv, 27136 + 196608) < 1 << 16
+
+
+@pytest.mark.parametrize("num_seqs,tokens,Hk,Hv", [(1000, 8000, 16, 32), (256, 1024, 2, 4), (64, 512, 16, 32), (40, 300, 1, 1)])
+def test_prefill_of_one_long_sequence_among_short_ones_goes_in_chunks(num_seqs, tokens, Hk, Hv):
+    need = kda.kda_gdn_prefill_workspace_bytes(torch.bfloat16, num_seqs, tokens, Hk, Hv)
+    assert 0 <= need - _in_chunks(num_seqs, tokens, Hv, 3 * 8192 + 1536) < 1 << 16
