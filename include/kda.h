@@ -466,7 +466,8 @@ KDA_API kda_status kda_prefill_noalloc(const void *q, const void *k, const void 
  */
 
 /*
- * Workspace of kda_gdn_prefill (device bytes, 256-byte aligned start).
+ * Workspace of kda_gdn_prefill (device bytes, 256-byte aligned start), enough
+ * for every call with as many tokens and sequences or fewer (of the same heads).
  * Returns 0 for invalid arguments.
  */
 KDA_API size_t kda_gdn_prefill_workspace_bytes(kda_dtype qkv_dtype, int32_t num_seqs, int64_t total_tokens,
@@ -484,7 +485,8 @@ KDA_API size_t kda_gdn_prefill_workspace_bytes(kda_dtype qkv_dtype, int32_t num_
  *   o          [total_tokens, Hv, dv]  qkv_dtype (out)
  *   S_final    [num_seqs, Hv, dk, dv]  fp32 (out), or NULL
  *   workspace  >= kda_gdn_prefill_workspace_bytes(...), else KDA_ERR_WORKSPACE
- *              (bf16: about 0.4 KB per token and value head)
+ *              (bf16: about 0.4 KB per token and value head and 26 KB per
+ *              sequence and value head)
  *
  * Sequences, start and final states, aliasing (S_final may be S0 exactly, no
  * other overlap) and errors are those of kda_prefill.  A malformed cu_seqlens
@@ -525,10 +527,11 @@ KDA_API kda_status kda_gdn_prefill(const void *q, const void *k, const void *v, 
  * repeatable.  The gradient of a log_decay at which the decay is 0 in fp32 is 0.
  *
  * Workspace: >= kda_gdn_prefill_backward_workspace_bytes(...) device bytes
- * (about 3.5 KB per token and value head, 64 KB where it goes token by token),
- * 256-byte aligned.  q, k, v, grad_o,
- * states and their gradients are 16-byte aligned, the others 4.  The outputs
- * overlap nothing (KDA_ERR_INVALID_ARG).  A malformed cu_seqlens sets
+ * (about 3.5 KB per token and value head and 220 KB per sequence and value
+ * head; 64 KB per token and value head where it goes token by token), enough
+ * for every call with as many tokens and sequences or fewer, 256-byte aligned.
+ * q, k, v, grad_o, states and their gradients are 16-byte aligned, the others
+ * 4.  The outputs overlap nothing (KDA_ERR_INVALID_ARG).  A malformed cu_seqlens sets
  * KDA_DEV_BAD_CU_SEQLENS and leaves the gradients unspecified.
  */
 KDA_API size_t kda_gdn_prefill_backward_workspace_bytes(kda_dtype qkv_dtype, int32_t num_seqs, int64_t total_tokens,

@@ -45,9 +45,9 @@ bool qk_maps(const kda::GdnArgs& a, CUtensorMap* tm_q, CUtensorMap* tm_k) {
 // (64 sequences, 16/32 heads: of 4 tokens each 134 us against 176 in chunks, 256 in one of them 155 against 96; of 8 tokens 176
 // against 177, 512 in one 247 against 101.  256 of 4: 510 against 614, 1024 in one 592 against 306; with 2/4 heads 71 against
 // 102 and 331 against 84, so that goes in chunks.  3000 tokens beside 255 of one take 650 us in chunks and 1493 token by token.)
+int64_t most_by_token(int64_t N, int32_t Hv) { return N == 1 ? 16 : std::min(8 * N, 192 + N * Hv / 16); }
 bool chunked(kda_dtype t, int32_t num_seqs, int64_t total_tokens, int32_t Hv) {
-    const int64_t N = num_seqs;
-    return t == KDA_DTYPE_BF16 && total_tokens > (N == 1 ? 16 : std::min(8 * N, 192 + N * Hv / 16));
+    return t == KDA_DTYPE_BF16 && total_tokens > most_by_token(num_seqs, Hv);
 }
 
 // The gradient goes token by token up to two tokens a sequence and six more, and up to so many in all that even a sequence
@@ -56,9 +56,30 @@ bool chunked(kda_dtype t, int32_t num_seqs, int64_t total_tokens, int32_t Hv) {
 // (One token in each of N sequences: 64 x 32 heads 119 us against 568 in chunks, 256 x 8 heads 120 against 582, 64 x 4 heads 25 against
 // 114.  As many tokens in one of them: 322 against 178, 1081 against 187, 221 against 64; so 256 x 8 and 64 x 4 go in chunks.
 // 64 of one and one of 65: 32 heads 383 against 567, 4 heads 253 against 109.)
+int64_t most_by_token_backward(int64_t N, int32_t Hv) { return std::min(2 * N + 6, 40 + N * Hv / 20); }
 bool chunked_backward(int32_t num_seqs, int64_t total_tokens, int32_t Hv) {
-    const int64_t N = num_seqs;
-    return total_tokens > std::min(2 * N + 6, 40 + N * Hv / 20);
+    return total_tokens > most_by_token_backward(num_seqs, Hv);
+}
+
+// What a call takes of its workspace.
+size_t prefill_takes(kda_dtype t, int32_t num_seqs, int64_t total_tokens, int32_t Hv) {
+    return chunked(t, num_seqs, total_tokens, Hv) ? kda::gdn_workspace(num_seqs, total_tokens, Hv, false, nullptr, nullptr) : kAlign;
+}
+size_t backward_takes(int32_t num_seqs, int64_t total_tokens, int32_t Hk, int32_t Hv) {
+    return chunked_backward(num_seqs, total_tokens, Hv) ? kda::gdn_workspace(num_seqs, total_tokens, Hv, true, nullptr, nullptr)
+                                                        : kda::gdn_recurrent_backward_workspace(total_tokens, Hk, Hv);
+}
+// The most sequences, up to num_seqs, with which so many tokens go in chunks (most(N) does not fall as N rises); 0 for
+// none.  A workspace is to serve every smaller call too, and with fewer sequences the same tokens may go in chunks.
+template <typename F>
+int32_t most_in_chunks(int32_t num_seqs, int64_t total_tokens, F most) {
+    int32_t lo = 0, hi = num_seqs;
+    while (lo < hi) {
+        const int32_t mid = hi - (hi - lo) / 2;
+        if (total_tokens > most(mid)) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
 }
 
 }  // namespace
@@ -68,8 +89,9 @@ extern "C" {
 size_t kda_gdn_prefill_workspace_bytes(kda_dtype qkv_dtype, int32_t num_seqs, int64_t total_tokens, int32_t Hk,
                                        int32_t Hv, int32_t dk, int32_t dv) {
     if (gdn_shape(qkv_dtype, total_tokens, num_seqs, Hk, Hv, dk, dv) != KDA_OK) return 0;
-    if (!chunked(qkv_dtype, num_seqs, total_tokens, Hv)) return kAlign;
-    return kda::gdn_workspace(num_seqs, total_tokens, Hv, false, nullptr, nullptr);
+    if (qkv_dtype != KDA_DTYPE_BF16) return kAlign;
+    const int32_t n = most_in_chunks(num_seqs, total_tokens, [&](int64_t N) { return most_by_token(N, Hv); });
+    return n ? prefill_takes(qkv_dtype, n, total_tokens, Hv) : kAlign;
 }
 
 kda_status kda_gdn_prefill(const void* q, const void* k, const void* v, kda_dtype qkv_dtype, const float* log_decay,
@@ -88,7 +110,7 @@ kda_status kda_gdn_prefill(const void* q, const void* k, const void* v, kda_dtyp
     if ((S0 && !aligned(S0, 16)) || (S_final && !aligned(S_final, 16)) || !aligned(workspace, kAlign) ||
         !aligned(cu_seqlens, 4) || (device_status && !aligned(device_status, 4)))
         return KDA_ERR_INVALID_ARG;
-    const size_t need = kda_gdn_prefill_workspace_bytes(qkv_dtype, num_seqs, total_tokens, Hk, Hv, dk, dv);
+    const size_t need = prefill_takes(qkv_dtype, num_seqs, total_tokens, Hv);
     if (workspace_bytes < need) return KDA_ERR_WORKSPACE;
 
     // outputs (and the workspace) overlap nothing; S_final may be S0 exactly
@@ -143,8 +165,9 @@ kda_status kda_gdn_prefill(const void* q, const void* k, const void* v, kda_dtyp
 size_t kda_gdn_prefill_backward_workspace_bytes(kda_dtype qkv_dtype, int32_t num_seqs, int64_t total_tokens, int32_t Hk,
                                                 int32_t Hv, int32_t dk, int32_t dv) {
     if (qkv_dtype != KDA_DTYPE_BF16 || gdn_shape(qkv_dtype, total_tokens, num_seqs, Hk, Hv, dk, dv) != KDA_OK) return 0;
-    if (!chunked_backward(num_seqs, total_tokens, Hv)) return kda::gdn_recurrent_backward_workspace(total_tokens, Hk, Hv);
-    return kda::gdn_workspace(num_seqs, total_tokens, Hv, true, nullptr, nullptr);
+    const int64_t few = std::min(total_tokens, most_by_token_backward(num_seqs, Hv));
+    const int32_t n = most_in_chunks(num_seqs, total_tokens, [&](int64_t N) { return most_by_token_backward(N, Hv); });
+    return std::max(backward_takes(num_seqs, few, Hk, Hv), n ? backward_takes(n, total_tokens, Hk, Hv) : 0);
 }
 
 kda_status kda_gdn_prefill_backward(const void* q, const void* k, const void* v, kda_dtype qkv_dtype,
@@ -171,7 +194,7 @@ kda_status kda_gdn_prefill_backward(const void* q, const void* k, const void* v,
                           static_cast<const void*>(cu_seqlens), static_cast<const void*>(device_status)})
         if (!aligned(x, 4)) return KDA_ERR_INVALID_ARG;
     if (!aligned(workspace, kAlign)) return KDA_ERR_INVALID_ARG;
-    const size_t need = kda_gdn_prefill_backward_workspace_bytes(qkv_dtype, num_seqs, total_tokens, Hk, Hv, dk, dv);
+    const size_t need = backward_takes(num_seqs, total_tokens, Hk, Hv);
     if (workspace_bytes < need) return KDA_ERR_WORKSPACE;
 
     // the outputs (and the workspace) overlap nothing

@@ -199,3 +199,19 @@ def test_backward_of_one_long_sequence_among_short_ones_goes_in_chunks(num_seqs,
 def test_prefill_of_one_long_sequence_among_short_ones_goes_in_chunks(num_seqs, tokens, Hk, Hv):
     need = kda.kda_gdn_prefill_workspace_bytes(torch.bfloat16, num_seqs, tokens, Hk, Hv)
     assert 0 <= need - _in_chunks(num_seqs, tokens, Hv, 3 * 8192 + 1536) < 1 << 16
+
+
+@pytest.mark.parametrize("Hk,Hv", [(1, 1), (2, 4), (16, 32), (4, 128)])
+@pytest.mark.parametrize("query", ["kda_gdn_prefill_workspace_bytes", "kda_gdn_prefill_backward_workspace_bytes"])
+def test_a_workspace_serves_every_smaller_call(query, Hk, Hv):
+    need = lambda n, t: getattr(kda, query)(torch.bfloat16, n, t, Hk, Hv)  # noqa: E731
+    seqs = [1, 2, 3, 5, 8, 9, 13, 60, 61, 64, 65, 200, 1000]
+    tokens = [0, 1, 2, 7, 8, 9, 14, 15, 16, 17, 40, 41, 64, 65, 70, 128, 129, 134, 135, 200, 201, 512, 513, 2000, 2048, 8000, 8001]
+    table = [[need(n, t) for t in tokens] for n in seqs]
+    for row in table:
+        assert row[0] >= 256 and row == sorted(row)
+    for column in zip(*table):
+        assert list(column) == sorted(column)
+    # and a workspace that is smaller than what a call takes is refused
+    call = _prefill if query == "kda_gdn_prefill_workspace_bytes" else _backward
+    assert call(kda.load_library(), N=1, T=128, Hk=Hk, Hv=Hv, wsb=need(1, 128) - 1) == WS

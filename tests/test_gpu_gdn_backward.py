@@ -312,3 +312,15 @@ def test_backward_around_the_choice_of_the_path(lengths, Hk, Hv):
     grads = kda.kda_gdn_prefill_backward(**x, device_status=status)
     assert int(status.item()) == 0
     check(x, grads)
+
+
+def test_one_workspace_for_smaller_calls():
+    Hk, Hv = 2, 4
+    fwd = torch.empty(kda.kda_gdn_prefill_workspace_bytes(torch.bfloat16, 40, 64, Hk, Hv), dtype=torch.uint8, device="cuda")
+    back = torch.empty(kda.kda_gdn_prefill_backward_workspace_bytes(torch.bfloat16, 40, 64, Hk, Hv), dtype=torch.uint8, device="cuda")
+    for lengths in ([1] * 40, [64], [7], [8], [1, 63], [0] * 30 + [34], [2] * 8, [0, 0]):
+        x = inputs(lengths, Hk, Hv, seed=107 + len(lengths))
+        g = with_grads(x)
+        for a, b in ((kda.kda_gdn_prefill(**x), kda.kda_gdn_prefill(**x, workspace=fwd)),
+                     (kda.kda_gdn_prefill_backward(**g), kda.kda_gdn_prefill_backward(**g, workspace=back))):
+            assert all(torch.equal(s, t) for s, t in zip(a, b))
