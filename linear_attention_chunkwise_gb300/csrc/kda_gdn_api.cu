@@ -224,10 +224,9 @@ kda_status kda_gdn_prefill_backward(const void* q, const void* k, const void* v,
     if (num_seqs == 0) return KDA_OK;
 
     kda::GdnArgs a;
-    // tensor maps want a valid base even when there are no tokens (never read then)
-    a.q = have_tokens ? q : workspace;
-    a.k = have_tokens ? k : workspace;
-    a.v = have_tokens ? v : workspace;
+    a.q = q;
+    a.k = k;
+    a.v = v;
     a.log_decay = log_decay;
     a.beta = beta;
     a.S0 = S0;
@@ -238,7 +237,7 @@ kda_status kda_gdn_prefill_backward(const void* q, const void* k, const void* v,
     a.Hk = Hk;
     a.Hv = Hv;
     kda::GdnBackwardArgs b;
-    b.grad_o = have_tokens ? grad_o : workspace;
+    b.grad_o = grad_o;
     b.grad_S_final = grad_S_final;
     b.grad_q = grad_q;
     b.grad_k = grad_k;

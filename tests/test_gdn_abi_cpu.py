@@ -215,3 +215,11 @@ def test_a_workspace_serves_every_smaller_call(query, Hk, Hv):
     # and a workspace that is smaller than what a call takes is refused
     call = _prefill if query == "kda_gdn_prefill_workspace_bytes" else _backward
     assert call(kda.load_library(), N=1, T=128, Hk=Hk, Hv=Hv, wsb=need(1, 128) - 1) == WS
+
+
+def test_backward_takes_no_tokens(lib):
+    # past validation: no GPU here, so the device check answers
+    if torch.cuda.is_available():
+        pytest.skip("fake addresses")
+    none = {n: None for n in ("q", "k", "v", "ld", "beta", "do", "dq", "dk", "dv", "dld", "db")}
+    assert _backward(lib, T=0, **none) in (kda.KDA_ERR_CUDA, UNS)
