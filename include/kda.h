@@ -497,6 +497,10 @@ KDA_API size_t kda_gdn_prefill_workspace_bytes(kda_dtype qkv_dtype, int32_t num_
  * is one sequence of up to 16 tokens, and several of up to 8 tokens on average
  * and 192 + num_seqs * Hv / 16 in all: the same sequence may get either o,
  * depending on what it is packed with.
+ * Inputs that are not finite reach the outputs of their token and of later ones
+ * of their sequence, and in chunks also up to 15 earlier ones: those of the same
+ * 16 tokens, counted from the sequence's start (the products with T and P go
+ * over whole 16 x 16 blocks, and 0 times NaN is NaN).
  */
 KDA_API kda_status kda_gdn_prefill(const void *q, const void *k, const void *v, kda_dtype qkv_dtype,
                                    const float *log_decay, const float *beta, const float *S0,

@@ -394,3 +394,21 @@ def test_prefill_with_a_workspace_of_nans(lengths, Hk, Hv):
 def test_prefill_around_the_most_tokens_of_short_sequences(lengths, Hk, Hv):
     x = inputs(lengths, Hk, Hv, seed=106 + sum(lengths))
     check(x, *kda.kda_gdn_prefill(**x))
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("name", ["q", "k", "v", "log_decay", "beta"])
+@pytest.mark.parametrize("lengths,Hk,Hv,exact", [([30, 130, 40], 1, 2, False), ([30, 130, 40], 16, 32, False), ([3, 2, 2], 1, 2, True)])
+def test_prefill_how_far_back_a_bad_token_reaches(lengths, Hk, Hv, exact, name, value):
+    """Not before the 16 tokens of its sequence that it is among (before itself where the call goes token by token)."""
+    x = inputs(lengths, Hk, Hv, seed=108)
+    o, S = kda.kda_gdn_prefill(**x)
+    start, end = lengths[0], lengths[0] + lengths[1]
+    bad = start + (1 if exact else 64 + 37)
+    first = bad if exact else start + 64 + 32
+    y = {n: t.clone() for n, t in x.items()}
+    y[name][bad] = value
+    o2, S2 = kda.kda_gdn_prefill(**y)
+    assert torch.equal(o[:first], o2[:first]) and torch.equal(o[end:], o2[end:])
+    assert torch.equal(S[[0, 2]], S2[[0, 2]])
+    assert not bool(o2[bad].isfinite().all())
