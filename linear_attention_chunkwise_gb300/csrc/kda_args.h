@@ -1,4 +1,4 @@
-// kda_args.h -- argument checks shared by the C-ABI front ends.
+// kda_args.h -- argument checks shared by the C-ABI front ends, and what kda_api.cu does for the others.
 #pragma once
 
 #include <cstddef>
@@ -7,6 +7,14 @@
 #include "kda_internal.h"
 
 namespace kda {
+
+// SMs of the current device (0 when the runtime cannot say).
+int device_sm_count();
+
+// Tensor map over a bf16 [T][H][128] tensor with boxes of box_rows tokens of one head and box_inner
+// channels; false when the driver refuses it.
+bool make_tensor_map(CUtensorMap* m, const void* base, uint64_t H, uint64_t T, uint32_t box_inner, uint32_t box_rows,
+                     CUtensorMapSwizzle sw);
 
 constexpr size_t kAlign = 256;  // workspaces and the regions inside them
 

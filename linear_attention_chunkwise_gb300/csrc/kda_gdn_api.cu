@@ -3,8 +3,7 @@
 #include <algorithm>
 #include <climits>
 
-#include "kda_args.h"
-#include "kda_internal.h"
+#include "kda_gdn_internal.h"
 
 using kda::aligned;
 using kda::esize_of;

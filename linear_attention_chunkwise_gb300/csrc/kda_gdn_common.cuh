@@ -4,9 +4,8 @@
 
 #include <cuda_bf16.h>
 
-#include "kda_args.h"
-#include "kda_internal.h"
-#include "kda_ptx.cuh"
+#include "kda_gdn_internal.h"
+#include "kda_gdn_ptx.cuh"
 
 namespace kda {
 namespace gdn {

@@ -11,9 +11,8 @@
 // Value head h reads q/k head h / (Hv / Hk).
 #include <cuda_bf16.h>
 
-#include "kda_args.h"
-#include "kda_internal.h"
-#include "kda_ptx.cuh"
+#include "kda_gdn_internal.h"
+#include "kda_gdn_ptx.cuh"
 
 namespace kda {
 namespace {

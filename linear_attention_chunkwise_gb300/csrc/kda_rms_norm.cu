@@ -18,9 +18,8 @@
 
 #include <algorithm>
 
-#include "kda_args.h"
-#include "kda_internal.h"
-#include "kda_ptx.cuh"
+#include "kda_gdn_internal.h"
+#include "kda_gdn_ptx.cuh"
 
 namespace kda {
 namespace {

@@ -55,3 +55,10 @@ def test_our_arm_json_line(monkeypatch, capsys):
     assert "decode" in d and "backward" in d
     assert set(d["prefill_workloads"]) == {"varlen_prefill", "long_prefill_1m"}
     assert d["chain_bound"]["us"] > 0 and 0 < d["chain_bound"]["frac"]
+
+
+def test_recorded_traffic_is_that_of_the_sources_as_they_are():
+    """profiles/ncu_traffic.json was captured on the kernels that are built now, so the line reports it."""
+    for kernel, sources in (("kda_prefill_two_pass", bench.PREFILL_SOURCES), ("kda_decode_kernel", bench.DECODE_SOURCES),
+                            ("kda_decode_multi_kernel", bench.DECODE_SOURCES), ("kda_prefill_backward", bench.BACKWARD_SOURCES)):
+        assert bench.ncu_traffic(kernel, sources), kernel
