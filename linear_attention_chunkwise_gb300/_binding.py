@@ -9,6 +9,7 @@ a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -185,6 +186,25 @@ def _stream_handle(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _in_its_streams_memory(entry):
+    """With stream=, what the call allocates is that stream's: work queued on the current stream may still use a block
+    that was freed there, and the call's workspace is free for the next user before the kernels are done with it.  The
+    results are recorded on the current stream, whose work a dropped one waits for.
+    """
+    @functools.wraps(entry)
+    def call(*args, stream=None, **kwargs):
+        if not isinstance(stream, torch.cuda.Stream):  # the current one, or a handle in an object of the caller's
+            return entry(*args, stream=stream, **kwargs)
+        current = torch.cuda.current_stream(stream.device)
+        with torch.cuda.stream(stream):
+            results = entry(*args, stream=stream, **kwargs)
+        for t in results if isinstance(results, tuple) else (results,):
+            if t is not None:
+                t.record_stream(current)
+        return results
+    return call
+
+
 def _check(t: torch.Tensor | None, name: str, dtype=None, device=None):
     if t is None:
         return
@@ -214,6 +234,7 @@ def kda_prefill_min_workspace_bytes(qkv_dtype, num_seqs: int, total_tokens: int,
                                                               int(dk), int(dv)))
 
 
+@_in_its_streams_memory
 def kda_prefill(q, k, v, log_alpha, beta, cu_seqlens, S0=None, *, o=None, S_final=None, return_final=True,
                 workspace=None, device_status=None, stream=None, path="two_pass"):
     """Chunkwise prefill over packed sequences (see include/kda.h).
@@ -263,6 +284,7 @@ def kda_prefill(q, k, v, log_alpha, beta, cu_seqlens, S0=None, *, o=None, S_fina
     return o, S_final
 
 
+@_in_its_streams_memory
 def kda_prefill_snapshots(q, k, v, log_alpha, beta, cu_seqlens, snap_seq, snap_pos, S0=None, *, o=None,
                           S_final=None, S_snap=None, workspace=None, device_status=None, stream=None):
     """kda_prefill that also returns the state at (sequence, position) entries (see include/kda.h).
@@ -330,6 +352,7 @@ def kda_prefill_backward_gated_workspace_bytes(qkv_dtype, num_seqs: int, total_t
                                                                          int(H), int(dk), int(dv)))
 
 
+@_in_its_streams_memory
 def kda_prefill_backward(q, k, v, log_alpha, beta, cu_seqlens, grad_o, S0=None, grad_S_final=None, *,
                          need_grad_S0=True, grads=None, workspace=None, device_status=None, stream=None):
     """Gradient of kda_prefill for L = <o, grad_o> + <S_final, grad_S_final> (see include/kda.h).
@@ -342,6 +365,7 @@ def kda_prefill_backward(q, k, v, log_alpha, beta, cu_seqlens, grad_o, S0=None, 
                      workspace, device_status, stream, None)
 
 
+@_in_its_streams_memory
 def kda_prefill_backward_ex(q, k, v, log_alpha, beta, cu_seqlens, grad_o, S0=None, grad_S_final=None, *,
                             fusion=None, need_grad_S0=True, grads=None, workspace=None, device_status=None,
                             stream=None):
@@ -354,6 +378,7 @@ def kda_prefill_backward_ex(q, k, v, log_alpha, beta, cu_seqlens, grad_o, S0=Non
                      workspace, device_status, stream, fusion)
 
 
+@_in_its_streams_memory
 def kda_prefill_backward_gated(q, k, v, log_alpha, beta, cu_seqlens, grad_y, S0=None, grad_S_final=None, *,
                                fusion, need_grad_S0=True, need_grad_rms_weight=True, grads=None, workspace=None,
                                device_status=None, stream=None):
@@ -444,6 +469,7 @@ def _check_fusion(fusion, q, tokens):
     return fusion.c_struct()
 
 
+@_in_its_streams_memory
 def kda_prefill_ex(q, k, v, log_alpha, beta, cu_seqlens, S0=None, *, fusion=None, o=None, S_final=None,
                    workspace=None, device_status=None, stream=None):
     """kda_prefill with the fused prologue / epilogue of `fusion` (a Fusion); returns (o, S_final)."""
@@ -479,6 +505,7 @@ def kda_prefill_ex(q, k, v, log_alpha, beta, cu_seqlens, S0=None, *, fusion=None
     return o, S_final
 
 
+@_in_its_streams_memory
 def kda_decode_step_ex(q, k, v, log_alpha, beta, S, state_indices=None, *, fusion=None, o=None,
                        device_status=None, stream=None):
     """kda_decode_step with the fused prologue / epilogue of `fusion` (a Fusion); returns o."""
@@ -506,6 +533,7 @@ def kda_decode_step_ex(q, k, v, log_alpha, beta, S, state_indices=None, *, fusio
     return o
 
 
+@_in_its_streams_memory
 def kda_decode_step(q, k, v, log_alpha, beta, S, state_indices=None, *, o=None, device_status=None, stream=None):
     """One fused decode step; S [slots, H, 128, 128] fp32 is updated in place.
 
@@ -536,6 +564,7 @@ def kda_decode_step(q, k, v, log_alpha, beta, S, state_indices=None, *, o=None, 
     return o
 
 
+@_in_its_streams_memory
 def kda_decode_multi(q, k, v, log_alpha, beta, S, state_indices=None, *, o=None, S_steps=None,
                      return_steps=False, device_status=None, stream=None):
     """T tokens per sequence in one launch; S [slots, H, 128, 128] fp32 is updated in place.
@@ -548,6 +577,7 @@ def kda_decode_multi(q, k, v, log_alpha, beta, S, state_indices=None, *, o=None,
                          device_status, stream)
 
 
+@_in_its_streams_memory
 def kda_decode_multi_ex(q, k, v, log_alpha, beta, S, state_indices=None, *, fusion=None, o=None, S_steps=None,
                         return_steps=False, device_status=None, stream=None):
     """kda_decode_multi with the fused prologue / epilogue of `fusion` (a Fusion; out_gate [N, T, H, 128])."""
