@@ -3,6 +3,7 @@
 Tolerances.  h = 2^-8 is half a step of bf16, the most that a rounding takes a value from itself, relative to it.
 With a chunk's start state S, U, P, W, X, M and E of the formulas (those of kda_gdn_prefill.cu and kda_gdn_backward.cu):
   o = e^g q S + P U takes S, P and U rounded to bf16 and is rounded: h e^g |q| |S| + (2 h + h^2) |P| |U|, and h |o|.
+      P's products q . k are sums of 128 in fp32, off by 128 x 2^-24 |q| . |k|, whatever is left of them.
   dq = e^g dO S^T + M K,  dk = -e^g b W S^T + e^(gC - g) U X^T + M^T Q + (E + E^T) K take M and E rounded, and are
       rounded: h |M| |K|, h (|M|^T |Q| + (|E| + |E|^T) |K|), and h of the value; dv = b W is rounded only.
 Everything else is fp32 or in two bf16 terms: for o at most STATE of the largest entry of S and of U (as the states are
@@ -59,8 +60,9 @@ def bound_o(x, ref):
             P = G * torch.einsum("ihc,jhc->hij", q[s], k[s])
             qs = eg[:, :, None] * torch.einsum("ihc,hcv->ihv", q[s].abs(), start.abs())
             pu = torch.einsum("hij,jhv->ihv", P.abs(), u.abs())
+            gram = torch.einsum("hij,jhv->ihv", G * torch.einsum("ihc,jhc->hij", q[s].abs(), k[s].abs()), u.abs())
             rest = eg * q[s].abs().sum(-1) * start.abs().amax((1, 2)) + P.abs().sum(-1).T * u.abs().amax((0, 2))
-            out[s] = (1 + H) * (H * qs + (2 * H + H * H) * pu + STATE * rest[:, :, None])
+            out[s] = (1 + H) * (H * qs + (2 * H + H * H) * pu + 2.0 ** -17 * gram + STATE * rest[:, :, None])
     return out.cpu().numpy() + H * np.abs(ref)
 
 
