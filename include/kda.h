@@ -460,9 +460,14 @@ KDA_API kda_status kda_prefill_noalloc(const void *q, const void *k, const void 
  * 128) and add heads in groups: Hk heads of q and k, Hv of v, Hv a multiple of
  * Hk; value head h uses q/k head h / (Hv / Hk).  log_decay has no lower limit
  * (-inf, a decay of 0, included): decays enter as exp of differences that are
- * at most the largest decay.  States, decays and the sums over tokens are
- * fp32-accurate: S_final agrees with the token-by-token recurrence to about
- * 1e-5 relative, not only to the rounding of bf16 operands.
+ * at most the largest decay.  States, decays and the sums over tokens are held
+ * in fp32.  Token by token (below: short sequences, fp32 inputs, the decode
+ * step) the products are fp32 too.  In chunks the products that make states and
+ * fp32 gradients take operands of two bf16 terms, off by at most 2^-17: S_final
+ * and those gradients agree with the recurrence to about 5e-6 of their 2-norm
+ * (fp32 products: 1e-7 to 4e-7).  The products that make o, grad_q and grad_k
+ * take some operands in one bf16 term: o is off by 3.3e-3, grad_q and grad_k by
+ * 2.2e-3, where their own rounding to bf16 is 1.7e-3.
  */
 
 /*
@@ -584,7 +589,7 @@ KDA_API kda_status kda_gdn_decode_step(const void *q, const void *k, const void 
  *              The code is y / scale rounded to nearest even (both quotients
  *              as products with the reciprocal, in fp32); it stands for
  *              code * scale.  Values that are not finite make the scale they
- *              share NaN.
+ *              share NaN (a y of infinity: infinite).
  *
  * x, residual, residual_out, y 16-byte aligned, weight and scales 4-byte; dim
  * from 1 to KDA_NORM_MAX_DIM.  Outputs overlap nothing but as said above
@@ -611,8 +616,8 @@ KDA_API kda_status kda_rms_norm(const void *x, const void *residual, kda_dtype d
  *   grad_y, h, grad_h  [rows, dim] dtype; h as the forward stored it; grad_h
  *                      may be NULL (zeros)
  *   grad_x             [rows, dim] dtype (out; may be grad_y or grad_h exactly)
- *   grad_weight        [dim] fp32 (out), or NULL (not computed); rows are added
- *                      in a fixed order (bitwise repeatable)
+ *   grad_weight        [dim] fp32 (out), 16-byte aligned, or NULL (not computed);
+ *                      rows are added in a fixed order (bitwise repeatable)
  *   workspace          >= kda_rms_norm_backward_workspace_bytes(rows, dim) when
  *                      grad_weight is given, 256-byte aligned, else it may be NULL
  */

@@ -38,7 +38,7 @@ bool qk_maps(const kda::GdnArgs& a, CUtensorMap* tm_q, CUtensorMap* tm_k) {
            kda::make_tensor_map(tm_k, a.k, a.Hk, a.total_tokens, 64, kda::kChunk, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// fp32 inputs and short sequences go token by token: one of up to 16 tokens (12 us against 15), several of up to 8 on
+// fp32 inputs and short sequences go token by token: one of up to 16 tokens (14 us against 17), several of up to 8 on
 // average, and up to so many in all that a sequence that has them all to itself, 0.3 us each one after the other, takes no
 // more than about twice what chunks take: the host does not know the longest, and empty sequences count in num_seqs.
 // (64 sequences, 16/32 heads: of 4 tokens each 134 us against 176 in chunks, 256 in one of them 155 against 96; of 8 tokens 176

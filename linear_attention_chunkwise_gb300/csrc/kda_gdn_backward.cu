@@ -34,7 +34,7 @@ using namespace gdn;
 // either is a chain that leaves the SM's issue slots and tensor cores half idle, and the two do not wait for
 // each other.  8192 tokens x 16/32 heads: 447 us, 3.5 us a chunk, 0.8 GB of records written; the tensor pipe is 51%
 // busy, the back walk's chain is the longer one.  The copying warps' registers go to the walks': launched with 168 a
-// thread, 3 x 168 = 216 + 248 + 40.
+// thread, 3 x 168 = 216 + 248 + 40; five words spill at 32 columns, none at 64.
 template <int NT>
 struct BackCfg {
     static constexpr int ST = 2;

@@ -7,11 +7,15 @@
 // (the chunk form of "Understanding Kimi Delta Attention" (pyshine), "The Chunkwise DPLR Algorithm",
 // with its scalar gate).  Unlike the channel-wise gate, the scalar one multiplies the Gram matrices
 // afterwards, so every product has the raw bf16 k or q as one operand, and the decays enter as
-// exponentials of differences: no lower limit on log_decay, and fp32 accuracy when the other operand
-// (state, right-hand side, U) is split into two bf16 terms, x = hi + lo with |x - hi - lo| <= 2^-17 |x|.
+// exponentials of differences: no lower limit on log_decay.  What else a state's products take (the state itself, the
+// right-hand side, T, U) is two bf16 terms, x = hi + lo with |x - hi - lo| <= 2^-17 |x|, accumulated in fp32: S_final is good
+// to about 4e-6 of itself, where fp32 products give up to 4e-7.  The outputs' products take one term of S, P
+// and U, since o is rounded to bf16 anyway: 3.3e-3 of itself, where the rounding alone is 1.7e-3.  (Second terms there
+// would be 52 more products a chunk beside the 200 of the mma.sync scan's warps; the tcgen05 scan has neither the TMEM columns
+// for U's nor the shared memory for P's.)
 //
 // pass 0  chunk table (launch_chunk_table)
-// pass 1  one CTA per (chunk, value head): Gram matrices, T, P, decays -> an image in the workspace
+// pass 1  one CTA per (chunk, q/k head, up to four of its value heads): Gram matrices, T, P, decays -> images in the workspace
 // pass 2  scan: the walk of kda_gdn_walk.cuh over the chunks of every (sequence, value head).
 #include <algorithm>
 
@@ -32,7 +36,8 @@ using namespace gdn;
 // its registers.  (The block products in fp32 on the CUDA cores and one value head a CTA, 256 threads:
 // 109 us for 8192 tokens x 32 heads, 16.1 K warp instructions a (chunk, head); a warp for every row of blocks
 // and the decays of one value head after the other: 70 us; now 63.  The issue slots are 38% busy, HBM 34%: the
-// rest is the latency of a CTA's steps, five CTAs an SM.)
+// rest is the latency of a CTA's steps, five CTAs an SM: 61.6 us, four of them 66.  The 96 registers that leaves spill 27
+// words of the plain images' kernel and 35 of the tiles'.)
 constexpr int kPrepThreads = 128;
 constexpr int kPrepHeads = 4;  // most value heads of a CTA: a warp for each one's decays
 

@@ -173,12 +173,8 @@ __device__ __forceinline__ void walk_forward(const WalkUnit& wu, const WalkPipe&
             BTerms b[NT];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                if constexpr (REC) {
-                    put_record(S[k][n], rec + kRecS, 32768, 2 * k, rcol + n, lane);
-                    b[n] = b_terms(S[k][n]);
-                } else {
-                    b[n] = b_terms(S[k][n]);
-                }
+                if constexpr (REC) put_record(S[k][n], rec + kRecS, 32768, 2 * k, rcol + n, lane);
+                b[n] = b_terms(S[k][n]);
                 sh[k][n][0] = b[n].h0;
                 sh[k][n][1] = b[n].h1;
             }
