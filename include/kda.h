@@ -500,7 +500,7 @@ KDA_API size_t kda_gdn_prefill_workspace_bytes(kda_dtype qkv_dtype, int32_t num_
  * fp32 inputs and short sequences go token by token, and o is rounded once; in
  * chunks of 64 it is rounded to bf16 from products whose operands are.  Short
  * is one sequence of up to 16 tokens, and several of up to 8 tokens on average
- * and 192 + num_seqs * Hv / 16 in all: the same sequence may get either o,
+ * and 240 + num_seqs * Hv / 8 in all: the same sequence may get either o,
  * depending on what it is packed with.
  * Inputs that are not finite reach the outputs of their token and of later ones
  * of their sequence, and in chunks also up to 15 earlier ones: those of the same
@@ -531,7 +531,7 @@ KDA_API kda_status kda_gdn_prefill(const void *q, const void *k, const void *v, 
  * chunkwise forward, keeping the state before every 64-token chunk, walks the
  * state's adjoint back over the chunks, and forms everything else per chunk.
  * Up to two tokens a sequence and six more go token by token, in fp32, but no
- * more than 40 + num_seqs * Hv / 20 in all.
+ * more than 64 + num_seqs * Hv / 20 in all.
  * The fp32 gradients are accurate as S_final is; results are bitwise
  * repeatable.  The gradient of a log_decay at which the decay is 0 in fp32 is 0.
  *

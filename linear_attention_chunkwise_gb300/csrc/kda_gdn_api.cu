@@ -40,22 +40,27 @@ bool qk_maps(const kda::GdnArgs& a, CUtensorMap* tm_q, CUtensorMap* tm_k) {
 
 // fp32 inputs and short sequences go token by token: one of up to 16 tokens (14 us against 17), several of up to 8 on
 // average, and up to so many in all that a sequence that has them all to itself, 0.3 us each one after the other, takes no
-// more than about twice what chunks take: the host does not know the longest, and empty sequences count in num_seqs.
-// (64 sequences, 16/32 heads: of 4 tokens each 134 us against 176 in chunks, 256 in one of them 155 against 96; of 8 tokens 176
-// against 177, 512 in one 247 against 101.  256 of 4: 510 against 614, 1024 in one 592 against 306; with 2/4 heads 71 against
-// 102 and 331 against 84, so that goes in chunks.  3000 tokens beside 255 of one take 650 us in chunks and 1493 token by token.)
-int64_t most_by_token(int64_t N, int32_t Hv) { return N == 1 ? 16 : std::min(8 * N, 192 + N * Hv / 16); }
+// more than about two and a half times what chunks take: the host does not know the longest, and empty sequences count in
+// num_seqs.  (us token by token and in chunks, tokens spread evenly, and all in one of the sequences:
+//   64 sequences x 32 heads,  256 tokens:  134, 176;   155,   96       512:   176,  177;   247, 101 (in chunks)
+//   256 x 32,                1024:         510, 614;   592,  306      2048:   677,  616;   988, 323 (in chunks)
+//   64 x 4,                   256:          22,  37;    72,   37       512:    28,   36;   133,  49 (in chunks)
+//   256 x 4,                  256:          57, 100;   107,   65       512:    62,  101;   186,  66 (in chunks)
+// 3000 tokens beside 255 of one: 1493 and 650, in chunks.)
+int64_t most_by_token(int64_t N, int32_t Hv) { return N == 1 ? 16 : std::min(8 * N, 240 + N * Hv / 8); }
 bool chunked(kda_dtype t, int32_t num_seqs, int64_t total_tokens, int32_t Hv) {
     return t == KDA_DTYPE_BF16 && total_tokens > most_by_token(num_seqs, Hv);
 }
 
-// The gradient goes token by token up to two tokens a sequence and six more, and up to so many in all that even a sequence
-// that has them all to itself, 3.5 us each one after the other, is not far behind: the host does not know the longest, and
-// empty sequences count in num_seqs.  Chunks take 0.26 us for every (sequence, head) that has a token, 0.07 where it has none.
-// (One token in each of N sequences: 64 x 32 heads 119 us against 568 in chunks, 256 x 8 heads 120 against 582, 64 x 4 heads 25 against
-// 114.  As many tokens in one of them: 322 against 178, 1081 against 187, 221 against 64; so 256 x 8 and 64 x 4 go in chunks.
-// 64 of one and one of 65: 32 heads 383 against 567, 4 heads 253 against 109.)
-int64_t most_by_token_backward(int64_t N, int32_t Hv) { return std::min(2 * N + 6, 40 + N * Hv / 20); }
+// The gradient goes token by token up to two tokens a sequence and six more, and up to so many in all that a sequence that
+// has them all to itself, 3.5 us each one after the other, takes no more than about four times what chunks take, since
+// chunks take about five times as long where the tokens are spread evenly.  (us token by token and in chunks, even; in one:
+//   64 sequences x 32 heads, 64 tokens: 119, 568;  322, 178       134: 179, 571;  642, 184
+//   256 x 32,               256:        437, 2119; 1364, 542      518: 645, 2130; 2578, 561 (in chunks)
+//   64 x 4,                  64:         25, 114;  221,  64       134:  26, 112;  463,  74 (in chunks)
+//   256 x 8,                256:        120, 582;  1081, 187 (in chunks)
+// 64 of one and one of 65: 32 heads 383 and 567, 4 heads 253 and 109, in chunks.)
+int64_t most_by_token_backward(int64_t N, int32_t Hv) { return std::min(2 * N + 6, 64 + N * Hv / 20); }
 bool chunked_backward(int32_t num_seqs, int64_t total_tokens, int32_t Hv) {
     return total_tokens > most_by_token_backward(num_seqs, Hv);
 }

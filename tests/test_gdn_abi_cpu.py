@@ -189,7 +189,7 @@ def _in_chunks(num_seqs, tokens, heads, per_chunk):  # workspace of the chunkwis
     return (-(-tokens // 64) + num_seqs) * heads * per_chunk
 
 
-@pytest.mark.parametrize("num_seqs,tokens,Hk,Hv", [(65, 129, 2, 4), (1000, 2000, 16, 32), (64, 64, 2, 4), (2000, 2000, 1, 1)])
+@pytest.mark.parametrize("num_seqs,tokens,Hk,Hv", [(65, 129, 2, 4), (1000, 2000, 16, 32), (64, 100, 2, 4), (2000, 2000, 1, 1)])
 def test_backward_of_one_long_sequence_among_short_ones_goes_in_chunks(num_seqs, tokens, Hk, Hv):
     need = kda.kda_gdn_prefill_backward_workspace_bytes(torch.bfloat16, num_seqs, tokens, Hk, Hv)
     assert 0 <= need - _in_chunks(num_seqs, tokens, Hv, 27136 + 196608) < 1 << 16

@@ -389,8 +389,8 @@ def test_prefill_with_a_workspace_of_nans(lengths, Hk, Hv):
     check(x, o, S)
 
 
-@pytest.mark.parametrize("lengths,Hk,Hv", [([0] * 40 + [200] + [0] * 30, 1, 2), ([0] * 40 + [201] + [0] * 30, 1, 2), ([4] * 60, 2, 4),
-                                           ([1] * 255 + [250], 2, 4), ([1] * 29 + [221], 16, 32), ([1] * 29 + [222], 16, 32)])
+@pytest.mark.parametrize("lengths,Hk,Hv", [([0] * 40 + [257] + [0] * 30, 1, 2), ([0] * 40 + [258] + [0] * 30, 1, 2), ([4] * 60, 2, 4),
+                                           ([1] * 255 + [250], 2, 4), ([1] * 29 + [211], 16, 32), ([1] * 29 + [212], 16, 32)])
 def test_prefill_around_the_most_tokens_of_short_sequences(lengths, Hk, Hv):
     x = inputs(lengths, Hk, Hv, seed=106 + sum(lengths))
     check(x, *kda.kda_gdn_prefill(**x))

@@ -304,8 +304,8 @@ def test_backward_with_a_workspace_of_nans(lengths, Hk, Hv):
     assert all(torch.equal(a, b) for a, b in zip(got, again))
 
 
-@pytest.mark.parametrize("lengths,Hk,Hv", [([1] * 64 + [65], 2, 4), ([0] * 40 + [70] + [0] * 20, 2, 4), ([0] * 19 + [41], 1, 1),
-                                           ([0] * 19 + [42], 1, 1), ([1] * 44, 2, 2), ([1] * 45, 2, 2), ([1] * 50 + [2] * 10, 16, 32)])
+@pytest.mark.parametrize("lengths,Hk,Hv", [([1] * 64 + [65], 2, 4), ([0] * 40 + [70] + [0] * 20, 2, 4), ([0] * 49 + [66], 1, 1),
+                                           ([0] * 49 + [67], 1, 1), ([1] * 71, 2, 2), ([1] * 72, 2, 2), ([1] * 50 + [2] * 10, 16, 32)])
 def test_backward_around_the_choice_of_the_path(lengths, Hk, Hv):
     x = with_grads(inputs(lengths, Hk, Hv, seed=105 + len(lengths)))
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
