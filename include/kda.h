@@ -783,8 +783,8 @@ KDA_API kda_status kda_fp8_matmul_grouped(const void *x, const float *x_scales, 
 /*
  * kda_fp8_quantize -- x in e4m3 with its scales, as laid out above:
  *   scale = max(max |x| / 448, 2^-126) over what shares it, code = x / scale
- * rounded to nearest even (both fp32 quotients, rounded once).  A NaN makes the
- * scale it shares NaN, an infinity infinite.
+ * rounded to nearest even (both fp32 quotients, rounded once; a code of zero may
+ * have either sign).  A NaN makes the scale it shares NaN, an infinity infinite.
  *
  *   x       [rows, cols] dtype       codes  rows x cols bytes (out)
  *   scales  fp32 (out)

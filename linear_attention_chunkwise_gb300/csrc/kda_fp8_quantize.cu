@@ -7,7 +7,9 @@
 // maximum is taken over the bits of |x|, whose order is that of the values with infinity and NaN on top, so either reaches the scale.
 // The quotients are those of a division rounded once: with r = 1 / scale so rounded, q = x r and q + (x - q scale) r in fma (P.
 // Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990), three operations in place of a
-// division's, which bound the kernel before (8192 x 4096 bf16 by rows: 59 us).
+// division's, which bound the kernel before (8192 x 4096 bf16 by rows: 59 us).  That needs a remainder that fp32 holds: its last bit stands 46
+// places below the product of q's and scale's leading ones, and q counts down to 2^-11 (half of the smallest code rounds at 2^-10), so
+// from scales of 2^-92 on it is 2^-149 or more.  Smaller scales divide.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -65,9 +67,11 @@ __device__ __forceinline__ float scale_of(uint32_t amax) {
     return s < 0x1p-126f ? 0x1p-126f : s;  // NaN stays
 }
 struct Scale {
-    float s, r;  // and its reciprocal; r = 0 where s is not finite
+    float s, r;  // and its reciprocal; r = 0 where quotients are divisions: s small or not finite
 };
-__device__ __forceinline__ Scale with_reciprocal(float s) { return {s, s < __int_as_float(0x7f800000) ? __frcp_rn(s) : 0.f}; }
+__device__ __forceinline__ Scale with_reciprocal(float s) {
+    return {s, s >= 0x1p-92f && s < __int_as_float(0x7f800000) ? __frcp_rn(s) : 0.f};
+}
 // Codes of four quotients, the first in the lowest byte.
 __device__ __forceinline__ uint32_t codes_of(const float (&q)[4]) {
     const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, __NV_E4M3);
