@@ -69,14 +69,14 @@ __global__ void __launch_bounds__(kGlrThreads, 2) kda_glr_prefill_kernel(const _
 #pragma unroll
             for (int i = 0; i < L; ++i) {
                 h[i] = COMPLEMENT ? wide_negative(tile[i * 32]) : wide(tile[i * 32]);
-                n[i] = wide(gates[i * 32]);
+                n[i] = glr_gates<SIGMOID, false>(gates[i * 32]);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < L; ++i) {
                 const bool in = live && t + i < T;
                 h[i].p = (COMPLEMENT ? -1.f : 1.f) * glr_f32(glr_load(static_cast<const X*>(a.x) + (t + i) * dim + ch, in));
-                n[i].p = glr_f32(glr_load(static_cast<const G*>(a.gate) + (t + i) * dim + ch, in));
+                n[i] = glr_gates<SIGMOID, false>(GlrVec<G, 1>{glr_load(static_cast<const G*>(a.gate) + (t + i) * dim + ch, in)});
             }
         }
 #pragma unroll
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kGlrThreads) kda_glr_decode_kernel(const GlrDe
     GlrVec<X, V> out;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const Lanes<1> d = glr_gate<SIGMOID, false>(Lanes<1>{glr_f32(g.e[j])}).n, xi = {glr_f32(x.e[j])};
+        const Lanes<1> d = glr_gate<SIGMOID, false>(glr_gates<SIGMOID, false>(GlrVec<G, 1>{g.e[j]})).n, xi = {glr_f32(x.e[j])};
         s.e[j] = glr_step(Lanes<1>{s.e[j]}, d, COMPLEMENT ? mul(d, Lanes<1>{-xi.p}) : xi).p;
         glr_round(out.e[j], s.e[j]);
     }

@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kGlrThreads, 2) kda_glr_backward_kernel(const 
             for (int i = 0; i < L; ++i) {
                 xr[i] = reinterpret_cast<const GlrVec<X, V>*>(at)[(warp * L + i) * 32 + lane];
                 dh[i] = wide(reinterpret_cast<const GlrVec<X, V>*>(at + F::kTileX)[(warp * L + i) * 32 + lane]);
-                n[i] = wide(reinterpret_cast<const GlrVec<G, V>*>(at + 2 * F::kTileX)[(warp * L + i) * 32 + lane]);
+                n[i] = glr_gates<SIGMOID, true>(reinterpret_cast<const GlrVec<G, V>*>(at + 2 * F::kTileX)[(warp * L + i) * 32 + lane]);
             }
         } else {
 #pragma unroll
@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kGlrThreads, 2) kda_glr_backward_kernel(const 
                 const bool in = live && t + i < T;
                 xr[i].e[0] = glr_load(static_cast<const X*>(a.x) + (t + i) * dim + ch, in);
                 dh[i].p = glr_f32(glr_load(static_cast<const X*>(b.grad_h) + (t + i) * dim + ch, in));
-                n[i].p = glr_f32(glr_load(static_cast<const G*>(a.gate) + (t + i) * dim + ch, in));
+                n[i] = glr_gates<SIGMOID, true>(GlrVec<G, 1>{glr_load(static_cast<const G*>(a.gate) + (t + i) * dim + ch, in)});
             }
         }
         coming = checkpoint(block_t - step);
