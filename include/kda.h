@@ -647,10 +647,12 @@ KDA_API kda_status kda_rms_norm_backward(const void *grad_y, const void *h, cons
  * together: a state is off by a few 2^-24 of the largest one among the 128 tokens
  * before it (in the gradient: behind it), which is more than its own rounding
  * where a channel forgets a large state faster than that; decays of exactly 0
- * forget it exactly.  Results are bitwise repeatable.
+ * forget it exactly.  The single token (kda_glr_decode_step) keeps a_t h_{t-1} to
+ * 2^-19 of its own value.  Results are bitwise repeatable.
  * Inputs that are not finite reach the outputs of their token and of later ones
  * (in the gradient: earlier ones) of their sequence and channel; an infinite
- * state becomes NaN at the next token.
+ * state becomes NaN at the next token of prefill, while the single token has
+ * a_t times it.
  */
 #define KDA_GLR_SIGMOID 0x1u
 #define KDA_GLR_COMPLEMENT 0x2u

@@ -10,6 +10,7 @@
 // round's chain (tile, gates, scan, exchange, outputs: 3.4 us with two blocks an SM) and that 256 blocks find 304 places.
 #include <cudaTypedefs.h>
 
+#include <limits>
 #include <mutex>
 
 #include "kda_glr_common.cuh"
@@ -146,7 +147,9 @@ __global__ void __launch_bounds__(kGlrThreads, 2) kda_glr_prefill_kernel(const _
     }
 }
 
-// A row by 256 threads a stretch of it: one token of every sequence, states read and written in place.
+// A row by 256 threads a stretch of it: one token of every sequence, states read and written in place.  Near a decay of 1 the step is as in a
+// stretch; elsewhere, and for a state that is infinite, it is a h.
+constexpr float kInfinity = std::numeric_limits<float>::infinity();
 template <typename X, typename G, int V, bool SIGMOID, bool COMPLEMENT>
 __global__ void __launch_bounds__(kGlrThreads) kda_glr_decode_kernel(const GlrDecodeArgs a, int32_t stretches) {
     const int64_t n = blockIdx.x / stretches, dim = a.dim;
@@ -163,8 +166,10 @@ __global__ void __launch_bounds__(kGlrThreads) kda_glr_decode_kernel(const GlrDe
     GlrVec<X, V> out;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const Lanes<1> d = glr_gate<SIGMOID, false>(glr_gates<SIGMOID, false>(GlrVec<G, 1>{g.e[j]})).n, xi = {glr_f32(x.e[j])};
-        s.e[j] = glr_step(Lanes<1>{s.e[j]}, d, COMPLEMENT ? mul(d, Lanes<1>{-xi.p}) : xi).p;
+        const GlrGate<1> d = glr_gate<SIGMOID, true>(glr_gates<SIGMOID, true>(GlrVec<G, 1>{g.e[j]}));
+        const float xi = glr_f32(x.e[j]), v = COMPLEMENT ? d.n.p * -xi : xi, h = s.e[j];
+        const float a = SIGMOID ? -d.n.p * d.e.p : fabsf(d.n.p) < kInfinity ? d.e.p : d.n.p;
+        s.e[j] = fabsf(d.n.p) < 0.5f && fabsf(h) < kInfinity ? glr_step(Lanes<1>{h}, d.n, Lanes<1>{v}).p : fmaf(a, h, v);
         glr_round(out.e[j], s.e[j]);
     }
     *reinterpret_cast<GlrVec<float, V>*>(a.state + slot * dim + ch) = s;

@@ -5,8 +5,8 @@
 //
 // The step is taken with n_t = a_t - 1, h_t = h_{t-1} + n_t h_{t-1} + s_t x_t (an fma and an addition).  A decay near 1 is what
 // gives a channel its memory of 1 / -n tokens: a rounded to fp32 is off by 2^-25, which the memory multiplies to 2^-25 / -n of the
-// state, while n itself is held to 2^-20 of its value.  Below a decay of 1/2 this form is off by 2^-25 of the state before,
-// no more than that state's own rounding.
+// state, while n itself is held to 2^-20 of its value.  Below a decay of 1/2 this form is off by 2^-25 of the state before, more than a
+// rounding of the little that is left of it: the single token takes a_t h_{t-1} there, a stretch is no better than its N (next).
 // Tokens i..j together are a pair (N, H): h_j = h_{i-1} + N h_{i-1} + H, where N = a_i .. a_j - 1 grows by N += n (1 + N).  Where little
 // of h_{i-1} is left, N's roundings near -1 are what stands for it, 2^-25 of h_{i-1}: relative to the states of the stretch, 128 tokens at most.
 // The product of the decays beside N would be good to 2^-24 of what is left, for a third operation a join and registers that are not there.
@@ -155,6 +155,7 @@ template <int V>
 struct GlrGate {
     Lanes<V> n;      // a - 1
     Lanes<V> slope;  // da / dg (asked for by SLOPE)
+    Lanes<V> e;      // e^g (with the sigmoid or SLOPE)
 };
 // The gates of a row.  Where e^g is corrected (below) they are held to where it is finite and what that loses is below fp32's normal range:
 // -150 and, of the sigmoid, 88.  bf16 pairs in one instruction a bound.
@@ -184,10 +185,9 @@ __device__ __forceinline__ GlrGate<V> glr_gate(const Lanes<V>& g) {
     GlrGate<V> r;
     const Lanes<V> t = mul(g, lanes<V>(-kLog2e));
     const Lanes<V> e = each(t, [](float x) { return ex2(-x); });
-    Lanes<V> exact;  // e^g = 2^-t e^(g + t ln(2))
-    if constexpr (SIGMOID || SLOPE) exact = fma(e, fma(t, lanes<V>(kRest), fma(t, lanes<V>(kLn2), g)), e);
+    if constexpr (SIGMOID || SLOPE) r.e = fma(e, fma(t, lanes<V>(kRest), fma(t, lanes<V>(kLn2), g)), e);  // 2^-t e^(g + t ln(2))
     if constexpr (SIGMOID) {
-        r.n = each(fma(exact, lanes<V>(-1.f), lanes<V>(-1.f)), [](float x) { return rcp(x); });
+        r.n = each(fma(r.e, lanes<V>(-1.f), lanes<V>(-1.f)), [](float x) { return rcp(x); });
     } else {
         // expm1(g): below 1/4 the first six terms of its series (the seventh is 5e-8 of the sum)
         Lanes<V> p = fma(g, lanes<V>(1.f / 720), lanes<V>(1.f / 120));
@@ -197,7 +197,7 @@ __device__ __forceinline__ GlrGate<V> glr_gate(const Lanes<V>& g) {
         p = fma(g, p, lanes<V>(1.f));
         r.n = each(g, mul(g, p), add(e, lanes<V>(-1.f)), [](float x, float near, float far) { return fabsf(x) < 0.25f ? near : far; });
     }
-    if constexpr (SLOPE) r.slope = SIGMOID ? mul(mul(r.n, exact), r.n) : exact;  // a (1 - a), with a = e^g (1 - a)
+    if constexpr (SLOPE) r.slope = SIGMOID ? mul(mul(r.n, r.e), r.n) : r.e;  // a (1 - a), with a = e^g (1 - a)
     return r;
 }
 

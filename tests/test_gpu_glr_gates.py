@@ -1,4 +1,5 @@
-"""Gates of the gated linear recurrence far from 0, element by element relative to their own values.
+"""Gates of the gated linear recurrence far from 0, element by element relative to their own values, and what a
+single token keeps of a state.
 
 u = 2^-24.  e^g is good to 5 u (ex2.approx 4 u, the remainder's product 1 u), so c = 1 / (1 + e^g) to 5 + 1 + 2 = 8 u (the sum's
 rounding, rcp.approx's 2^-23) and a (1 - a) = e^g c^2 to 5 + 2 * 8 + 2 = 23 u, whatever g.  Gates end where c or its slope leaves fp32's
@@ -58,3 +59,47 @@ def test_far_sigmoid_gates_past_fp32():
     assert all(bool((g.abs() <= 2.0 ** -122).all()) for g in grads[:2])
     low, _, _ = kda.kda_glr_prefill(x, -gate, cu_of([1]), **SIGMOID)
     assert torch.equal(low, x) and torch.equal(kda.kda_glr_decode_step(x, -gate, torch.ones_like(x), **SIGMOID), x)
+
+
+@pytest.mark.parametrize("kind", ["log_decay", "sigmoid"])
+@pytest.mark.parametrize("dim", [4096, 4001])
+def test_decode_keeps_what_is_left_of_a_state(dim, kind):
+    """The state's share of the next one is a h: a to 14 u below 1/2 (sigmoid e c: 5 + 8 + 1; exp 5), the product's rounding; from 1/2 on
+    h - c h with c off by 8 u of 1 or less, 16 u of a.  With an input, its own 9 u and the sum's roundings besides."""
+    gate, h0 = spread(-80.0, 0.0, dim)
+    a = gate.double().exp() if kind == "log_decay" else torch.sigmoid(gate.double())
+    for complement in (False, True):
+        opts = dict(gate_kind=kind, complement=complement)
+        state = h0.clone()
+        h = kda.kda_glr_decode_step(torch.zeros_like(h0), gate, state, **opts)
+        near(h, a * h0.double(), 18)
+        assert torch.equal(h, state)
+        x, state = randn(1, dim, seed=5), h0.clone()
+        v = x.double() * (1 - a if complement else 1)
+        kda.kda_glr_decode_step(x, gate, state, **opts)
+        size = (a * h0.double()).abs() + v.abs()
+        close(state, a * h0.double() + v, 18 * U * size + (8 * U * x.double().abs() if complement else 0))
+
+
+def test_decode_of_states_that_are_not_finite():
+    """a times an infinite state is infinite, 0 times it NaN, as the formula has it."""
+    inf, nan = float("inf"), float("nan")
+    state = torch.tensor([inf, -inf, inf, nan, -inf, inf], device="cuda").repeat(1, 6)
+    gate = torch.tensor([-0.1, -5.0, -inf, -0.1, -0.01, 0.0], device="cuda").repeat(1, 6)
+    want = torch.tensor([inf, -inf, nan, nan, -inf, inf], device="cuda").repeat(1, 6)
+    for kind, g in (("log_decay", gate), ("sigmoid", torch.where(gate == -inf, gate, gate + 1))):
+        s = state.clone()
+        h = kda.kda_glr_decode_step(torch.ones_like(g), g, s, gate_kind=kind)
+        for got in (h, s):
+            assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.nan_to_num(5.0, 1e30, -1e30), want.nan_to_num(5.0, 1e30, -1e30))
+
+
+@pytest.mark.parametrize("gate", [0.2, 0.3, 0.45, 1.0, 5.0, 40.0, 80.0])
+def test_decode_of_states_that_grow(gate):
+    """Decays above 1: a to 5 u beyond 1.5; below it h + n h with n off by less than 16 u (5 u of a and the difference's rounding, or less)."""
+    h0 = randn(1, 256, seed=1)
+    g = torch.full_like(h0, gate)
+    h = kda.kda_glr_decode_step(torch.zeros_like(h0), g, h0.clone())
+    near(h, g.double().exp() * h0.double(), 18)
+    beyond = kda.kda_glr_decode_step(torch.zeros_like(h0), torch.full_like(h0, 100.0), h0.clone())
+    assert bool((beyond == h0 * float("inf")).all())
