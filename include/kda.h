@@ -29,8 +29,9 @@
  *     synchronises the host, and enqueues all work on `stream` (a
  *     cudaStream_t; NULL = the legacy default stream).  It owns no streams,
  *     events or locks and keeps no state between calls except, per device,
- *     the kernels' attribute settings, the entry points it looks up in the
- *     driver, and (kda_prefill_noalloc only) its fixed scratch array.
+ *     the kernels' attribute settings, how many clusters of a kernel fit, the
+ *     entry points it looks up in the driver, and (kda_prefill_noalloc only)
+ *     its fixed scratch array.
  *   - Argument errors are returned synchronously before anything is
  *     enqueued.  Data-dependent errors found on the device are OR-ed into
  *     *device_status (if non-NULL) as KDA_DEV_* bits; the affected sequences

@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kGlrThreads) kda_glr_decode_kernel(const GlrDe
 template <typename X, typename G, bool TMA, bool SIGMOID, bool COMPLEMENT>
 cudaError_t prefill_as(const GlrArgs& a, const GlrMaps& maps, cudaStream_t stream) {
     using F = Form<X, G, TMA>;
-    static GlrRoom rooms[64];
+    static GlrRooms rooms;
     const int64_t slices = (a.dim + 32 * F::V - 1) / (32 * F::V);
     return glr_launch(kda_glr_prefill_kernel<X, G, TMA, SIGMOID, COMPLEMENT>, slices, a.total_tokens, F::kBlockTokens,
                       F::kSmem, F::V, rooms, stream, maps, a);

@@ -15,16 +15,15 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <atomic>
 
 #include "kda_gdn_ptx.cuh"
 #include "kda_glr_internal.h"
+#include "kda_glr_room.h"
 
 namespace kda {
 
-constexpr int kGlrWarps = 8;         // of a block: consecutive stretches of time
+constexpr int kGlrWarps = 8;  // of a block: consecutive stretches of time; a cluster's blocks have consecutive chunks of it
 constexpr int kGlrThreads = 32 * kGlrWarps;
-constexpr int kGlrMaxCluster = 16;   // blocks of a cluster: consecutive chunks of time
 
 // ------------------------------------------------------- a thread's channels --
 // V channels beside each other, and their arithmetic in fp32: two at once in one instruction (fma, mul and add of f32x2 take
@@ -477,16 +476,11 @@ __device__ __forceinline__ T glr_load(const T* p, bool in) {
 bool glr_map(CUtensorMap* m, const void* base, bool f32, int64_t tokens, int32_t dim, int32_t rows);
 // Whether the rows of all its tensors are whole multiples of 16 bytes apart.
 inline bool glr_tiled(const GlrKind& kind, int32_t dim) { return dim % (kind.x_f32 && kind.gate_f32 ? 4 : 8) == 0; }
-// How many clusters of 1, 2 .. blocks of a kernel find room beside each other, by device; looked up once.
-struct GlrRoom {
-    std::atomic<bool> known{false};
-    int clusters[kGlrMaxCluster + 1] = {};
-};
 // A kernel over `slices` slices of channels with a cluster of blocks on each: as many blocks as have tokens of their own, while all the
 // clusters find room beside each other (a training step of 8192 tokens, 2560 channels: 7 blocks 114 us, 4 blocks 150; 64 channels: 16
 // blocks 42, 8 blocks 61).  `smem`: bytes of tiles; V: channels of a thread.
 template <typename K, typename... A>
-inline cudaError_t glr_launch(K kernel, int64_t slices, int64_t tokens, int block_tokens, uint32_t smem, int V, GlrRoom* rooms,
+inline cudaError_t glr_launch(K kernel, int64_t slices, int64_t tokens, int block_tokens, uint32_t smem, int V, GlrRooms& rooms,
                               cudaStream_t stream, const A&... args) {
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
@@ -504,18 +498,18 @@ inline cudaError_t glr_launch(K kernel, int64_t slices, int64_t tokens, int bloc
         cfg.attrs = attr;
         cfg.numAttrs = 1;
     };
-    GlrRoom& room = rooms[dev % 64];
-    if (dev >= 64 || !room.known.load(std::memory_order_acquire)) {
+    GlrRoom room;
+    err = rooms.get(dev, [&](GlrRoom* r) {
         shape(kGlrMaxCluster);
-        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(cfg.dynamicSmemBytes));
-        if (err == cudaSuccess) err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        for (int n = 1; err == cudaSuccess && n <= kGlrMaxCluster; ++n) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(cfg.dynamicSmemBytes));
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        for (int n = 1; e == cudaSuccess && n <= kGlrMaxCluster; ++n) {
             shape(n);
-            err = cudaOccupancyMaxActiveClusters(&room.clusters[n], kernel, &cfg);
+            e = cudaOccupancyMaxActiveClusters(&r->clusters[n], kernel, &cfg);
         }
-        if (err != cudaSuccess) return err;
-        room.known.store(true, std::memory_order_release);
-    }
+        return e;
+    }, &room);
+    if (err != cudaSuccess) return err;
     int blocks = static_cast<int>(std::min<int64_t>(kGlrMaxCluster, std::max<int64_t>(1, (tokens + block_tokens - 1) / block_tokens)));
     while (blocks > 1 && slices > room.clusters[blocks]) --blocks;
     shape(blocks);
