@@ -650,6 +650,11 @@ KDA_API kda_status kda_rms_norm_backward(const void *grad_y, const void *h, cons
  * where a channel forgets a large state faster than that; decays of exactly 0
  * forget it exactly.  The single token (kda_glr_decode_step) keeps a_t h_{t-1} to
  * 2^-19 of its own value.  Results are bitwise repeatable.
+ * Gates above 0 of the exp kind are growth.  Prefill and its gradient take them
+ * while the product of any 128 consecutive tokens' decays is finite (gates that
+ * add up to less than 88); beyond that they may give NaN where the recurrence is
+ * finite, a state of 0 among them.  1 - a_t is then good to (22 + 1.25 gate_t)
+ * 2^-24 of its value.
  * Inputs that are not finite reach the outputs of their token and of later ones
  * (in the gradient: earlier ones) of their sequence and channel; an infinite
  * state becomes NaN at the next token of prefill, while the single token has

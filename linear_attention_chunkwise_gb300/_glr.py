@@ -43,10 +43,10 @@ def kda_glr_prefill(x, gate, cu_seqlens, h0=None, *, gate_kind="log_decay", comp
     """h_t = a_t h_{t-1} + s_t x_t over packed sequences, channel by channel (see include/kda.h).
 
     x: [T, dim] (bf16 or fp32); gate: [T, dim] in that type or fp32, a = exp(gate) ("log_decay") or
-    sigmoid(gate) ("sigmoid"); s = 1, or 1 - a with complement; cu_seqlens: int32 [N+1] on the device; h0:
-    fp32 [N, dim] or None.  Returns (h, h_final, checkpoints): h [T, dim] in the type of x, h_final fp32
-    [N, dim], or None when return_final is False and none was given; checkpoints fp32 [ceil(T / 64), dim] for
-    kda_glr_prefill_backward, or None unless asked for or given.
+    sigmoid(gate) ("sigmoid"); kda.h bounds log decays above 0; s = 1, or 1 - a with complement; cu_seqlens: int32
+    [N+1] on the device; h0: fp32 [N, dim] or None.  Returns (h, h_final, checkpoints): h [T, dim] in the type of x,
+    h_final fp32 [N, dim], or None when return_final is False and none was given; checkpoints fp32 [ceil(T / 64), dim]
+    for kda_glr_prefill_backward, or None unless asked for or given.
     """
     lib = _b.load_library()
     dev, code = _first(x, "x", 2)

@@ -1,5 +1,5 @@
-"""Gates of the gated linear recurrence far from 0, element by element relative to their own values, and what a
-single token keeps of a state.
+"""Gates of the gated linear recurrence far from 0, element by element relative to their own values, what a single token
+keeps of a state, and states that grow.
 
 u = 2^-24.  e^g is good to 5 u (ex2.approx 4 u, the remainder's product 1 u), so c = 1 / (1 + e^g) to 5 + 1 + 2 = 8 u (the sum's
 rounding, rcp.approx's 2^-23) and a (1 - a) = e^g c^2 to 5 + 2 * 8 + 2 = 23 u, whatever g.  Gates end where c or its slope leaves fp32's
@@ -103,3 +103,47 @@ def test_decode_of_states_that_grow(gate):
     near(h, g.double().exp() * h0.double(), 18)
     beyond = kda.kda_glr_decode_step(torch.zeros_like(h0), torch.full_like(h0, 100.0), h0.clone())
     assert bool((beyond == h0 * float("inf")).all())
+
+
+@pytest.mark.parametrize("dim", [64, 33])
+def test_growth_while_128_tokens_products_are_finite(dim):
+    """Log gates above 0: a token's 1 - a is good to (22 + 1.25 g) u of its value (the difference of e^g, 5 + 1.25 g u, and 1, which
+    is less of it below g = 1), its step and joins round by 6 u more.  Sums of one sign, so a token adds 30 u of the state at most.  The
+    products over 128 tokens are e^64; a state of zero stays zero."""
+    T = 150
+    x, gate, h0 = randn(2 * T, dim, seed=1).abs(), torch.full((2 * T, dim), 0.5, device="cuda"), randn(2, dim, seed=3).abs()
+    x[:T - 1], h0[0] = 0, 0  # nothing but zeros, and an input at the last token
+    dh, cu = randn(2 * T, dim, seed=4).abs(), cu_of([T, T])
+    dh[T + 1:] = 0
+    h, final, ck = kda.kda_glr_prefill(x, gate, cu, h0, return_checkpoints=True)
+    ref, s = torch.empty_like(x, dtype=torch.float64), None
+    for t in range(2 * T):
+        s = ref[t] = gate[t].double().exp() * (h0[t // T].double() if t % T == 0 else s) + x[t].double()
+    assert bool((h[:T - 1] == 0).all())
+    near(h, ref, 30 * T)
+    near(final, ref[T - 1::T], 30 * T)
+    dx, dg, dh0 = kda.kda_glr_prefill_backward(x, gate, cu, dh, h0, checkpoints=ck)
+    lam, m = torch.empty_like(ref), None
+    for t in reversed(range(2 * T)):
+        lam[t] = dh[t].double() + (0 if t % T == T - 1 else m)
+        m = gate[t].double().exp() * lam[t]
+    assert bool((dx[T + 1:] == 0).all())
+    near(dx, lam, 30 * T)
+    near(dh0, torch.stack([gate[0].double().exp() * lam[0], gate[T].double().exp() * lam[T]]), 30 * T)
+    before = torch.cat([ref[:1] * 0, ref[:-1]])
+    before[0], before[T] = h0[0].double(), h0[1].double()
+    near(dg, gate.double().exp() * lam * before, 60 * T + 32)
+
+
+def test_a_gate_of_zero_in_a_captured_decode():
+    """A decay of 1 leaves the state, replay after replay."""
+    state, gate, x = randn(3, 128, seed=1), torch.zeros(3, 128, device="cuda"), torch.zeros(3, 128, device="cuda")
+    keep = state.clone()
+    kda.kda_glr_decode_step(x, gate, state)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        h = kda.kda_glr_decode_step(x, gate, state)
+    for _ in range(3):
+        graph.replay()
+    assert torch.equal(h, keep) and torch.equal(state, keep)
