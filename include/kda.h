@@ -739,7 +739,10 @@ KDA_API kda_status kda_glr_decode_step(const void *x, kda_dtype dtype, const voi
  *
  * A layer's three products are y = x W^T, dx = dy W and dW = dy^T x, all of them
  * rows times rows: dx takes the transposed codes and scales of W (blocks stay
- * blocks), dW takes dy and x as KDA_FP8_COLUMNS makes them.
+ * blocks), dW takes dy and x as KDA_FP8_COLUMNS makes them.  K, of which the
+ * products take multiples of 16, is W's number of rows in dx and that of tokens
+ * in dW: others are filled up with zeros before they are quantised (rows of W
+ * and columns of dy; rows of dy and x), which changes no scale and no code.
  */
 #define KDA_FP8_BLOCK 128
 #define KDA_FP8_MAX_DIM (1 << 24)
@@ -761,7 +764,9 @@ typedef enum {
  * M >= 0, N from 1 to KDA_FP8_MAX_DIM, K a multiple of 16 up to it (others:
  * KDA_ERR_UNSUPPORTED); x, w and out 16-byte aligned, the others 4.  A block's
  * products are summed by the tensor cores in fp32, blocks are added in fp32 after
- * their scales, and out is rounded once.  Results are bitwise repeatable.  A
+ * their scales, and out is rounded once.  The two scales of a block are multiplied
+ * with each other first: xs ws has to lie in fp32's range, below its normal
+ * numbers it loses bits.  Results are bitwise repeatable.  A
  * scale or code that is not finite spoils the outputs of its row (column of out
  * for w) only.  out overlaps nothing (KDA_ERR_INVALID_ARG).  Asynchronous, no
  * workspace.

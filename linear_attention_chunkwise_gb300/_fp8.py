@@ -89,7 +89,8 @@ def kda_fp8_quantize(x, *, form="rows", codes=None, scales=None, stream=None):
 
     x: [rows, cols] (bf16 or fp32).  form "rows": a scale for 128 of a row, codes [rows, cols], scales [rows,
     ceil(cols / 128)]; "blocks": for 128 x 128, scales [ceil(rows / 128), ceil(cols / 128)]; "columns": the rows form of
-    the transposed x, codes [cols, rows], scales [cols, ceil(rows / 128)].
+    the transposed x, codes [cols, rows], scales [cols, ceil(rows / 128)].  A product over those codes takes a multiple
+    of 16 rows of x: fill others up with rows of zeros, which change no scale and no code.
     """
     lib = _b.load_library()
     if not isinstance(x, torch.Tensor):
