@@ -1,8 +1,11 @@
 // kda_args.h -- argument checks shared by the C-ABI front ends, and what kda_api.cu does for the others.
 #pragma once
 
+#include <cudaTypedefs.h>
+
 #include <cstddef>
 #include <cstdint>
+#include <mutex>
 
 #include "kda_internal.h"
 
@@ -10,6 +13,20 @@ namespace kda {
 
 // SMs of the current device (0 when the runtime cannot say).
 int device_sm_count();
+
+// The driver's encoder of tensor maps, looked up once; NULL where it has none.
+inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult qr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &qr) == cudaSuccess &&
+            qr == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
 
 // Tensor map over a bf16 [T][H][128] tensor with boxes of box_rows tokens of one head and box_inner
 // channels; false when the driver refuses it.

@@ -10,10 +10,8 @@
 // registers is an fma in fp32.  8192 x 8192 x 4096: 230 us, 2.4 PFLOP/s, the tensor pipe 55 % busy: bound by the accumulators' way from
 // products to registers and back.  16 x 8192 x 4096: 12 us, of which the weights' bytes are 5.
 #include <cuda_bf16.h>
-#include <cudaTypedefs.h>
 
 #include <algorithm>
-#include <mutex>
 
 #include "kda_fp8_internal.h"
 #include "kda_gdn_ptx.cuh"
@@ -120,7 +118,7 @@ struct Shape {
     static constexpr int kBlocks = TN >= 128 ? 1 : 2;             // on an SM
     static constexpr int kStaged = 64;                            // bytes of a row that a warp turns over at once on its way out
 };
-template <int TN, bool PAIR, bool SWAP>
+template <int TN, bool PAIR>
 struct Shared {
     using S = Shape<TN, PAIR>;
     uint64_t full[S::kStages], empty[S::kStages];
@@ -131,11 +129,11 @@ struct Shared {
     int32_t stop;
     alignas(16) float p_scale[S::kScaleStages][kTileP][kQuad];
     alignas(16) float q_scale[S::kScaleStages][kQuad][TN];
-    alignas(16) uint8_t staged[SWAP ? 1 : S::kWarps][SWAP ? 16 : 32 * S::kStaged];
+    alignas(16) uint8_t staged[PAIR ? S::kWarps : 1][PAIR ? 32 * S::kStaged : 16];
 };
-template <int TN, bool PAIR, bool SWAP>
+template <int TN, bool PAIR>
 constexpr uint32_t smem_bytes() {
-    return Shape<TN, PAIR>::kStages * Shape<TN, PAIR>::kStage + 1024 + static_cast<uint32_t>(sizeof(Shared<TN, PAIR, SWAP>));
+    return Shape<TN, PAIR>::kStages * Shape<TN, PAIR>::kStage + 1024 + static_cast<uint32_t>(sizeof(Shared<TN, PAIR>));
 }
 
 // One lane of a converged warp.
@@ -165,8 +163,9 @@ struct Tile {
     int32_t row_end;         // behind the expert's rows of x
     int32_t blocks;          // of K
 };
-template <int TN, bool PAIR, bool SWAP>
+template <int TN, bool PAIR>
 struct Walk {
+    static constexpr bool SWAP = !PAIR;
     int32_t e0 = 0;       // the experts looked at start here
     int64_t before = 0;   // tiles of those before
     __device__ __forceinline__ bool find(const Fp8MatmulArgs& a, int32_t tile, Tile* t) {
@@ -223,16 +222,17 @@ __device__ __forceinline__ void store1(const Fp8MatmulArgs& a, int64_t at, float
 
 // PER_Q: a scale for every q, else one for 128 of them.  gridDim = clusters of `split` blocks, which take a share of K each; PAIR:
 // of two, which share a tile of 256 rows of P.
-template <int TN, bool PAIR, bool SWAP, bool PER_Q>
+template <int TN, bool PAIR, bool PER_Q>
 __global__ void __launch_bounds__(Shape<TN, PAIR>::kThreads, Shape<TN, PAIR>::kBlocks)
     kda_fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
                           const Fp8MatmulArgs a, const int32_t split) {
     using S = Shape<TN, PAIR>;
-    static_assert(!(PAIR && SWAP), "pairs are for many rows");
-    static_assert(S::kBlocks * (smem_bytes<TN, PAIR, SWAP>() + 1024) <= 228 * 1024, "kBlocks of them fit an SM");
+    constexpr bool SWAP = !PAIR;  // pairs are for many rows
+    static_assert(PAIR || PER_Q, "x's rows, which the few are of, have a scale each");
+    static_assert(S::kBlocks * (smem_bytes<TN, PAIR>() + 1024) <= 228 * 1024, "kBlocks of them fit an SM");
     extern __shared__ uint8_t raw[];
     uint8_t* ring = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-    using Sh = Shared<TN, PAIR, SWAP>;
+    using Sh = Shared<TN, PAIR>;
     Sh& s = *reinterpret_cast<Sh*>(ring + S::kStages * S::kStage);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int32_t half = PAIR ? blockIdx.x & 1 : 0;  // of the pair
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(Shape<TN, PAIR>::kThreads, Shape<TN, PAIR>::kB
     if (PAIR) cluster_sync();  // the other's barriers are set
     tc_fence_after();
     const uint32_t tmem = s.tmem;
-    Walk<TN, PAIR, SWAP> walk;
+    Walk<TN, PAIR> walk;
     Tile t;
     bool met = false;  // at the cluster's first barrier, behind which its blocks exchange their sums
 
@@ -313,8 +313,8 @@ __global__ void __launch_bounds__(Shape<TN, PAIR>::kThreads, Shape<TN, PAIR>::kB
                         pair_tma_load_3d(at_q, &map_q, bar, k, t.q0 + half * S::kQ, t.expert);
                     } else {
                         mbar_arrive_expect_tx(&s.full[st], S::kStage);
-                        tma_load_3d(at, &map_p, &s.full[st], k, t.p0, SWAP ? t.expert : 0);
-                        tma_load_3d(at_q, &map_q, &s.full[st], k, t.q0, SWAP ? 0 : t.expert);
+                        tma_load_3d(at, &map_p, &s.full[st], k, t.p0, t.expert);
+                        tma_load_3d(at_q, &map_q, &s.full[st], k, t.q0, 0);
                     }
                 }
                 __syncwarp();
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(Shape<TN, PAIR>::kThreads, Shape<TN, PAIR>::kB
     if (!PAIR && split > 1) {
         if (!met) cluster_sync();
         cluster_sync();
-        Walk<TN, PAIR, SWAP> again;
+        Walk<TN, PAIR> again;
         if (warp < S::kWarps && !*stop && again.find(a, first, &t)) {
             const int per = TN / split, prow = threadIdx.x % kTileP;
             const int32_t p = t.p0 + prow;
@@ -595,8 +595,7 @@ __global__ void __launch_bounds__(Shape<TN, PAIR>::kThreads, Shape<TN, PAIR>::kB
                 float sum = 0.f;
                 for (int r = 0; r < split; ++r) sum += from[(r * per + j) * kTileP + prow];  // in the order of K
                 const int32_t q = t.q0 + rank * per + j;
-                if (SWAP ? p < a.N && q < t.row_end : p < t.row_end && q < a.N)
-                    store1(a, SWAP ? static_cast<int64_t>(q) * a.N + p : static_cast<int64_t>(p) * a.N + q, sum);
+                if (p < a.N && q < t.row_end) store1(a, static_cast<int64_t>(q) * a.N + p, sum);
             }
         }
     }
@@ -610,21 +609,9 @@ __global__ void __launch_bounds__(Shape<TN, PAIR>::kThreads, Shape<TN, PAIR>::kB
     }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult qr;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &qr) == cudaSuccess &&
-            qr == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
 // Rows of 128 codes of [outer, rows, K], `box` of them, 128-byte swizzled; what lies behind K or the rows reads as zeros.
 bool code_map(CUtensorMap* m, const void* base, int32_t K, int32_t rows, int32_t outer, int32_t box) {
-    auto fn = encode_fn();
+    const auto fn = tensor_map_encoder();
     if (!fn) return false;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(outer)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(K) * rows};
@@ -635,16 +622,16 @@ bool code_map(CUtensorMap* m, const void* base, int32_t K, int32_t rows, int32_t
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int TN, bool PAIR, bool SWAP, bool PER_Q>
+template <int TN, bool PAIR, bool PER_Q>
 cudaError_t launch(const Fp8MatmulArgs& a, int split, int64_t tiles, cudaStream_t stream) {
     using S = Shape<TN, PAIR>;
     static int configured[64] = {};
     CUtensorMap map_p, map_q;
-    if (!(SWAP ? code_map(&map_p, a.w, a.K, a.N, a.experts, kTileP) && code_map(&map_q, a.x, a.K, a.rows, 1, TN)
-               : code_map(&map_p, a.x, a.K, a.rows, 1, kTileP) && code_map(&map_q, a.w, a.K, a.N, a.experts, S::kQ)))
+    if (!(PAIR ? code_map(&map_p, a.x, a.K, a.rows, 1, kTileP) && code_map(&map_q, a.w, a.K, a.N, a.experts, S::kQ)
+               : code_map(&map_p, a.w, a.K, a.N, a.experts, kTileP) && code_map(&map_q, a.x, a.K, a.rows, 1, TN)))
         return cudaErrorUnknown;
-    const auto kernel = kda_fp8_matmul_kernel<TN, PAIR, SWAP, PER_Q>;
-    constexpr uint32_t smem = smem_bytes<TN, PAIR, SWAP>();
+    const auto kernel = kda_fp8_matmul_kernel<TN, PAIR, PER_Q>;
+    constexpr uint32_t smem = smem_bytes<TN, PAIR>();
     const cudaError_t err = set_smem(kernel, smem, configured);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
@@ -679,12 +666,12 @@ cudaError_t few_rows(const Fp8MatmulArgs& a, cudaStream_t stream) {
     int split = 1;
     if (!a.offsets)
         while (split < kMaxSplit && tiles * split * 2 <= places<TN>() && split * 2 <= quads) split *= 2;
-    return launch<TN, false, true, true>(a, split, tiles, stream);
+    return launch<TN, false, true>(a, split, tiles, stream);
 }
 cudaError_t many_rows(const Fp8MatmulArgs& a, cudaStream_t stream) {
     constexpr int kPair = 2 * kTileP;
     const int64_t tiles = (a.offsets ? a.rows / kPair + a.experts : ceil_div(a.rows, kPair)) * ceil_div(a.N, 256);
-    return a.w_div == 1 ? launch<256, true, false, true>(a, 1, tiles, stream) : launch<256, true, false, false>(a, 1, tiles, stream);
+    return a.w_div == 1 ? launch<256, true, true>(a, 1, tiles, stream) : launch<256, true, false>(a, 1, tiles, stream);
 }
 
 }  // namespace

@@ -8,10 +8,8 @@
 // the cluster's) adds what comes in.  One pass, no second reading and no waiting on other clusters; sums are taken in a fixed
 // order, so results are bitwise repeatable.  12345 tokens x 4096 channels, bf16 with fp32 gates: 84 us, 4.8 TB/s of 6.8; what is left is a
 // round's chain (tile, gates, scan, exchange, outputs: 3.4 us with two blocks an SM) and that 256 blocks find 304 places.
-#include <cudaTypedefs.h>
 
 #include <limits>
-#include <mutex>
 
 #include "kda_glr_common.cuh"
 
@@ -206,23 +204,10 @@ cudaError_t decode(const GlrDecodeArgs& a, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult qr;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &qr) == cudaSuccess &&
-            qr == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
 }  // namespace
 
 bool glr_map(CUtensorMap* m, const void* base, bool f32, int64_t tokens, int32_t dim, int32_t rows) {
-    auto fn = encode_fn();
+    const auto fn = tensor_map_encoder();
     if (!fn) return false;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(tokens)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(dim) * (f32 ? 4 : 2)};
