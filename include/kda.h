@@ -644,7 +644,8 @@ KDA_API kda_status kda_rms_norm_backward(const void *grad_y, const void *h, cons
  *
  * States, decays and sums are fp32; every output is rounded once.  The step is
  * taken with 1 - a_t, held to 2^-20 of its value, so a channel with a memory of
- * many tokens keeps its accuracy.  Prefill and its gradient take up to 128 tokens
+ * many tokens keeps its accuracy; decays, 1 - a_t and slopes below fp32's normal
+ * numbers count as 0.  Prefill and its gradient take up to 128 tokens
  * together: a state is off by a few 2^-24 of the largest one among the 128 tokens
  * before it (in the gradient: behind it), which is more than its own rounding
  * where a channel forgets a large state faster than that; decays of exactly 0
